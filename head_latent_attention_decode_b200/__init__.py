@@ -28,7 +28,7 @@ MLA_FLAG_BAD_BLOCK = 2
 MLA_FLAG_BAD_CONTEXT = 4
 MLA_FLAG_WAIT_TIMEOUT = 8
 
-MLA_F32, MLA_BF16, MLA_FP8_E4M3_B128 = 0, 1, 2
+MLA_F32, MLA_BF16, MLA_FP8_E4M3_B128, MLA_FP8_E4M3_ROW = 0, 1, 2, 3
 MLA_ROW_LATENT_FIRST, MLA_ROW_PE_FIRST = 0, 1
 
 SYMBOLS = (
@@ -37,7 +37,9 @@ SYMBOLS = (
     "mla_decode_qkv", "mla_decode_attn", "mla_prefill", "mla_strerror",
     "mla_kernel_launch_count", "mla_set_kernel_timer", "mla_decode_qkv_noalloc",
     "mla_decode_step_host_bytes", "mla_decode_step_host", "mla_rope_cos_sin_inv_freq",
-    "mla_v4_qkv", "mla_noalloc_read_device_flag",
+    "mla_v4_qkv", "mla_noalloc_read_device_flag", "mla_set_cache_dtype", "mla_cache_block_bytes",
+    "mla_cache_write", "mla_cache_read", "mla_prefix_workspace_bytes", "mla_latent_attn",
+    "mla_decode_attn_prefix",
 )
 
 MLA_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -116,6 +118,20 @@ def lib() -> ctypes.CDLL:
         L.mla_decode_step_host.restype = i
         L.mla_decode_step_host.argtypes = [vp, vp, vp, vp, vp, i, vp, i, i, ctypes.c_double, vp, i, vp, vp, sz,
                                            vp, sz, vp]
+        L.mla_set_cache_dtype.restype = i
+        L.mla_set_cache_dtype.argtypes = [vp, i]
+        L.mla_cache_block_bytes.restype = sz
+        L.mla_cache_block_bytes.argtypes = [vp]
+        L.mla_cache_write.restype = i
+        L.mla_cache_write.argtypes = [vp, vp, i, vp, i, vp, vp, sz, vp]
+        L.mla_cache_read.restype = i
+        L.mla_cache_read.argtypes = [vp, vp, i, vp, i, vp, vp, sz, vp]
+        L.mla_prefix_workspace_bytes.restype = sz
+        L.mla_prefix_workspace_bytes.argtypes = [vp, i, i, i]
+        L.mla_latent_attn.restype = i
+        L.mla_latent_attn.argtypes = [vp, vp, vp, vp, i, vp, i, vp, i, vp, i, i, vp, vp, vp, sz, vp]
+        L.mla_decode_attn_prefix.restype = i
+        L.mla_decode_attn_prefix.argtypes = [vp, vp, vp, vp, i, vp, i, vp, i, vp, i, i, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -284,6 +300,94 @@ def mla_v4_qkv(handle, hidden, cos, sin, kv_norm_w, q_out, kv_out, ws, stream=No
     S = hidden.shape[0]
     _check(lib().mla_v4_qkv(handle, _ptr(hidden), S, _ptr(cos), _ptr(sin), _ptr(kv_norm_w), _ptr(q_out),
                             _ptr(kv_out), _ptr(ws), _nbytes(ws), _stream(stream)), "mla_v4_qkv")
+
+
+def mla_set_cache_dtype(handle, cache_dtype: int) -> None:
+    """What the handle's kv_cache arguments hold: the activation dtype, or MLA_FP8_E4M3_ROW."""
+    _check(lib().mla_set_cache_dtype(handle, int(cache_dtype)), "mla_set_cache_dtype")
+
+
+def mla_cache_block_bytes(handle) -> int:
+    return int(lib().mla_cache_block_bytes(handle))
+
+
+def _check_tensors(where: str, need: dict, ints: dict) -> None:
+    """Contiguous tensors on one device; `ints` (name -> tensor) are int32."""
+    dev = None
+    for name, t in {**need, **ints}.items():
+        if t is None:
+            continue
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be a contiguous device tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, not on {dev}")
+        dev = t.device
+    for name, t in ints.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{where}: {name} must be int32")
+
+
+def mla_cache_write(handle, rows, kv_cache, slot_mapping, ws, stream=None) -> None:
+    """rows [n, R] into the cache's flat rows slot_mapping [n] (negative: skipped),
+    quantised if the handle's cache is 8-bit."""
+    _check_tensors("mla_cache_write", dict(rows=rows, kv_cache=kv_cache, ws=ws), dict(slot_mapping=slot_mapping))
+    if slot_mapping.numel() != rows.shape[0]:
+        raise ValueError("mla_cache_write: one slot per row")
+    _check(lib().mla_cache_write(handle, _ptr(rows), rows.shape[0], _ptr(kv_cache), kv_cache.shape[0],
+                                 _ptr(slot_mapping), _ptr(ws), _nbytes(ws), _stream(stream)), "mla_cache_write")
+
+
+def mla_cache_read(handle, kv_cache, slots, rows, ws, stream=None) -> None:
+    """rows [n, R] = the values of the cache's flat rows slots [n] (negative: left as it was)."""
+    _check_tensors("mla_cache_read", dict(kv_cache=kv_cache, rows=rows, ws=ws), dict(slots=slots))
+    if slots.numel() != rows.shape[0]:
+        raise ValueError("mla_cache_read: one slot per row")
+    _check(lib().mla_cache_read(handle, _ptr(kv_cache), kv_cache.shape[0], _ptr(slots), rows.shape[0], _ptr(rows),
+                                _ptr(ws), _nbytes(ws), _stream(stream)), "mla_cache_read")
+
+
+def mla_prefix_workspace_bytes(handle, max_tokens: int, max_prefix_len: int, max_context_len: int) -> int:
+    return int(lib().mla_prefix_workspace_bytes(handle, int(max_tokens), int(max_prefix_len), int(max_context_len)))
+
+
+def _check_latent(where, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens, more):
+    _check_tensors(where, dict(q_abs=q_abs, q_pe=q_pe, kv_cache=kv_cache, **more),
+                   dict(prefix_table=prefix_table, block_table=block_table, context_lens=context_lens))
+    n = q_abs.shape[0]
+    if q_abs.dim() != 3 or q_pe.shape[:2] != q_abs.shape[:2] or q_pe.dtype != q_abs.dtype:
+        raise ValueError(f"{where}: q_abs [n, H, r_kv] and q_pe [n, H, d_r] of one dtype")
+    if block_table.dim() != 2 or block_table.shape[0] != n or context_lens.numel() != n:
+        raise ValueError(f"{where}: block_table [n, blocks] and context_lens [n]")
+    if prefix_len and prefix_table is None:
+        raise ValueError(f"{where}: prefix_len without a prefix_table")
+
+
+def mla_latent_attn(handle, q_abs, q_pe, kv_cache, block_table, context_lens, max_context_len, o_lat, ws,
+                    lse=None, prefix_table=None, prefix_len: int = 0, stream=None) -> None:
+    """o_lat [n, H, r_kv] (and lse [n, H] fp32) of the shared prefix's keys followed by each
+    sequence's own (see include/mla.h). The prefix_table must cover prefix_len rows."""
+    _check_latent("mla_latent_attn", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
+                  dict(o_lat=o_lat, lse=lse, ws=ws))
+    if o_lat.shape != q_abs.shape or o_lat.dtype != q_abs.dtype:
+        raise ValueError("mla_latent_attn: o_lat must have q_abs's shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q_abs.shape[:2]):
+        raise ValueError("mla_latent_attn: lse must be fp32 [n, H]")
+    _check(lib().mla_latent_attn(handle, _ptr(q_abs), _ptr(q_pe), _ptr(kv_cache), kv_cache.shape[0],
+                                 _ptr(prefix_table) if prefix_len else None, int(prefix_len), _ptr(block_table),
+                                 block_table.shape[1], _ptr(context_lens), int(max_context_len), q_abs.shape[0],
+                                 _ptr(o_lat), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)), "mla_latent_attn")
+
+
+def mla_decode_attn_prefix(handle, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
+                           max_context_len, out, ws, head_out=None, stream=None) -> None:
+    """mla_decode_attn over a prefix shared by the batch followed by each sequence's own rows."""
+    _check_latent("mla_decode_attn_prefix", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table,
+                  context_lens, dict(out=out, head_out=head_out, ws=ws))
+    _check(lib().mla_decode_attn_prefix(handle, _ptr(q_abs), _ptr(q_pe), _ptr(kv_cache), kv_cache.shape[0],
+                                        _ptr(prefix_table) if prefix_len else None, int(prefix_len),
+                                        _ptr(block_table), block_table.shape[1], _ptr(context_lens),
+                                        int(max_context_len), q_abs.shape[0], _ptr(out), _ptr(head_out), _ptr(ws),
+                                        _nbytes(ws), _stream(stream)), "mla_decode_attn_prefix")
 
 
 def mla_kernel_launch_count() -> int:

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/mla.h"
+#include "cache8.cuh"
 #include "tc_state.cuh"
 
 static inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -49,6 +50,7 @@ struct mla_handle {
   char* base;
   int has_sink;   // attn_sink given at init: one fp32 logit per head at base + L.sink
   int device;
+  int cache8 = 0;  // the kv_cache arguments hold 8-bit rows (mla_set_cache_dtype)
   TcState tc;
   // mla_decode_step_host: page-locked packing buffer for the step's int32
   // inputs, and an event marking the end of the last transfer out of it
@@ -69,3 +71,17 @@ struct mla_handle {
   }
 };
 
+// The 8-bit cache's layout for this handle (on = 0: act-dtype rows).
+static inline mla::Cache8 cache8_of(const mla_handle* h) {
+  const mla_config& c = h->cfg;
+  mla::Cache8 k{};
+  k.on = h->cache8;
+  k.bs = c.block_size;
+  k.r_kv = c.kv_lora_rank;
+  k.d_r = c.qk_rope;
+  k.esz = c.act_dtype == MLA_F32 ? 4 : 2;
+  k.pe_off = (long long)c.block_size * c.kv_lora_rank;
+  k.sc_off = k.pe_off + (long long)c.block_size * c.qk_rope * k.esz;
+  k.block_bytes = (long long)align_up((size_t)(k.sc_off + 4LL * c.block_size), 128);
+  return k;
+}

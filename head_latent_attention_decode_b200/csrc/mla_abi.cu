@@ -11,6 +11,7 @@
 #include "simt_kernels.cuh"
 #include "handle.cuh"
 #include "tc_path.cuh"
+#include "latent_attn.cuh"
 
 using namespace mla;
 
@@ -125,6 +126,8 @@ struct WsLayout {
   size_t Y1, qn, Q, part_o, part_ml, nseg, o_lat, head, xn, oy;   // decode
   size_t pY1, pqn, pQ, pcn, pkpe, pKV, phead, pDQ, poy;            // prefill
   size_t tc;                                                   // tensor-core path scratch
+  size_t lat;                                                  // 8-bit cache: the attention's scratch (latent_attn.cuh)
+  size_t qkv_total;                                            // what the decode front-fold needs
   size_t dec_total;                                            // what the decode calls need
   size_t total;                                                // what every call needs
   int splits;
@@ -155,6 +158,8 @@ static WsLayout make_ws(const mla_handle* h, long long n, int max_ctx) {
   W.xn = put((size_t)n * c->hidden * a);
   W.oy = put((size_t)n * (L.G ? L.G * L.ro : 1) * a);   // grouped output projection: the low-rank rows
   W.tc = put(tc_decode_ws_bytes(h, n, max_ctx));
+  W.qkv_total = off;
+  W.lat = put(h->cache8 ? latent_ws_bytes(h, n, 0, max_ctx) : 0);
   const size_t dec_end = off;
   W.dec_total = dec_end;
   off = 256;
@@ -263,11 +268,12 @@ static void launch_o_proj_simt(const mla_handle* h, const void* head, void* out,
 // ---------------------------------------------------------------------------
 // entry points
 // ---------------------------------------------------------------------------
-// The decode calls' own requirement (mla_workspace_bytes also covers prefill,
-// whose FP8 weight dequantisation buffer decode never touches).
+// The decode front-fold's own requirement (mla_workspace_bytes also covers the
+// attention on an 8-bit cache and prefill, whose FP8 weight dequantisation
+// buffer decode never touches).
 size_t mla_decode_workspace_bytes_internal(const mla_handle* h, int n) {
   if (!h || n < 1) return 0;
-  return make_ws(h, n, 1).dec_total;
+  return make_ws(h, n, 1).qkv_total;
 }
 
 // Commits mla_decode_qkv_noalloc's device array on the current device (mla_noalloc.cu).
@@ -441,9 +447,10 @@ int mla_decode_qkv(mla_handle* h, const void* hidden, int n, const float* cos, c
   if (n == 0) return MLA_OK;
   if (!hidden || !cos || !sin || !kv_cache || !slot_mapping || !q_abs || !q_pe || !ws)
     return MLA_ERR_INVALID_ARG;
+  if (h->cache8 && (uintptr_t)kv_cache % 16) return MLA_ERR_INVALID_ARG;
   const mla_config* c = &h->cfg;
   const WsLayout W = make_ws(h, n, 1);
-  if (ws_bytes < W.dec_total) return MLA_ERR_WORKSPACE;
+  if (ws_bytes < W.qkv_total) return MLA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   char* wsb = (char*)ws;
   int* flag = (int*)wsb;
@@ -476,6 +483,7 @@ int mla_decode_qkv(mla_handle* h, const void* hidden, int n, const float* cos, c
   f.qn = rq ? wsb + W.qn : nullptr; f.ldqn = rq;
   f.cache = kv_cache; f.n_rows = (long long)n_blocks * c->block_size;
   f.slot = slot_mapping; f.layout = c->row_layout; f.flag = flag;
+  f.c8 = cache8_of(h);
   if (ta == 0) frontfold_epilogue_kernel<float><<<n, 256, 0, s>>>(f);
   else frontfold_epilogue_kernel<bf16><<<n, 256, 0, s>>>(f);
   count_launch();
@@ -500,17 +508,13 @@ int mla_decode_qkv(mla_handle* h, const void* hidden, int n, const float* cos, c
   return cuda_status();
 }
 
-int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
-                    const int32_t* block_table, int max_blocks_per_seq, const int32_t* context_lens,
-                    int max_context_len, int n, void* out, void* head_out, void* ws, size_t ws_bytes,
-                    void* stream) {
-  if (!h || n < 0 || n_blocks < 0 || max_blocks_per_seq < 0) return MLA_ERR_INVALID_ARG;
-  if (n == 0) return MLA_OK;
-  if (!q_abs || !q_pe || !kv_cache || !block_table || !context_lens || !out || !ws) return MLA_ERR_INVALID_ARG;
-  if (max_context_len < 1 || max_blocks_per_seq < 1) return MLA_ERR_INVALID_ARG;
+// The decode attention, V extraction and output projection; `ext` replaces the
+// attention by latent_core on what it names.
+static int decode_attn_impl(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
+                            const int32_t* block_table, int max_blocks_per_seq, const int32_t* context_lens,
+                            int max_context_len, int n, void* out, void* head_out, void* ws, const WsLayout& W,
+                            const LatentExt* ext, void* stream) {
   const mla_config* c = &h->cfg;
-  const WsLayout W = make_ws(h, n, max_context_len);
-  if (ws_bytes < W.dec_total) return MLA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   char* wsb = (char*)ws;
   int* flag = (int*)wsb;
@@ -522,11 +526,14 @@ int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
     const int r = tc_decode_attn(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq,
                                  context_lens, max_context_len, n, out, head, wsb, W.tc, s,
                                  (float*)(wsb + W.part_o), (float*)(wsb + W.part_ml), W.splits,
-                                 (bf16*)(wsb + W.o_lat), (int*)(wsb + W.nseg), head_out == nullptr);
+                                 (bf16*)(wsb + W.o_lat), (int*)(wsb + W.nseg), head_out == nullptr, ext);
     return r != MLA_OK ? r : cuda_status();
   }
   void* o_lat = wsb + W.o_lat;
-  if (tc_attention_supported(h)) {
+  if (ext) {
+    const int r = latent_core(h, *ext->call, o_lat, ta, nullptr, ext->scratch, flag, s);
+    if (r != MLA_OK) return r;
+  } else if (tc_attention_supported(h)) {
     // tensor-core attention (bf16 activations) ahead of CUDA-core W_UV / o_proj
     const int r = tc_attention_core(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq,
                                     context_lens, max_context_len, n, (float*)(wsb + W.part_o),
@@ -563,6 +570,134 @@ int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
   // out = head_out @ wo (or wo_a -> wo_b)
   launch_o_proj_simt(h, head, out, wsb + W.oy, n, s);
   return cuda_status();
+}
+
+int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
+                    const int32_t* block_table, int max_blocks_per_seq, const int32_t* context_lens,
+                    int max_context_len, int n, void* out, void* head_out, void* ws, size_t ws_bytes,
+                    void* stream) {
+  if (!h || n < 0 || n_blocks < 0 || max_blocks_per_seq < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  if (!q_abs || !q_pe || !kv_cache || !block_table || !context_lens || !out || !ws) return MLA_ERR_INVALID_ARG;
+  if (max_context_len < 1 || max_blocks_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (h->cache8 && (uintptr_t)kv_cache % 16) return MLA_ERR_INVALID_ARG;
+  const WsLayout W = make_ws(h, n, max_context_len);
+  if (ws_bytes < W.dec_total) return MLA_ERR_WORKSPACE;
+  const LatentCall call{q_abs, q_pe, kv_cache, n_blocks, nullptr, 0, block_table, max_blocks_per_seq,
+                        context_lens, max_context_len, n};
+  const LatentExt ext{&call, (char*)ws + W.lat};
+  return decode_attn_impl(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq, context_lens,
+                          max_context_len, n, out, head_out, ws, W, h->cache8 ? &ext : nullptr, stream);
+}
+
+// ---- the cache's type, its rows in and out ----
+
+// The handle's weights live on one device, and a launch goes to the current one.
+static bool on_device(const mla_handle* h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+int mla_set_cache_dtype(mla_handle* h, int cache_dtype) {
+  if (!h) return MLA_ERR_INVALID_ARG;
+  if (cache_dtype == h->cfg.act_dtype) { h->cache8 = 0; return MLA_OK; }
+  if (cache_dtype == MLA_FP8_E4M3_ROW) { h->cache8 = 1; return MLA_OK; }
+  return cache_dtype == MLA_F32 || cache_dtype == MLA_BF16 ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+}
+
+size_t mla_cache_block_bytes(const mla_handle* h) {
+  if (!h) return 0;
+  const mla_config* c = &h->cfg;
+  if (h->cache8) return (size_t)cache8_of(h).block_bytes;
+  return (size_t)c->block_size * (c->kv_lora_rank + c->qk_rope) * dtype_size(c->act_dtype);
+}
+
+static int cache_rows(mla_handle* h, const void* rows, int n, const void* kv_cache, int n_blocks,
+                      const int32_t* slots, void* ws, size_t ws_bytes, void* stream, bool write) {
+  if (!h || n < 0 || n_blocks < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  if (!rows || !kv_cache || !slots || !ws || (uintptr_t)rows % 16 || (uintptr_t)kv_cache % 16) return MLA_ERR_INVALID_ARG;
+  if (ws_bytes < 256) return MLA_ERR_WORKSPACE;
+  if (!on_device(h)) return MLA_ERR_INVALID_ARG;
+  const mla_config* c = &h->cfg;
+  CacheRowArgs p{};
+  p.c = cache8_of(h);
+  p.rows = const_cast<void*>(rows); p.cache = (uint8_t*)const_cast<void*>(kv_cache); p.slots = slots;
+  p.n = n; p.n_rows = (long long)n_blocks * c->block_size; p.layout = c->row_layout; p.flag = (int*)ws;
+  const long long want = cdiv(n, 8), most = 8LL * (h->tc.num_sms > 0 ? h->tc.num_sms : 148);   // 8 CTAs of 256 per SM
+  const unsigned grid = (unsigned)(want < most ? want : most);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (c->act_dtype == MLA_F32) {
+    if (write) launch_pdl(cache_rows_kernel<float, true>, grid, 256, 0, s, p);
+    else launch_pdl(cache_rows_kernel<float, false>, grid, 256, 0, s, p);
+  } else {
+    if (write) launch_pdl(cache_rows_kernel<bf16, true>, grid, 256, 0, s, p);
+    else launch_pdl(cache_rows_kernel<bf16, false>, grid, 256, 0, s, p);
+  }
+  count_launch();
+  return cuda_status();
+}
+
+int mla_cache_write(mla_handle* h, const void* rows, int n, void* kv_cache, int n_blocks,
+                    const int32_t* slot_mapping, void* ws, size_t ws_bytes, void* stream) {
+  return cache_rows(h, rows, n, kv_cache, n_blocks, slot_mapping, ws, ws_bytes, stream, true);
+}
+
+int mla_cache_read(mla_handle* h, const void* kv_cache, int n_blocks, const int32_t* slots, int n, void* rows,
+                   void* ws, size_t ws_bytes, void* stream) {
+  return cache_rows(h, rows, n, kv_cache, n_blocks, slots, ws, ws_bytes, stream, false);
+}
+
+// ---- attention with a shared prefix, and in latent form ----
+
+size_t mla_prefix_workspace_bytes(const mla_handle* h, int max_tokens, int max_prefix_len, int max_context_len) {
+  if (!h || max_tokens < 1 || max_prefix_len < 0 || max_context_len < 1) return 0;
+  if ((long long)max_prefix_len + max_context_len > (1 << 30)) return 0;
+  return make_ws(h, max_tokens, max_context_len).total + latent_ws_bytes(h, max_tokens, max_prefix_len, max_context_len);
+}
+
+// Checks shared by the two calls below; *W the workspace layout.
+static int latent_check(mla_handle* h, const LatentCall& a, const void* out, const void* ws, size_t ws_bytes,
+                        WsLayout* W) {
+  if (!a.q_abs || !a.q_pe || !a.cache || !a.table || !a.ctx || !out || !ws) return MLA_ERR_INVALID_ARG;
+  if (a.max_ctx < 1 || a.mbps < 1 || a.prefix_len < 0 || (a.prefix_len > 0) != (a.prefix_table != nullptr))
+    return MLA_ERR_INVALID_ARG;
+  if ((long long)a.prefix_len + a.max_ctx > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  if ((uintptr_t)a.cache % 16 || !on_device(h)) return MLA_ERR_INVALID_ARG;
+  *W = make_ws(h, a.n, a.max_ctx);
+  if (ws_bytes < W->total + latent_ws_bytes(h, a.n, a.prefix_len, a.max_ctx)) return MLA_ERR_WORKSPACE;
+  return MLA_OK;
+}
+
+int mla_latent_attn(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
+                    const int32_t* prefix_table, int prefix_len, const int32_t* block_table, int max_blocks_per_seq,
+                    const int32_t* context_lens, int max_context_len, int n, void* o_lat, float* lse, void* ws,
+                    size_t ws_bytes, void* stream) {
+  if (!h || n < 0 || n_blocks < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  const LatentCall a{q_abs, q_pe, kv_cache, n_blocks, prefix_table, prefix_len, block_table, max_blocks_per_seq,
+                     context_lens, max_context_len, n};
+  WsLayout W;
+  const int st = latent_check(h, a, o_lat, ws, ws_bytes, &W);
+  if (st != MLA_OK) return st;
+  const int r = latent_core(h, a, o_lat, acode(h), lse, (char*)ws + W.total, (int*)ws, (cudaStream_t)stream);
+  return r != MLA_OK ? r : cuda_status();
+}
+
+int mla_decode_attn_prefix(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
+                           const int32_t* prefix_table, int prefix_len, const int32_t* block_table,
+                           int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, int n, void* out,
+                           void* head_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!h || n < 0 || n_blocks < 0) return MLA_ERR_INVALID_ARG;
+  if (n == 0) return MLA_OK;
+  const LatentCall a{q_abs, q_pe, kv_cache, n_blocks, prefix_table, prefix_len, block_table, max_blocks_per_seq,
+                     context_lens, max_context_len, n};
+  WsLayout W;
+  const int st = latent_check(h, a, out, ws, ws_bytes, &W);
+  if (st != MLA_OK) return st;
+  const LatentExt ext{&a, (char*)ws + W.total};
+  return decode_attn_impl(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq, context_lens,
+                          max_context_len, n, out, head_out, ws, W, &ext, stream);
 }
 
 // Stage buffer of mla_decode_step_host: staged inputs, then the step's own
@@ -673,7 +808,7 @@ int mla_decode_step_host(mla_handle* h, const void* hidden_host, const int32_t* 
       (unsigned long long)stage_bytes,            (unsigned long long)n,
       (unsigned long long)max_blocks_per_seq,     (unsigned long long)max_context_len,
       (unsigned long long)n_blocks,               theta_bits,
-      (unsigned long long)(uintptr_t)h->host_pack, 1ull};
+      (unsigned long long)(uintptr_t)h->host_pack, 1ull + (unsigned long long)h->cache8};
   if (!h->step_exec || memcmp(key, h->step_key, sizeof key) != 0) {
     if (!h->capture_stream && cudaStreamCreateWithFlags(&h->capture_stream, cudaStreamNonBlocking) != cudaSuccess) {
       h->capture_stream = nullptr;
@@ -715,6 +850,7 @@ int mla_prefill(mla_handle* h, const void* hidden, int S, const float* cos, cons
   if (S == 0) return MLA_OK;
   if (!hidden || !cos || !sin || !out || !ws) return MLA_ERR_INVALID_ARG;
   if ((kv_cache == nullptr) != (slot_mapping == nullptr)) return MLA_ERR_INVALID_ARG;
+  if (h->cache8 && (uintptr_t)kv_cache % 16) return MLA_ERR_INVALID_ARG;
   const mla_config* c = &h->cfg;
   const WsLayout W = make_ws(h, S, 1);
   if (ws_bytes < W.total) return MLA_ERR_WORKSPACE;
@@ -753,6 +889,7 @@ int mla_prefill(mla_handle* h, const void* hidden, int S, const float* cos, cons
   f.cache = kv_cache; f.n_rows = (long long)n_blocks * c->block_size;
   f.slot = slot_mapping; f.layout = c->row_layout; f.flag = flag;
   f.cn = wsb + W.pcn; f.kpe = wsb + W.pkpe;
+  f.c8 = cache8_of(h);
   if (ta == 0) frontfold_epilogue_kernel<float><<<S, 256, 0, s>>>(f);
   else frontfold_epilogue_kernel<bf16><<<S, 256, 0, s>>>(f);
   count_launch();

@@ -7,6 +7,7 @@
 
 #include <math.h>
 
+#include "cache8.cuh"
 #include "common.cuh"
 
 namespace mla {
@@ -124,6 +125,7 @@ struct FrontFoldArgs {
   // the whole kv row [r_kv + d_r] is RMS-normed with a gamma of that length and
   // its normed tail is rotated; with slot == NULL row t goes to cache row t
   int v4;
+  Cache8 c8;                              // c8.on: the cache is 8-bit (cache8.cuh)
 };
 
 template <typename TACT>
@@ -147,16 +149,24 @@ __global__ void __launch_bounds__(256) frontfold_epilogue_kernel(FrontFoldArgs p
   for (int i = threadIdx.x; i < nn; i += blockDim.x) ss += kv[i] * kv[i];
   const float r = rsqrtf(block_sum(ss, red) / (float)nn + p.eps);
   TACT* row = nullptr;
+  TACT* row_pe = nullptr;
+  const int lat_off = (p.layout == MLA_ROW_LATENT_FIRST) ? 0 : p.d_r;
+  const int pe_off = (p.layout == MLA_ROW_LATENT_FIRST) ? p.r_kv : 0;
   if (p.cache) {
     const int s = p.slot ? p.slot[t] : t;
     if (s >= 0 && (long long)s < p.n_rows) {
-      row = (TACT*)p.cache + (long long)s * R;
+      if (p.c8.on) {
+        c8_store_latent<TACT>(p.c8, (uint8_t*)p.cache, s,
+                              [&](int i) { return to_f32(from_f32<TACT>(kv[i] * r * p.kv_norm_w[i])); }, red);
+        row_pe = c8_rotary<TACT>(p.c8, (uint8_t*)p.cache, s);
+      } else {
+        row = (TACT*)p.cache + (long long)s * R;
+        row_pe = row + pe_off;
+      }
     } else if (s >= 0) {
       if (threadIdx.x == 0) set_flag(p.flag, MLA_FLAG_BAD_SLOT);
     }
   }
-  const int lat_off = (p.layout == MLA_ROW_LATENT_FIRST) ? 0 : p.d_r;
-  const int pe_off = (p.layout == MLA_ROW_LATENT_FIRST) ? p.r_kv : 0;
   for (int i = threadIdx.x; i < p.r_kv; i += blockDim.x) {
     const TACT v = from_f32<TACT>(kv[i] * r * p.kv_norm_w[i]);
     if (row) row[lat_off + i] = v;
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(256) frontfold_epilogue_kernel(FrontFoldArgs p
     float o0, o1;
     rope_pair(e0, e1, p.cos[(long long)t * half + i], p.sin[(long long)t * half + i], &o0, &o1);
     const TACT a = from_f32<TACT>(o0), b = from_f32<TACT>(o1);
-    if (row) { row[pe_off + 2 * i] = a; row[pe_off + 2 * i + 1] = b; }
+    if (row_pe) { row_pe[2 * i] = a; row_pe[2 * i + 1] = b; }
     if (p.kpe) {
       ((TACT*)p.kpe)[(long long)t * p.d_r + 2 * i] = a;
       ((TACT*)p.kpe)[(long long)t * p.d_r + 2 * i + 1] = b;
@@ -310,11 +320,15 @@ struct AttnArgs {
   float* part_o;                           // [n, n_splits, H, r_kv]
   float* part_ml;                          // [n, n_splits, H, 2]
   int* flag;
+  // EXT: keys 0 .. prefix_len - 1 come from the batch's shared prefix blocks
+  // (a sequence may then have no rows of its own), and with c8.on the cache is 8-bit
+  const int* prefix_table; int prefix_len;
+  Cache8 c8;
 };
 
 constexpr int ATT_HPB = 8, ATT_TR = 32;
 
-template <typename T>
+template <typename T, bool EXT = false>
 __global__ void __launch_bounds__(256) attn_decode_simt_kernel(AttnArgs p) {
   extern __shared__ float smem[];
   const int R = p.r_kv + p.d_r, RP = R + 1;
@@ -325,9 +339,12 @@ __global__ void __launch_bounds__(256) attn_decode_simt_kernel(AttnArgs p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = g * ATT_HPB + warp;
   int L = p.ctx[t];
-  if (L < 1 || L > p.max_ctx || L > p.mbps * p.bs) {
+  const int P = EXT ? p.prefix_len : 0;
+  if (L < (EXT && P > 0 ? 0 : 1) || L > p.max_ctx || (long long)L > (long long)p.mbps * p.bs) {
     if (threadIdx.x == 0 && s == 0 && g == 0) set_flag(p.flag, MLA_FLAG_BAD_CONTEXT);
     L = 0;
+  } else {
+    L += P;
   }
   const int j0 = s * p.chunk, j1 = min(L, j0 + p.chunk);
   const int lat_off = (p.layout == MLA_ROW_LATENT_FIRST) ? 0 : p.d_r;
@@ -356,12 +373,23 @@ __global__ void __launch_bounds__(256) attn_decode_simt_kernel(AttnArgs p) {
       int ok = 0;
       long long row = 0;
       if (j < j1) {
-        const int blk = p.block_table[(long long)t * p.mbps + j / p.bs];
-        if (blk >= 0 && blk < p.n_blocks) { ok = 1; row = (long long)blk * p.bs + j % p.bs; }
+        const int jj = EXT && j >= P ? j - P : j;   // the row's position in its own list of blocks
+        const int blk = EXT && j < P ? p.prefix_table[j / p.bs] : p.block_table[(long long)t * p.mbps + jj / p.bs];
+        if (blk >= 0 && blk < p.n_blocks) { ok = 1; row = (long long)blk * p.bs + jj % p.bs; }
         else if (lane == 0) set_flag(p.flag, MLA_FLAG_BAD_BLOCK);
       }
-      const T* src = (const T*)p.cache + row * R;
-      for (int k = lane; k < R; k += 32) rows[r * RP + k] = ok ? to_f32(src[k]) : 0.f;
+      if (EXT && p.c8.on) {
+        const uint8_t* cb = (const uint8_t*)p.cache + row / p.bs * p.c8.block_bytes;
+        const long long ro = row % p.bs;
+        const uint8_t* codes = cb + ro * p.r_kv;
+        const T* pe = (const T*)(cb + p.c8.pe_off) + ro * p.d_r;
+        const float sc = ok ? ((const float*)(cb + p.c8.sc_off))[ro] : 0.f;
+        for (int k = lane; k < p.r_kv; k += 32) rows[r * RP + lat_off + k] = ok ? e4m3_to_f32(codes[k]) * sc : 0.f;
+        for (int k = lane; k < p.d_r; k += 32) rows[r * RP + pe_off + k] = ok ? to_f32(pe[k]) : 0.f;
+      } else {
+        const T* src = (const T*)p.cache + row * R;
+        for (int k = lane; k < R; k += 32) rows[r * RP + k] = ok ? to_f32(src[k]) : 0.f;
+      }
       if (lane == 0) valid_row[r] = ok;
     }
     __syncthreads();

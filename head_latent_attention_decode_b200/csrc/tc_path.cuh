@@ -218,6 +218,7 @@ struct FrontFoldTcArgs {
   bf16* cache; long long n_rows; const int* slot; int layout;
   int* flag;
   int q_cols;   // columns of the q part per CTA: all r_q, or whole heads of d_n + d_r
+  Cache8 c8;    // c8.on: the cache is 8-bit (cache8.cuh)
 };
 
 // Sum the K-split partials of columns [c0, c0 + w) of token t's row of x @ W1
@@ -309,17 +310,25 @@ __global__ void __launch_bounds__(512) frontfold_tc_kernel(FrontFoldTcArgs p) {
     if (threadIdx.x == 0) set_flag(p.flag, MLA_FLAG_BAD_SLOT);
     return;
   }
-  bf16* row = p.cache + (long long)slot * (p.rkv + p.dr);
-  const int lat_off = (p.layout == MLA_ROW_LATENT_FIRST) ? 0 : p.dr;
-  const int pe_off = (p.layout == MLA_ROW_LATENT_FIRST) ? p.rkv : 0;
-  for (int i = threadIdx.x; i < p.rkv; i += blockDim.x)
-    row[lat_off + i] = __float2bfloat16_rn(kv[i] * r * p.kv_norm_w[i]);
+  bf16* pe_row;
+  if (p.c8.on) {
+    // the codes are of the values a bf16 cache would hold
+    c8_store_latent<bf16>(p.c8, (uint8_t*)p.cache, slot,
+                          [&](int i) { return to_f32(__float2bfloat16_rn(kv[i] * r * p.kv_norm_w[i])); }, red);
+    pe_row = c8_rotary<bf16>(p.c8, (uint8_t*)p.cache, slot);
+  } else {
+    bf16* row = p.cache + (long long)slot * (p.rkv + p.dr);
+    const int lat_off = (p.layout == MLA_ROW_LATENT_FIRST) ? 0 : p.dr;
+    pe_row = row + ((p.layout == MLA_ROW_LATENT_FIRST) ? p.rkv : 0);
+    for (int i = threadIdx.x; i < p.rkv; i += blockDim.x)
+      row[lat_off + i] = __float2bfloat16_rn(kv[i] * r * p.kv_norm_w[i]);
+  }
   for (int i = threadIdx.x; i < half; i += blockDim.x) {
     float o0, o1;
     rope_pair(kv[p.rkv + 2 * i], kv[p.rkv + 2 * i + 1], p.cos[(long long)t * half + i],
               p.sin[(long long)t * half + i], &o0, &o1);
-    row[pe_off + 2 * i] = __float2bfloat16_rn(o0);
-    row[pe_off + 2 * i + 1] = __float2bfloat16_rn(o1);
+    pe_row[2 * i] = __float2bfloat16_rn(o0);
+    pe_row[2 * i + 1] = __float2bfloat16_rn(o1);
   }
 }
 
@@ -664,6 +673,7 @@ static inline int tc_decode_qkv(const mla_handle* h, const void* hidden, int n, 
   f.qn = (bf16*)(tw + W.qn); f.q_nope = (bf16*)(tw + W.q_nope); f.q_pe = (bf16*)q_pe; f.act_f16 = af16;
   f.cache = (bf16*)kv_cache; f.n_rows = (long long)n_blocks * c.block_size; f.slot = slot_mapping;
   f.layout = c.row_layout; f.flag = flag;
+  f.c8 = cache8_of(h);
   // the q part in slices: all of r_q (its RMSNorm spans it), or about a third
   // of the heads each without q_lora; the kv part in CTA 0
   const int hd = dn + dr;
@@ -686,6 +696,16 @@ static inline int tc_decode_qkv(const mla_handle* h, const void* hidden, int n, 
   g3.b_rows_dim2 = 1;
   return wgemm(h, W_UK, vn, g3, bn, 1, f16buf, dq, s);
 }
+
+// What a decode-attention call on an 8-bit cache or with a shared prefix attends
+// to, and its scratch (latent_attn.cuh).
+struct LatentCall;
+static inline int latent_core(const mla_handle* h, const LatentCall& a, void* o_lat, int o_dt, float* lse, char* scratch,
+                              int* flag, cudaStream_t s);
+struct LatentExt {
+  const LatentCall* call;
+  char* scratch;
+};
 
 // Split-KV absorbed attention and the LSE merge of the splits -> o_lat (bf16).
 // tcgen05 kernel for the DeepSeek latent dims, CUDA-core kernel otherwise.
@@ -806,7 +826,7 @@ static inline int tc_decode_attn(const mla_handle* h, const void* q_abs, const v
                                  int n_blocks, const int32_t* block_table, int mbps, const int32_t* ctx,
                                  int max_ctx, int n, void* out, void* head, char* ws, size_t tc_off,
                                  cudaStream_t s, float* part_o, float* part_ml, int splits, bf16* o_lat,
-                                 int* nseg, bool head_internal) {
+                                 int* nseg, bool head_internal, const LatentExt* ext = nullptr) {
   const mla_config& c = h->cfg;
   const TcDecodeWs W = tc_decode_ws(h, n);
   char* tw = ws + tc_off;
@@ -816,8 +836,9 @@ static inline int tc_decode_attn(const mla_handle* h, const void* q_abs, const v
   // with the FP8-weight GEMM, o_lat, the head outputs (unless the caller asked for
   // them) and the grouped low-rank rows are written in f16: only those GEMMs read them
   const int af16 = h->tc.fp8 && !W.deq, hf16 = af16 && head_internal;
-  int st = tc_attention_core(h, q_abs, q_pe, kv_cache, n_blocks, block_table, mbps, ctx, max_ctx, n, part_o,
-                             part_ml, splits, o_lat, flag, nseg, s, af16);
+  int st = ext ? latent_core(h, *ext->call, o_lat, af16 ? 2 : 1, nullptr, ext->scratch, flag, s)
+               : tc_attention_core(h, q_abs, q_pe, kv_cache, n_blocks, block_table, mbps, ctx, max_ctx, n, part_o,
+                                   part_ml, splits, o_lat, flag, nseg, s, af16);
   if (st != MLA_OK) return st;
   // 2. head_out[h] = o_lat[h] @ W_UV[h]  (A = Wuv[h] [d_v, r_kv], B = o_lat[:, h, :])
   void* f16buf = tw + W.bf16c;
@@ -960,6 +981,7 @@ static inline int tc_prefill(const mla_handle* h, const void* hidden, int S, con
   f.cache = kv_cache; f.n_rows = (long long)n_blocks * c.block_size;
   f.slot = slot_mapping; f.layout = c.row_layout; f.flag = flag;
   f.cn = ws + pcn; f.kpe = ws + pkpe;
+  f.c8 = cache8_of(h);
   launch_pdl(frontfold_epilogue_kernel<bf16>, S, 256, 0, s, f);
   mla_count_launch(1);
   if (rq) {

@@ -8,9 +8,11 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (MLA_ROW_LATENT_FIRST, make_config, mla_decode_attn, mla_decode_qkv, mla_destroy,
-               mla_init_weights, mla_prefill, mla_rope_cos_sin, mla_rope_cos_sin_inv_freq, mla_v4_qkv,
-               mla_weights_bytes, mla_workspace_bytes, mla_workspace_init)
+from . import (MLA_FP8_E4M3_ROW, MLA_ROW_LATENT_FIRST, make_config, mla_cache_block_bytes, mla_cache_read,
+               mla_cache_write, mla_decode_attn, mla_decode_attn_prefix, mla_decode_qkv, mla_destroy,
+               mla_init_weights, mla_latent_attn, mla_prefill, mla_prefix_workspace_bytes, mla_rope_cos_sin,
+               mla_rope_cos_sin_inv_freq, mla_set_cache_dtype, mla_v4_qkv, mla_weights_bytes,
+               mla_workspace_bytes, mla_workspace_init)
 
 ACT_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
 
@@ -35,7 +37,11 @@ class MlaLayer:
     """One layer's repacked weights (device) and C-ABI handle."""
 
     def __init__(self, shape, weights, row_layout: int = MLA_ROW_LATENT_FIRST,
-                 device: str = "cuda", softmax_scale: float = 0.0, attn_sink=None):
+                 device: str = "cuda", softmax_scale: float = 0.0, attn_sink=None, cache_dtype: str | None = None):
+        """cache_dtype: None for a cache in the activation dtype, "fp8" for the 8-bit cache."""
+        if cache_dtype not in (None, "fp8"):
+            raise ValueError(f"cache_dtype must be None or 'fp8', not {cache_dtype!r}")
+        self.cache_dtype = cache_dtype
         self.shape = shape
         self.device = torch.device(device)
         self.act = ACT_TORCH[shape.act_dtype]
@@ -51,6 +57,8 @@ class MlaLayer:
         self.handle = mla_init_weights(self.cfg, src, self.blob)
         torch.cuda.current_stream(self.device).synchronize()
         del src
+        if cache_dtype == "fp8":
+            mla_set_cache_dtype(self.handle, MLA_FP8_E4M3_ROW)
         self.ws = None
 
     def close(self) -> None:
@@ -71,6 +79,79 @@ class MlaLayer:
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             mla_workspace_init(self.ws)
         return self.ws
+
+    def prefix_workspace(self, max_tokens: int, max_prefix_len: int, max_context_len: int) -> torch.Tensor:
+        """A workspace for latent_attn and decode_attn_prefix (and every other call)."""
+        need = mla_prefix_workspace_bytes(self.handle, max(1, max_tokens), max(0, max_prefix_len),
+                                          max(1, max_context_len))
+        if need == 0:
+            raise ValueError("prefix_workspace: sizes not accepted by the library")
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            mla_workspace_init(self.ws)
+        return self.ws
+
+    def new_cache(self, n_blocks: int) -> torch.Tensor:
+        """A zeroed paged cache: [n_blocks, 1, block_size, R], or [n_blocks, block bytes] uint8 if 8-bit."""
+        if self.cache_dtype == "fp8":
+            return torch.zeros((n_blocks, mla_cache_block_bytes(self.handle)), dtype=torch.uint8, device=self.device)
+        return torch.zeros((n_blocks, 1, self.shape.block_size, self.shape.kv_row_dim), dtype=self.act,
+                           device=self.device)
+
+    def _check_cache(self, kv_cache):
+        want = torch.uint8 if self.cache_dtype == "fp8" else self.act
+        if kv_cache.dtype != want or kv_cache[:1].numel() * kv_cache.element_size() != mla_cache_block_bytes(self.handle):
+            raise ValueError(f"kv_cache does not hold blocks of this layer's cache ({want}, "
+                             f"{mla_cache_block_bytes(self.handle)} bytes a block)")
+
+    def _check_rows(self, rows):
+        if rows.dtype != self.act or rows.dim() != 2 or rows.shape[1] != self.shape.kv_row_dim:
+            raise ValueError(f"rows must be [n, {self.shape.kv_row_dim}] {self.act}")
+
+    def cache_write(self, rows, kv_cache, slot_mapping):
+        """rows [n, R] into the cache's flat rows slot_mapping (negative: skipped), quantised if it is 8-bit."""
+        self._check_rows(rows)
+        self._check_cache(kv_cache)
+        mla_cache_write(self.handle, rows, kv_cache, slot_mapping, self.ws if self.ws is not None else self.workspace(1))
+        return kv_cache
+
+    def cache_read(self, kv_cache, slots, rows=None):
+        """[n, R] in the activation dtype: the values of the cache's flat rows `slots`."""
+        if rows is None:
+            rows = torch.zeros((slots.numel(), self.shape.kv_row_dim), dtype=self.act, device=self.device)
+        self._check_rows(rows)
+        self._check_cache(kv_cache)
+        mla_cache_read(self.handle, kv_cache, slots, rows, self.ws if self.ws is not None else self.workspace(1))
+        return rows
+
+    def _check_prefix(self, prefix_table, prefix_len):
+        if prefix_len and prefix_table.numel() * self.shape.block_size < prefix_len:
+            raise ValueError("prefix_table does not cover prefix_len rows")
+
+    def latent_attn(self, q_abs, q_pe, kv_cache, block_table, context_lens, max_context_len, prefix_table=None,
+                    prefix_len: int = 0, o_lat=None, want_lse: bool = False):
+        """(o_lat [n, H, r_kv], lse [n, H] fp32 or None) over the batch's shared prefix and each sequence's own rows."""
+        self._check_cache(kv_cache)
+        self._check_prefix(prefix_table, prefix_len)
+        if o_lat is None:
+            o_lat = torch.empty_like(q_abs)
+        lse = torch.empty(q_abs.shape[:2], dtype=torch.float32, device=self.device) if want_lse else None
+        ws = self.prefix_workspace(q_abs.shape[0], prefix_len, max_context_len)
+        mla_latent_attn(self.handle, q_abs, q_pe, kv_cache, block_table, context_lens, max_context_len, o_lat, ws,
+                        lse=lse, prefix_table=prefix_table, prefix_len=prefix_len)
+        return o_lat, lse
+
+    def decode_attn_prefix(self, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
+                           max_context_len, out=None, head_out=None):
+        """decode_attn over a prefix shared by the batch (its blocks in prefix_table) and each sequence's own rows."""
+        self._check_cache(kv_cache)
+        self._check_prefix(prefix_table, prefix_len)
+        if out is None:
+            out = torch.empty((q_abs.shape[0], self.shape.hidden), dtype=self.act, device=self.device)
+        ws = self.prefix_workspace(q_abs.shape[0], prefix_len, max_context_len)
+        mla_decode_attn_prefix(self.handle, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table,
+                               context_lens, max_context_len, out, ws, head_out=head_out)
+        return out
 
     def rope(self, positions: torch.Tensor, inv_freq: torch.Tensor | None = None):
         """cos/sin [n, qk_rope/2] fp32 of the positions; inv_freq (device fp32

@@ -17,7 +17,8 @@
  *     as the pages give them ("MLA Decode QKV Kernel API Reference",
  *     Parameters; "QKV CTE MLA Kernel API Reference", qkv_mla_mx parameters).
  *   - Activation dtype (MLA_F32 or MLA_BF16) applies to hidden states,
- *     q_abs / q_pe, the KV cache, head_out and out. RoPE tables and RMSNorm
+ *     q_abs / q_pe, the KV cache (unless mla_set_cache_dtype makes it 8-bit),
+ *     head_out and out. RoPE tables and RMSNorm
  *     gammas are always fp32.
  *   - Content errors that only the device can see (a slot or block id out of
  *     range, a context length out of range) set bits of a sticky int32 flag in
@@ -61,7 +62,10 @@ typedef enum {
    * wq_a_fp8 (128x128 block scales, dequantised in fp32 before the MAC with
    * bf16 activations); scale shape as "QKV CTE MLA Kernel API Reference",
    * *_scale_hbm. Weights only; needs act_dtype MLA_BF16. */
-  MLA_FP8_E4M3_B128 = 2
+  MLA_FP8_E4M3_B128 = 2,
+  /* 8-bit cache rows (mla_set_cache_dtype): E4M3 codes of the latent with one
+   * power-of-two fp32 scale per row, the rotary key in the activation dtype. */
+  MLA_FP8_E4M3_ROW = 3
 } mla_dtype;
 
 typedef enum {
@@ -178,6 +182,47 @@ int mla_workspace_init(void* ws, size_t ws_bytes, void* stream);
 int mla_read_device_flag(const void* ws, int* flag_out, void* stream);
 int mla_clear_device_flag(void* ws, void* stream);
 
+/* ---- the cache's type ------------------------------------------------------- */
+
+/* What the kv_cache arguments of this handle's calls hold, from now on:
+ *   the activation dtype (the default)  rows of r_kv + d_r elements,
+ *       [n_blocks, 1, block_size, R] as described with each call;
+ *   MLA_FP8_E4M3_ROW  n_blocks blocks of mla_cache_block_bytes(h) bytes, each
+ *       [bs, r_kv] E4M3 codes | [bs, d_r] rotary keys (act dtype) | [bs] fp32
+ *       scales, padded to a multiple of 128 bytes (bs = block_size).
+ *       A row's latent is scale * code with scale = 2^k, k the least integer in
+ *       [-64, 7] that brings the row's largest finite magnitude to at most 448
+ *       (a row of zeros: k = 0). The codes are the nearest E4M3 values of the
+ *       latent as a cache of the activation dtype would hold it (ties to even,
+ *       saturating at 448 * 2^7); NaN and infinities become NaN. row_layout
+ *       does not matter to it.
+ * mla_decode_qkv, mla_decode_qkv_noalloc, mla_prefill and mla_decode_step_host
+ * then quantise the rows they write, and mla_decode_attn reads them; kv_cache
+ * must be 16-byte aligned. mla_workspace_bytes depends on it: ask again after a
+ * change. Not to be called while calls on the same handle are in progress. */
+int mla_set_cache_dtype(mla_handle* h, int cache_dtype);
+
+/* Bytes of one block of the cache as the handle's calls take it. */
+size_t mla_cache_block_bytes(const mla_handle* h);
+
+/* Write n rows into the cache: row t (r_kv + d_r elements of the activation
+ * dtype, in row_layout's order, as mla_v4_qkv's kv_out gives them) goes to flat
+ * row slot_mapping[t], quantised if the cache is 8-bit.
+ * rows          device [n, R] act dtype, 16-byte aligned
+ * kv_cache      device, n_blocks blocks, 16-byte aligned, mutated in place;
+ *               only the slots named are written
+ * slot_mapping  device [n] int32, as in mla_decode_qkv. Slots must be distinct.
+ * ws            device workspace (the device flag: 256 bytes suffice) */
+int mla_cache_write(mla_handle* h, const void* rows, int n, void* kv_cache, int n_blocks,
+                    const int32_t* slot_mapping, void* ws, size_t ws_bytes, void* stream);
+
+/* Read n rows back: rows[t] = the values that flat cache row slots[t] holds
+ * (scale * code is exact in bf16 and fp32). A negative slot leaves rows[t] as
+ * it was; one beyond the cache sets MLA_FLAG_BAD_SLOT and does the same. The
+ * same slot may appear more than once. Arguments as in mla_cache_write. */
+int mla_cache_read(mla_handle* h, const void* kv_cache, int n_blocks, const int32_t* slots, int n, void* rows,
+                   void* ws, size_t ws_bytes, void* stream);
+
 /* ---- RoPE tables ---------------------------------------------------------- */
 
 /* cos/sin [n, d_r/2] fp32 (device) of positions[n] (device int32):
@@ -246,6 +291,50 @@ int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe,
                     int max_blocks_per_seq, const int32_t* context_lens,
                     int max_context_len, int n, void* out, void* head_out, void* ws,
                     size_t ws_bytes, void* stream);
+
+/* ---- decode attention with a shared prefix, and in latent form --------------- */
+
+/* Workspace of the two calls below (and of every other call) for up to
+ * max_tokens sequences, prefixes of up to max_prefix_len rows (0: none) and own
+ * contexts of up to max_context_len rows. 0 on invalid arguments. */
+size_t mla_prefix_workspace_bytes(const mla_handle* h, int max_tokens, int max_prefix_len, int max_context_len);
+
+/* The attention of mla_decode_attn alone, in the latent space, over the keys of
+ * a prefix that all n sequences share followed by each sequence's own rows:
+ *   keys(t) = rows 0 .. prefix_len - 1 of prefix_table, then rows
+ *             0 .. context_lens[t] - 1 of block_table[t]
+ *   s[h, j] = (q_abs[t, h] . c_j + q_pe[t, h] . k_pe_j) * softmax_scale
+ *   o_lat[t, h] = softmax_j(s[h]) @ c,  lse[t, h] = log sum_j e^{s[h, j]}
+ * with attn_sink[h], when the handle has it, as one more column of the softmax
+ * and of the sum. The prefix is read once for the whole batch. The results of
+ * several calls over different keys combine by their lse (without attn_sink,
+ * which each call counts).
+ * q_abs, q_pe      device, as written by mla_decode_qkv
+ * kv_cache         device, n_blocks blocks, 16-byte aligned (read only)
+ * prefix_table     device [ceil(prefix_len / bs)] int32, or NULL with
+ *                  prefix_len 0. prefix_len is a host int: a captured graph
+ *                  keeps it
+ * block_table, context_lens, max_context_len
+ *                  as in mla_decode_attn; with a prefix a context length may be
+ *                  0 (the sequence has no rows of its own). A sequence whose
+ *                  length is invalid attends to nothing: o_lat 0, lse -inf (the
+ *                  sink's, if any), and MLA_FLAG_BAD_CONTEXT. A block id out of
+ *                  range sets MLA_FLAG_BAD_BLOCK and its rows are left out
+ * o_lat            device [n, H, r_kv] act dtype
+ * lse              device [n, H] fp32, or NULL
+ * ws               device workspace of mla_prefix_workspace_bytes(h, n,
+ *                  prefix_len, max_context_len) bytes */
+int mla_latent_attn(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
+                    const int32_t* prefix_table, int prefix_len, const int32_t* block_table,
+                    int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, int n, void* o_lat,
+                    float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* mla_decode_attn over the keys of mla_latent_attn: attention, V extraction and
+ * o_proj. With prefix_len 0 it is mla_decode_attn. out, head_out as there. */
+int mla_decode_attn_prefix(mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache, int n_blocks,
+                           const int32_t* prefix_table, int prefix_len, const int32_t* block_table,
+                           int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, int n,
+                           void* out, void* head_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Size of the device array mla_decode_qkv_noalloc() uses as its workspace. */
 #define MLA_NOALLOC_SCRATCH_BYTES (64u << 20)

@@ -1,0 +1,498 @@
+"""GPU tests of the 8-bit latent cache (written, read back, attended to) and of
+decode attention over a shared prefix, against the fp64 definitions in
+oracle/latent_ref.py. Writing and reading are exact; the attention's bounds are
+derived in latent_common.Case.oracle."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import head_latent_attention_decode_b200 as mla
+from head_latent_attention_decode_b200 import workloads as wl
+from oracle import latent_ref as lr
+
+from latent_common import ACT, ESZ, Case, check, layer_of, pack_cache, row_values, shape_of
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = {"latent512": dict(bs=64), "bs48": dict(bs=48), "small": dict(bs=16, r_kv=64, d_r=16),
+          "odd_block": dict(bs=7, r_kv=96, d_r=8)}
+
+
+def special_rows(shape, n, seed):
+    """Rows of many sizes, with the values at which a quantiser can go wrong."""
+    rng = np.random.default_rng(seed)
+    r = shape.kv_lora_rank
+    x = rng.standard_normal((n, shape.kv_row_dim)) * 2.0 ** rng.integers(-6, 6, (n, 1))
+    rows = torch.from_numpy(x.astype(np.float32)).to(ACT[shape.act_dtype])
+    lat = rows[:, :r]
+    edge = [lambda v: v.zero_(), lambda v: v.fill_(448.0), lambda v: v.fill_(450.0), lambda v: v.mul_(1e-30),
+            lambda v: v.mul_(1e30), lambda v: v[1:3].fill_(float("nan")), lambda v: v[:1].fill_(float("inf")),
+            lambda v: v.fill_(-float("inf")), lambda v: v[5:6].fill_(57344.0), lambda v: v.fill_(1.75 * 2.0 ** -3),
+            lambda v: v[:8].copy_(torch.tensor([17, 19, 21, 23, 25, 27, 29, 448.0])), lambda v: v.mul_(2.0 ** -90)]
+    for i, f in enumerate(edge):
+        if i < n:
+            f(lat[i])
+    return rows
+
+
+def same_bytes(a, b):
+    return torch.equal(a.cpu().view(torch.uint8), b.cpu().view(torch.uint8))
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(SHAPES))
+@pytest.mark.parametrize("n", [1, 13, 301])
+def test_write_and_read_are_exact(name, act, n):
+    shape = shape_of(4, act=act, **SHAPES[name])
+    layer = layer_of(shape, True)
+    rows = special_rows(shape, n, n)
+    n_blocks = -(-n // shape.block_size) + 2
+    rng = np.random.default_rng(n)
+    slots = rng.permutation(n_blocks * shape.block_size)[:n].astype(np.int32)
+    if n > 12:
+        slots[12] = -1
+    cache = layer.new_cache(n_blocks)
+    cache.fill_(0xAB)
+    layer.cache_write(rows.cuda(), cache, torch.from_numpy(slots).cuda())
+    want = pack_cache(shape, rows, slots, n_blocks, fill=0xAB)
+    got = cache.cpu().numpy()
+    # E4M3 has two NaN codes and two zeros: the codes' values count, all other bytes are equal
+    diff = got != want
+    codes = np.zeros_like(diff)
+    codes[:, :shape.block_size * shape.kv_lora_rank] = True
+    assert not (diff & ~codes).any()
+    a, b = lr.E4M3[got[codes]], lr.E4M3[want[codes]]
+    assert np.array_equal(a, b, equal_nan=True)
+    # back, with a repeated slot and one that is skipped
+    back = np.concatenate([slots, slots[:1], [-5]]).astype(np.int32)
+    out = torch.full((n + 2, shape.kv_row_dim), 7.0, dtype=ACT[act], device="cuda")
+    layer.cache_read(cache, torch.from_numpy(back).cuda(), out)
+    vals = row_values(shape, rows)
+    vals[slots < 0] = 7.0
+    vals = np.concatenate([vals, vals[:1], np.full((1, shape.kv_row_dim), 7.0)])
+    assert np.array_equal(out.double().cpu().numpy(), vals, equal_nan=True)
+    assert mla.mla_read_device_flag(layer.ws) == 0
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_row_copies_of_an_activation_dtype_cache(act):
+    shape = shape_of(4, 16, act=act, r_kv=64, d_r=16)
+    layer = layer_of(shape, False)
+    rows = torch.randn(33, shape.kv_row_dim).to(ACT[act])
+    slots = torch.randperm(64)[:33].int()
+    cache = layer.new_cache(4)
+    layer.cache_write(rows.cuda(), cache, slots.cuda())
+    want = torch.zeros(64, shape.kv_row_dim, dtype=ACT[act])
+    want[slots.long()] = rows
+    assert same_bytes(cache.reshape(64, -1), want)
+    assert same_bytes(layer.cache_read(cache, slots.cuda()), rows)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_pe_first_rows(fp8):
+    shape = shape_of(4, 16, r_kv=64, d_r=16)
+    layer = layer_of(shape, fp8, row_layout=mla.MLA_ROW_PE_FIRST)
+    rows = special_rows(shape, 5, 3)
+    flipped = torch.cat([rows[:, 64:], rows[:, :64]], 1).contiguous().cuda()
+    slots = torch.tensor([3, 1, 17, 30, 0], dtype=torch.int32, device="cuda")
+    cache = layer.new_cache(2)
+    layer.cache_write(flipped, cache, slots)
+    want = row_values(shape, rows) if fp8 else rows.double().numpy()
+    want = np.concatenate([want[:, 64:], want[:, :64]], 1)
+    assert np.array_equal(layer.cache_read(cache, slots).double().cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_slots_beyond_the_cache_are_flagged_and_left_out(fp8):
+    shape = shape_of(4, 16, r_kv=64, d_r=16)
+    layer = layer_of(shape, fp8)
+    cache = layer.new_cache(2)
+    before = cache.clone()
+    rows = torch.randn(3, shape.kv_row_dim, device="cuda").bfloat16()
+    slots = torch.tensor([32, -1, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    layer.cache_write(rows, cache, slots)
+    assert mla.mla_read_device_flag(layer.ws) == mla.MLA_FLAG_BAD_SLOT
+    assert same_bytes(cache, before)
+    mla.mla_clear_device_flag(layer.ws)
+    out = torch.full_like(rows, 5.0)
+    layer.cache_read(cache, slots, out)
+    assert mla.mla_read_device_flag(layer.ws) == mla.MLA_FLAG_BAD_SLOT
+    assert (out == 5.0).all()
+
+
+ATTN = {
+    # name: (heads, block size, own lengths, prefix length)
+    "one_key": (16, 64, [1], 0),
+    "ragged": (16, 64, [1, 63, 64, 65, 127, 128, 129, 300], 0),
+    "long": (16, 64, [2111], 0),
+    "blocks_of_16": (16, 16, [5, 200, 131], 0),
+    "blocks_of_48": (16, 48, [1, 47, 49, 260], 0),
+    "blocks_of_192": (16, 192, [191, 193, 500], 0),
+    "blocks_of_24": (16, 24, [100, 30], 0),
+    "one_head": (1, 64, [77, 400], 0),
+    "24_heads": (24, 64, [300, 128, 1], 0),
+    "40_heads": (40, 64, [150, 257], 0),
+    "128_heads": (128, 64, [200, 65, 1], 0),
+    "many_short": (16, 64, [1 + (7 * i) % 90 for i in range(160)], 0),
+    "prefix_one_row": (16, 64, [0, 1, 70], 1),
+    "prefix_only": (16, 64, [0, 0, 0], 130),
+    "prefix": (16, 64, [0, 1, 5, 64, 100], 300),
+    "prefix_blocks_of_16": (16, 16, [3, 40], 77),
+    "prefix_24_heads": (24, 64, [10, 0, 129, 64, 64, 1, 2], 129),
+    "prefix_128_heads": (128, 64, [10, 0, 129], 190),
+    "prefix_5_heads": (5, 64, [i % 3 for i in range(67)], 64),
+    "prefix_long": (16, 64, [100, 7], 1500),
+    "prefix_odd_block": (8, 7, [20, 0, 9], 33),
+}
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("name", list(ATTN))
+def test_latent_attention(name, fp8):
+    heads, bs, lens, prefix = ATTN[name]
+    case = Case(shape_of(heads, bs), lens, prefix, fp8, seed=len(name))
+    layer = case.layer()
+    o, lse = layer.latent_attn(want_lse=True, **case.device_inputs())
+    torch.cuda.synchronize()
+    assert mla.mla_read_device_flag(layer.ws) == 0
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache32"])
+@pytest.mark.parametrize("name", ["ragged", "prefix", "prefix_odd_block"])
+def test_latent_attention_fp32(name, fp8):
+    heads, bs, lens, prefix = ATTN[name]
+    case = Case(shape_of(heads, bs, act="f32", r_kv=64, d_r=16), lens, prefix, fp8, seed=3)
+    layer = case.layer()
+    o, lse = layer.latent_attn(want_lse=True, **case.device_inputs())
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("name", ["ragged", "prefix", "prefix_only", "128_heads", "prefix_128_heads"])
+def test_attention_sink(name, fp8):
+    heads, bs, lens, prefix = ATTN[name]
+    case = Case(shape_of(heads, bs), lens, prefix, fp8, sink=True, seed=5)
+    o, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_sharp_scores(fp8, prefix):
+    # a few keys carry nearly everything, some of them late: the reference max moves by far
+    case = Case(shape_of(16, 64), [400, 129], prefix, fp8, seed=9)
+    for t in range(2):
+        s = case.key_slots(t)
+        for at in (5, len(s) // 2, len(s) - 1):
+            case.rows[s[at], :64] = case.q_abs[t, at % 16, :64] * 3
+    case.keys = row_values(case.shape, case.rows) if fp8 else case.rows.double().numpy()
+    o, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("prefix", [0, 2000])
+def test_one_heavy_key_among_many_light_ones(prefix):
+    # the first key has probability about 1/2, thousands of others share the rest
+    n = 4000
+    case = Case(shape_of(16, 64), [n - prefix], prefix, True, seed=2, q_size=0.05)
+    s = case.key_slots(0)
+    q = case.q_abs[0].double().mean(0)
+    case.q_abs[0] = q.bfloat16()[None].expand(16, -1) + case.q_abs[0] * 0.1
+    u = case.q_abs[0].double().mean(0)
+    case.rows[s[0], :512] = (u / u.norm() ** 2 * np.log(n) / case.scale).bfloat16()
+    case.keys = row_values(case.shape, case.rows)
+    o, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads,bs,prefix", [(16, 64, 0), (16, 64, 100), (128, 64, 100), (4, 24, 50)])
+def test_bad_lengths_and_blocks(heads, bs, prefix, fp8):
+    lens = [50, 90, 70, 20]
+    case = Case(shape_of(heads, bs), lens, prefix, fp8, seed=6)
+    layer = case.layer()
+    x = case.device_inputs()
+    x["context_lens"] = torch.tensor([50, -3, 70, 2 ** 30], dtype=torch.int32, device="cuda")
+    o, lse = layer.latent_attn(want_lse=True, **x)
+    assert mla.mla_read_device_flag(layer.ws) == mla.MLA_FLAG_BAD_CONTEXT
+    want = case.oracle()
+    for t in (1, 3):
+        want[0][t], want[1][t] = 0.0, -np.inf
+    check(case, o, lse, want)
+    mla.mla_clear_device_flag(layer.ws)
+    # a block id out of range: its rows are left out
+    x = case.device_inputs()
+    bad = case.table.copy()
+    for t, v in ((0, case.n_blocks), (2, -7)):
+        bad[t, 0] = v
+    x["block_table"] = torch.from_numpy(bad).cuda()
+    o, lse = layer.latent_attn(want_lse=True, **x)
+    assert mla.mla_read_device_flag(layer.ws) == mla.MLA_FLAG_BAD_BLOCK
+    slots = case.key_slots
+    case.key_slots = lambda t: np.delete(slots(t), np.arange(prefix, prefix + min(bs, lens[t]))) if t in (0, 2) else slots(t)
+    check(case, o, lse)
+
+
+def test_a_nan_row_stays_visible_and_a_zero_row_counts():
+    case = Case(shape_of(16, 64), [200, 200], 0, True, seed=1)
+    s = case.key_slots(0)
+    case.rows[s[150], 7] = float("nan")
+    case.rows[case.key_slots(1)[100], :512] = 0.0
+    case.keys = row_values(case.shape, case.rows)
+    o, _ = case.layer().latent_attn(**case.device_inputs())
+    assert torch.isnan(o[0]).all()
+    one = Case.__new__(Case)
+    one.__dict__.update(case.__dict__)
+    one.lens, one.q_abs, one.q_pe = [200], case.q_abs[1:], case.q_pe[1:]
+    one.table = case.table[1:]
+    check(one, o[1:], None)
+
+
+def test_rows_never_written_count_as_zero_rows():
+    shape = shape_of(16, 64)
+    layer = layer_of(shape, True)
+    cache = layer.new_cache(4)
+    q = torch.randn(1, 16, 512, device="cuda").bfloat16()
+    pe = torch.randn(1, 16, 64, device="cuda").bfloat16()
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    o, lse = layer.latent_attn(q, pe, cache, table, torch.tensor([100], dtype=torch.int32, device="cuda"), 100, want_lse=True)
+    assert (o == 0).all()
+    assert torch.allclose(lse, torch.full_like(lse, float(np.log(100.0))), atol=1e-5)
+
+
+# ---------------------------------------------------------------------------
+# the layer's own paths on an 8-bit cache
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["v2lite_bf16", "tiny_fp32", "v3_fp8"])
+def test_front_folds_write_what_cache_write_would(name):
+    w = wl.WORKLOADS[name]
+    shape = dataclasses.replace(w.shape, hidden=512 if name == "v3_fp8" else w.shape.hidden,
+                                n_heads=4, q_lora_rank=128 if name == "v3_fp8" else w.shape.q_lora_rank)
+    from head_latent_attention_decode_b200.layer import MlaLayer
+    weights = wl.make_weights(shape, 5)
+    plain, quant = MlaLayer(shape, weights), MlaLayer(shape, weights, cache_dtype="fp8")
+    n, act = 37, ACT[shape.act_dtype]
+    x = torch.randn(n, shape.hidden, device="cuda").to(act)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda") * 3
+    cos, sin = plain.rope(pos)
+    bs = shape.block_size
+    n_blocks = n // bs + 2
+    slots = torch.randperm(n_blocks * bs, device="cuda")[:n].int()
+    slots[4] = -1
+    rows16, got, want = plain.new_cache(n_blocks), quant.new_cache(n_blocks), quant.new_cache(n_blocks)
+    for call in ("decode", "noalloc", "prefill"):
+        for layer, cache in ((plain, rows16), (quant, got)):
+            cache.zero_()
+            if call == "decode":
+                layer.decode_qkv(x, cos, sin, cache, slots)
+            elif call == "noalloc":
+                q_abs = torch.empty((n, shape.n_heads, shape.kv_lora_rank), dtype=act, device="cuda")
+                q_pe = torch.empty((n, shape.n_heads, shape.qk_rope), dtype=act, device="cuda")
+                mla.mla_decode_qkv_noalloc(layer.handle, x, cos, sin, cache, slots, q_abs, q_pe)
+            else:
+                layer.prefill(x, cos, sin, kv_cache=cache, slot_mapping=slots)
+        want.zero_()
+        keep = slots >= 0
+        rows = rows16.reshape(n_blocks * bs, -1)[slots[keep].long()].contiguous()
+        quant.cache_write(rows, want, slots[keep].contiguous())
+        assert int((want != 0).sum()) > 0 and same_bytes(got, want), call
+    assert mla.mla_read_device_flag(quant.ws) == 0
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_serving_a_batch_over_a_shared_prompt(heads):
+    """Prefill a prompt into the 8-bit cache, read it back, decode a batch over it: the steps as a
+    server runs them, against the same steps with the values read back into a 16-bit cache."""
+    shape = dataclasses.replace(wl.V2LITE, hidden=512, n_heads=heads)
+    from head_latent_attention_decode_b200.layer import MlaLayer
+    weights = wl.make_weights(shape, 7)
+    quant, plain = MlaLayer(shape, weights, cache_dtype="fp8"), MlaLayer(shape, weights)
+    S, n, bs = 192, 5, 64
+    perm = torch.randperm(3 + n + 1, device="cuda").int()
+    ptable, own = perm[:3].contiguous(), perm[3:3 + n].view(n, 1).contiguous()
+    n_blocks = perm.numel()
+    cache = quant.new_cache(n_blocks)
+    x = torch.randn(S, shape.hidden, device="cuda").bfloat16()
+    cos, sin = quant.rope(torch.arange(S, dtype=torch.int32, device="cuda"))
+    p = torch.arange(S, device="cuda")
+    quant.prefill(x, cos, sin, kv_cache=cache, slot_mapping=(ptable[p // bs] * bs + p % bs).int())
+    for step in range(3):
+        h = torch.randn(n, shape.hidden, device="cuda").bfloat16()
+        cos, sin = quant.rope(torch.full((n,), S + step, dtype=torch.int32, device="cuda"))
+        q_abs, q_pe = quant.decode_qkv(h, cos, sin, cache, own[:, 0] * bs + step)
+        ctx = torch.full((n,), step + 1, dtype=torch.int32, device="cuda")
+        head = torch.empty((n, heads, shape.v_dim), dtype=torch.bfloat16, device="cuda")
+        out = quant.decode_attn_prefix(q_abs, q_pe, cache, ptable, S, own, ctx, step + 1, head_out=head)
+        # the whole context as one table per sequence, on both caches
+        table = torch.cat([ptable[None].expand(n, 3), own], 1).contiguous()
+        full = ctx + S
+        one = quant.decode_attn(q_abs, q_pe, cache, table, full, S + step + 1)
+        c16 = quant.cache_read(cache, torch.arange(n_blocks * bs, dtype=torch.int32, device="cuda"))
+        want = plain.decode_attn(q_abs, q_pe, c16.view(n_blocks, 1, bs, -1), table, full, S + step + 1)
+        scale = want.float().abs().max()
+        for y in (out, one):   # as the decode path's own parity bound: 2e-2 of the largest
+            assert ((y.float() - want.float()).abs().max() / scale) < 2e-2
+        pre16 = plain.decode_attn_prefix(q_abs, q_pe, c16.view(n_blocks, 1, bs, -1), ptable, S, own, ctx, step + 1)
+        assert ((pre16.float() - want.float()).abs().max() / scale) < 2e-2
+        assert torch.isfinite(head.float()).all()
+    for layer in (quant, plain):
+        assert mla.mla_read_device_flag(layer.ws) == 0
+
+
+def test_decode_attn_prefix_without_a_prefix_and_fp32():
+    case = Case(shape_of(4, 16, act="f32", r_kv=64, d_r=16), [30, 70], 0, False, seed=4)
+    layer = case.layer()
+    x = case.device_inputs()
+    a = layer.decode_attn(x["q_abs"], x["q_pe"], x["kv_cache"], x["block_table"], x["context_lens"], 70)
+    b = layer.decode_attn_prefix(x["q_abs"], x["q_pe"], x["kv_cache"], None, 0, x["block_table"], x["context_lens"], 70)
+    assert torch.allclose(a, b, rtol=1e-4, atol=1e-6)
+
+
+def test_host_step_on_an_8bit_cache():
+    shape = dataclasses.replace(wl.V2LITE, hidden=512)
+    from head_latent_attention_decode_b200.layer import MlaLayer
+    layer = MlaLayer(shape, wl.make_weights(shape, 3), cache_dtype="fp8")
+    n, ctx = 3, 90
+    cache = layer.new_cache(8)
+    rows = torch.randn(8 * 64, shape.kv_row_dim, device="cuda").bfloat16()
+    layer.cache_write(rows, cache, torch.arange(512, dtype=torch.int32, device="cuda"))
+    table = torch.tensor([[0, 3], [5, 1], [2, 7]], dtype=torch.int32)
+    lens = torch.full((n,), ctx, dtype=torch.int32)
+    slots = table[:, 1] * 64 + (ctx - 1) % 64
+    pos = lens - 1
+    h = torch.randn(n, shape.hidden).bfloat16()
+    ws = layer.workspace(n, ctx)
+    stage = torch.empty(mla.mla_decode_step_host_bytes(layer.handle, n, 2), dtype=torch.uint8, device="cuda")
+    out = torch.empty(n, shape.hidden).bfloat16()
+    c2 = cache.clone()
+    mla.mla_decode_step_host(layer.handle, h, pos, slots, table, lens, ctx, 10000.0, c2, out, stage, ws)
+    torch.cuda.synchronize()
+    cos, sin = layer.rope(pos.cuda())
+    q_abs, q_pe = layer.decode_qkv(h.cuda(), cos, sin, cache, slots.cuda())
+    want = layer.decode_attn(q_abs, q_pe, cache, table.cuda(), lens.cuda(), ctx)
+    assert same_bytes(cache, c2) and same_bytes(out, want)
+
+
+# ---------------------------------------------------------------------------
+# streams, graphs, workspaces, refusals
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_repeats_graphs_and_other_streams_give_the_same_bits(heads, fp8):
+    case = Case(shape_of(heads, 64), [1, 200, 64, 0], 150, fp8, seed=8)
+    layer = case.layer()
+    x = case.device_inputs()
+    want, wl_ = layer.latent_attn(want_lse=True, **x)
+    check(case, want, wl_)
+    for _ in range(3):
+        o, lse = layer.latent_attn(want_lse=True, **x)
+        assert same_bytes(o, want) and same_bytes(lse, wl_)
+    # a stream of its own with a workspace of its own, at the same time
+    other = case.layer()
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        outs.append(layer.latent_attn(**x)[0])
+        with torch.cuda.stream(st):
+            outs.append(other.latent_attn(**x)[0])
+    torch.cuda.synchronize()
+    assert all(same_bytes(o, want) for o in outs)
+    # two graphs that share a workspace, replayed in turn on changed inputs
+    outs, graphs = [torch.empty_like(want) for _ in range(2)], []
+    xs = [x, dict(x, q_abs=x["q_abs"].flip(0).contiguous(), q_pe=x["q_pe"].flip(0).contiguous(),
+                  context_lens=x["context_lens"].flip(0).contiguous(), block_table=x["block_table"].flip(0).contiguous())]
+    for y, o in zip(xs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.latent_attn(o_lat=o, **y)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert same_bytes(outs[0], want) and same_bytes(outs[1], want.flip(0).contiguous())
+    assert mla.mla_read_device_flag(layer.ws) == 0
+
+
+def test_cache_calls_in_a_graph():
+    shape = shape_of(16, 64)
+    layer = layer_of(shape, True)
+    cache = layer.new_cache(3)
+    rows = torch.randn(100, 576, device="cuda").bfloat16()
+    slots = torch.randperm(192, device="cuda")[:100].int()
+    out = torch.zeros_like(rows)
+    layer.workspace(1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.cache_write(rows, cache, slots)
+        layer.cache_read(cache, slots, out)
+    for seed in range(2):
+        rows.copy_(torch.randn_like(rows))
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.double().cpu().numpy(), row_values(shape, rows.cpu()))
+
+
+def test_refusals():
+    shape = shape_of(16, 64)
+    layer = layer_of(shape, True)
+    L = mla.lib()
+    h = layer.handle
+    assert L.mla_set_cache_dtype(h, 9) == mla.MLA_ERR_INVALID_ARG
+    assert L.mla_set_cache_dtype(h, mla.MLA_F32) == mla.MLA_ERR_UNSUPPORTED
+    assert mla.mla_prefix_workspace_bytes(h, 1, -1, 1) == 0 and mla.mla_prefix_workspace_bytes(h, 1, 2 ** 30, 1) == 0
+    case = Case(shape, [10, 20], 30, True, seed=0)
+    x = case.device_inputs()
+    ws = layer.prefix_workspace(2, 30, 20)
+    o = torch.empty_like(x["q_abs"])
+    kw = {k: v for k, v in x.items()}
+
+    def status(**change):
+        a = dict(kw, ws=ws, o_lat=o)
+        a.update(change)
+        with pytest.raises(mla.MlaError) as e:
+            mla.mla_latent_attn(h, **a)
+        return e.value.status
+
+    assert status(prefix_len=-1) == mla.MLA_ERR_INVALID_ARG
+    assert status(max_context_len=0) == mla.MLA_ERR_INVALID_ARG
+    assert status(ws=ws[:1024]) == mla.MLA_ERR_WORKSPACE
+    assert status(prefix_len=2 ** 30) == mla.MLA_ERR_UNSUPPORTED
+    odd = torch.empty(x["kv_cache"].numel() + 8, dtype=torch.uint8, device="cuda")[8:].view(x["kv_cache"].shape)
+    assert status(kv_cache=odd) == mla.MLA_ERR_INVALID_ARG
+    for bad in (dict(prefix_table=None), dict(q_pe=x["q_pe"][:1].contiguous()), dict(o_lat=o.float()),
+                dict(context_lens=x["context_lens"].long()), dict(q_abs=x["q_abs"].transpose(0, 1)),
+                dict(lse=torch.empty(2, 16, device="cuda").double()), dict(block_table=x["block_table"][:1].contiguous())):
+        with pytest.raises(ValueError):
+            mla.mla_latent_attn(h, **{**kw, "ws": ws, "o_lat": o, **bad})
+    rows = torch.zeros(2, 576, device="cuda").bfloat16()
+    slots = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        mla.mla_cache_write(h, rows, x["kv_cache"], slots[:1].contiguous(), ws)
+    with pytest.raises(ValueError):
+        layer.cache_write(rows.float(), x["kv_cache"], slots)
+    with pytest.raises(ValueError):
+        layer.cache_write(rows, x["kv_cache"][:, :-128].contiguous(), slots)
+    with pytest.raises(ValueError):
+        layer.latent_attn(**dict(x, prefix_len=65))
+    # nothing to do is no error
+    mla.mla_cache_write(h, rows[:0], x["kv_cache"], slots[:0], ws)
+    mla.mla_latent_attn(h, **dict(kw, q_abs=x["q_abs"][:0], q_pe=x["q_pe"][:0], block_table=x["block_table"][:0],
+                                  context_lens=x["context_lens"][:0]), ws=ws, o_lat=o[:0])
+
+
+def test_block_bytes():
+    for name, act in (("latent512", "bf16"), ("odd_block", "f32")):
+        shape = shape_of(4, act=act, **SHAPES[name])
+        _, _, size = lr.block_layout(shape.block_size, shape.kv_lora_rank, shape.qk_rope, ESZ[act])
+        assert mla.mla_cache_block_bytes(layer_of(shape, True).handle) == size
+        assert mla.mla_cache_block_bytes(layer_of(shape, False).handle) == shape.block_size * shape.kv_row_dim * ESZ[act]
