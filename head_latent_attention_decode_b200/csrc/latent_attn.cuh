@@ -16,6 +16,7 @@
 
 #include "handle.cuh"
 #include "simt_kernels.cuh"
+#include "tc_attn8.cuh"
 #include "tc_path.cuh"
 
 namespace mla {
@@ -161,26 +162,64 @@ struct LatentCall {
   int n;
 };
 
-struct LatentWs {
-  size_t o, ml, total;
-  int splits;
+// Which kernels a call takes, how many tokens at a time, and where their partials lie.
+struct LatentPlan {
+  int tc8;                 // the 8-bit tensor-core kernel
+  int chunk;               // tokens per pass
+  int splits;              // CUDA cores: splits of the keys
+  int NH, groups, units;   // tc8: rows per CTA, head groups and slices of the own pass
+  int NHp, ents_p, units_p;   // ... rows per entry, entries and slices of the prefix pass
+  size_t o, ml, seg, o_p, ml_p, seg_p, total;
 };
 
-static inline LatentWs latent_ws(const mla_handle* h, long long n, int prefix_len, int max_ctx) {
-  LatentWs w{};
-  const long long keys = (long long)prefix_len + max_ctx;
-  const long long c = cdiv(keys, 256);
-  w.splits = c < 2 ? 2 : (c > 16 ? 16 : (int)c);
+static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned) {
+  const mla_config& c = h->cfg;
+  const int H = c.n_heads;
+  const int sms = h->tc.num_sms > 0 ? h->tc.num_sms : 148;
+  LatentPlan w{};
   size_t off = 0;
   auto put = [&](size_t b) { size_t o = off; off = align_up(off + b, 256); return o; };
-  const long long rows = n * w.splits * h->cfg.n_heads;
-  w.o = put((size_t)rows * h->cfg.kv_lora_rank * 4);
-  w.ml = put((size_t)rows * 2 * 4);
+  // DeepSeek latent, blocks of a multiple of 16 rows (a TMA box is 16, 32 or 64 rows of one block)
+  w.tc8 = h->cache8 && h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64 && c.block_size % 16 == 0;
+  if (w.tc8) {
+    // the tile list of a pass is counted in int
+    const long long tiles = cdiv(max_ctx, 128), tiles_p = cdiv(prefix_len, 128);
+    long long most = A8_MAX_ENT;
+    if (tiles * most > (1 << 30)) most = (1 << 30) / tiles;
+    if (tiles_p > 0 && tiles_p * cdiv(most * H, 16) > (1 << 30)) most = (1 << 30) / tiles_p * 16 / H - 1;
+    w.chunk = (int)(n < most ? n : (most < 1 ? 1 : most));
+    w.NH = H <= 16 ? 16 : 32;
+    w.groups = (int)cdiv(H, w.NH);
+    w.units = sms / w.groups > 0 ? sms / w.groups : 1;
+    const size_t rows = (size_t)w.groups * (w.units + w.chunk) * w.NH;
+    w.o = put(rows * 512 * 4);
+    w.ml = put(rows * 2 * 4);
+    w.seg = put((size_t)w.chunk * 8);
+    if (prefix_len > 0) {
+      const long long q = (long long)w.chunk * H;
+      w.NHp = q <= 16 ? 16 : 32;
+      w.ents_p = (int)cdiv(q, w.NHp);
+      w.units_p = sms;
+      const size_t rows_p = (size_t)(w.units_p + w.ents_p) * w.NHp;
+      w.o_p = put(rows_p * 512 * 4);
+      w.ml_p = put(rows_p * 2 * 4);
+      w.seg_p = put((size_t)w.ents_p * 8);
+    }
+  } else {
+    w.chunk = (int)n;
+    const long long s = cdiv((long long)prefix_len + max_ctx, 256);
+    w.splits = s < 2 ? 2 : (s > 16 ? 16 : (int)s);
+    const size_t rows = (size_t)n * w.splits * H;
+    w.o = put(rows * c.kv_lora_rank * 4);
+    w.ml = put(rows * 2 * 4);
+  }
   w.total = off;
   return w;
 }
 static inline size_t latent_ws_bytes(const mla_handle* h, long long n, int prefix_len, int max_ctx) {
-  return latent_ws(h, n, prefix_len, max_ctx).total;
+  const size_t a = latent_plan(h, n, prefix_len, max_ctx, true).total;
+  const size_t b = latent_plan(h, n, prefix_len, max_ctx, false).total;
+  return a > b ? a : b;
 }
 
 static inline void launch_merge(const MergeArgs& m, int n, int most, int o_dt, cudaStream_t s) {
@@ -193,28 +232,96 @@ static inline void launch_merge(const MergeArgs& m, int n, int most, int o_dt, c
   mla_count_launch(1);
 }
 
-// o_lat [n, H, r_kv] (o_dt: 0 fp32, 1 bf16, 2 f16) and, if given, lse [n, H].
-static inline int latent_core(const mla_handle* h, const LatentCall& a, void* o_lat, int o_dt, float* lse, char* scratch,
-                              int* flag, cudaStream_t s) {
+// The 8-bit cache's planes as TMA sees them: the codes as {128 columns, 8 rows,
+// 4 column groups, octets of a block, blocks}, boxes of two column groups and
+// `box` rows; the rotary keys as {64, rows of a block, blocks}.
+static int make_maps_cache8(CUtensorMap* codes, CUtensorMap* rope, const void* base, const Cache8& c, long long n_blocks,
+                            int box) {
+  auto fn = encode_fn();
+  if (!fn) return MLA_ERR_CUDA;
+  cuuint64_t d5[5] = {128, 8, 4, (cuuint64_t)(c.bs / 8), (cuuint64_t)n_blocks};
+  cuuint64_t s5[4] = {512, 128, 4096, (cuuint64_t)c.block_bytes};
+  cuuint32_t b5[5] = {128, 8, 2, (cuuint32_t)(box / 8), 1}, e5[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), d5, s5, b5, e5,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return MLA_ERR_CUDA;
+  cuuint64_t d3[3] = {64, (cuuint64_t)c.bs, (cuuint64_t)n_blocks}, s3[2] = {128, (cuuint64_t)c.block_bytes};
+  cuuint32_t b3[3] = {64, (cuuint32_t)box, 1}, e3[3] = {1, 1, 1};
+  r = fn(rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (char*)const_cast<void*>(base) + c.pe_off, d3, s3, b3, e3,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
+}
+
+template <int NH>
+static void launch_attn8(const CUtensorMap& codes, const CUtensorMap& rope, const TcAttn8Args& a, cudaStream_t s) {
+  static std::atomic<bool> attr[64];
+  set_smem_once(attr, tc_attn8_kernel<NH>, Attn8Smem<NH>::SIZE);
+  launch_pdl(tc_attn8_kernel<NH>, (unsigned)(a.units * a.groups), Attn8Smem<NH>::THREADS, Attn8Smem<NH>::SIZE, s, codes,
+             rope, a);
+  mla_count_launch(1);
+}
+
+// One pass of at most plan.chunk tokens on the 8-bit tensor-core kernel.
+static int latent_pass8(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
+                        int* flag, cudaStream_t s) {
+  const mla_config& c = h->cfg;
+  const Cache8 c8 = cache8_of(h);
+  const int box = c.block_size % 64 == 0 ? 64 : (c.block_size % 32 == 0 ? 32 : 16);
+  CUtensorMap codes, rope;
+  const int st = make_maps_cache8(&codes, &rope, a.cache, c8, a.n_blocks > 0 ? a.n_blocks : 1, box);
+  if (st != MLA_OK) return st;
+  TcAttn8Args k{};
+  k.H = c.n_heads; k.rows_total = (long long)a.n * c.n_heads;
+  k.mbps = a.mbps; k.bs = c.block_size; k.box = box; k.n_blocks = a.n_blocks;
+  k.cache = (const uint8_t*)a.cache; k.block_bytes = c8.block_bytes; k.sc_off = c8.sc_off;
+  k.q_abs = (const bf16*)a.q_abs; k.q_pe = (const bf16*)a.q_pe;
+  k.scale_log2 = h->scale * 1.4426950408889634f;
+  k.flag = flag;
+  if (a.prefix_len > 0) {
+    TcAttn8Args p = k;
+    p.flat = 1; p.groups = 1; p.units = w.units_p;
+    p.n_ent = (int)cdiv(p.rows_total, w.NHp);
+    p.len = a.prefix_len; p.table = a.prefix_table;
+    p.part_o = (float*)(scratch + w.o_p); p.part_ml = (float*)(scratch + w.ml_p); p.seg = (int2*)(scratch + w.seg_p);
+    mla_timer_begin("attn_prefix", s);
+    if (w.NHp == 16) launch_attn8<16>(codes, rope, p, s);
+    else launch_attn8<32>(codes, rope, p, s);
+    mla_timer_end("attn_prefix", s);
+    MergeSrc& q = m->src[m->n_src++];
+    q.o = p.part_o; q.ml = p.part_ml; q.seg = p.seg; q.rows = w.NHp; q.flat = 1;
+  }
+  k.groups = w.groups; k.units = w.units; k.n_ent = a.n;
+  k.ctx = a.ctx; k.min_ctx = m->min_ctx; k.max_ctx = a.max_ctx;
+  k.table = a.table; k.table_stride = a.mbps;
+  k.part_o = (float*)(scratch + w.o); k.part_ml = (float*)(scratch + w.ml); k.seg = (int2*)(scratch + w.seg);
+  mla_timer_begin("attn", s);
+  if (w.NH == 16) launch_attn8<16>(codes, rope, k, s);
+  else launch_attn8<32>(codes, rope, k, s);
+  mla_timer_end("attn", s);
+  MergeSrc& q = m->src[m->n_src++];
+  q.o = k.part_o; q.ml = k.part_ml; q.seg = k.seg; q.rows = w.NH;
+  q.group_units = k.units + k.n_ent;
+  return MLA_OK;
+}
+
+// The same on CUDA cores (any shape, fp32 activations): the prefix rows simply
+// come first in every sequence's list of keys.
+static int latent_pass_simt(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
+                            int* flag, cudaStream_t s) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads, rkv = c.kv_lora_rank, dr = c.qk_rope, R = rkv + dr;
-  const LatentWs W = latent_ws(h, a.n, a.prefix_len, a.max_ctx);
-  MergeArgs m{};
-  m.H = H; m.r_kv = rkv;
-  m.sink = h->has_sink ? (const float*)(h->base + h->L.sink) : nullptr;
-  m.o = o_lat; m.lse = lse;
-  m.ctx = a.ctx; m.min_ctx = a.prefix_len > 0 ? 0 : 1; m.max_ctx = a.max_ctx;
-  m.cap = (long long)a.mbps * c.block_size;
   AttnArgs p{};
   p.q_abs = a.q_abs; p.q_pe = a.q_pe; p.cache = a.cache; p.n_blocks = a.n_blocks; p.bs = c.block_size;
   p.block_table = a.table; p.mbps = a.mbps; p.ctx = a.ctx; p.max_ctx = a.max_ctx;
   p.H = H; p.r_kv = rkv; p.d_r = dr; p.layout = c.row_layout; p.scale = h->scale;
-  p.n_splits = W.splits;
-  p.chunk = (int)(cdiv(cdiv((long long)a.prefix_len + a.max_ctx, W.splits), ATT_TR) * ATT_TR);
-  p.part_o = (float*)(scratch + W.o); p.part_ml = (float*)(scratch + W.ml); p.flag = flag;
+  p.n_splits = w.splits;
+  p.chunk = (int)(cdiv(cdiv((long long)a.prefix_len + a.max_ctx, w.splits), ATT_TR) * ATT_TR);
+  p.part_o = (float*)(scratch + w.o); p.part_ml = (float*)(scratch + w.ml); p.flag = flag;
   p.prefix_table = a.prefix_table; p.prefix_len = a.prefix_len; p.c8 = cache8_of(h);
   const size_t smem = (size_t)(ATT_TR * (R + 1) + ATT_HPB * R) * 4;
-  const dim3 grid(W.splits, a.n, (unsigned)cdiv(H, ATT_HPB));
+  const dim3 grid(w.splits, a.n, (unsigned)cdiv(H, ATT_HPB));
   mla_timer_begin("attn", s);
   if (c.act_dtype == MLA_F32) {
     cudaFuncSetAttribute(attn_decode_simt_kernel<float, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -225,9 +332,42 @@ static inline int latent_core(const mla_handle* h, const LatentCall& a, void* o_
   }
   mla_timer_end("attn", s);
   mla_count_launch(1);
-  MergeSrc& q = m.src[0];
-  q.o = p.part_o; q.ml = p.part_ml; q.splits = W.splits; q.rows = H;
-  m.n_src = 1;
-  launch_merge(m, a.n, W.splits, o_dt, s);
+  MergeSrc& q = m->src[m->n_src++];
+  q.o = p.part_o; q.ml = p.part_ml; q.splits = w.splits; q.rows = H;
+  return MLA_OK;
+}
+
+// o_lat [n, H, r_kv] (o_dt: 0 fp32, 1 bf16, 2 f16) and, if given, lse [n, H].
+static inline int latent_core(const mla_handle* h, const LatentCall& call, void* o_lat, int o_dt, float* lse,
+                              char* scratch, int* flag, cudaStream_t s) {
+  const mla_config& c = h->cfg;
+  const int H = c.n_heads, rkv = c.kv_lora_rank, dr = c.qk_rope;
+  const size_t esz = c.act_dtype == MLA_F32 ? 4 : 2, o_esz = o_dt == 0 ? 4 : 2;
+  const bool aligned = (((uintptr_t)call.q_abs | (uintptr_t)call.q_pe) & 15) == 0;
+  const LatentPlan w = latent_plan(h, call.n, call.prefix_len, call.max_ctx, aligned);
+  for (int t = 0; t < call.n; t += w.chunk) {
+    LatentCall a = call;
+    a.n = call.n - t < w.chunk ? call.n - t : w.chunk;
+    a.q_abs = (const char*)call.q_abs + (size_t)t * H * rkv * esz;
+    a.q_pe = (const char*)call.q_pe + (size_t)t * H * dr * esz;
+    a.table = call.table + (size_t)t * call.mbps;
+    a.ctx = call.ctx + t;
+    MergeArgs m{};
+    m.H = H; m.r_kv = rkv;
+    m.sink = h->has_sink ? (const float*)(h->base + h->L.sink) : nullptr;
+    m.o = (char*)o_lat + (size_t)t * H * rkv * o_esz;
+    m.lse = lse ? lse + (size_t)t * H : nullptr;
+    m.ctx = a.ctx; m.min_ctx = a.prefix_len > 0 ? 0 : 1; m.max_ctx = a.max_ctx;
+    m.cap = (long long)a.mbps * c.block_size;
+    const int st = w.tc8 ? latent_pass8(h, w, a, &m, scratch, flag, s) : latent_pass_simt(h, w, a, &m, scratch, flag, s);
+    if (st != MLA_OK) return st;
+    int most = w.splits;   // split partials of one query row, about
+    if (w.tc8) {
+      const long long own = cdiv(a.max_ctx, 128), pre = cdiv(a.prefix_len, 128);
+      most = (int)((own < cdiv(w.units, a.n) + 1 ? own : cdiv(w.units, a.n) + 1) +
+                   (pre < cdiv(w.units_p, w.ents_p ? w.ents_p : 1) + 1 ? pre : cdiv(w.units_p, w.ents_p ? w.ents_p : 1) + 1));
+    }
+    launch_merge(m, a.n, most, o_dt, s);
+  }
   return MLA_OK;
 }

@@ -1,0 +1,670 @@
+// Latent attention over the 8-bit cache on tcgen05, for the DeepSeek latent
+// (kv_lora_rank 512, qk_rope 64) and blocks of a multiple of 16 rows. The E4M3
+// codes go to the tensor cores as they are (kind::f8f6f4); no value is ever
+// widened in shared memory.
+//
+// The other operand of each product would lose accuracy in E4M3, so it is split
+// in two E4M3 parts, x = hi + lo with hi = e4m3(x) and lo = e4m3(x - hi): two 4-bit
+// significands carry the 8 bits of a bf16 value, and both parts ride in one MMA
+// as extra columns (N = 2 NH). A small-N MMA costs its issue whatever N is, so
+// the second part is free.
+//   q_abs_h = 2^k_h (hi + lo): k_h brings the row's largest to at most 448; columns
+//     within 2^-10 of it are exact, smaller ones off by at most 2^-18 of it
+//   p: per head and tile of 128 keys, relative to that tile's own largest
+//     weight, so that no key underflows because of a heavier one elsewhere: a
+//     weight is off by 2^-8 of itself or 2^-18 of the tile's largest
+//
+// The row scale s_j = 2^k_j folds into both products: with u_hj = q_h . code_j,
+//   y_hj = scale log2(e) (s_j u_hj + q_pe_h . k_pe_j) + k_j
+//   w_hj = 2^(y_hj - m_h + 8) in [0, 256],  m_h = max over the tile's keys of y_hj
+//   O_h  = sum_j w_hj code_j  (= 2^(8 - m_h) sum_j p_hj s_j code_j)
+//   l_h  = sum_j w_hj 2^-k_j
+//
+// Transposed tiles as in the 16-bit few-head kernel: 128 cache rows fill the
+// MMA's M. One CTA takes whole rows (an 8-bit tile is 64 KB of codes and 16 KB
+// of rotary keys, so nothing has to be exchanged between CTAs):
+//   U^T [128 keys x (hi | lo)] = codes . Q^T          16 MMAs, M 128 x N 2 NH x K 32
+//   R^T [128 keys x NH]        = k_pe . q_pe^T (bf16)  4 MMAs, M 128 x N NH x K 16
+//   O^T [128 latent x (hi | lo)] x 4 = codes^T . W^T  16 MMAs; codes^T is the same
+//                                                     shared-memory tile read MN-major
+// O^T leaves TMEM after every tile and is accumulated in registers (64 per
+// thread), where the change of reference is one multiply; so TMEM holds no
+// running state, and a tile's reference is free to go down as well as up.
+//
+// Roles: warpgroup g of NH / 16 runs the softmax of heads [16 g, 16 g + 16)
+// (thread <-> key) and accumulates their O^T (thread <-> latent column); then
+// one warp each for TMA, the score MMAs and the value MMAs. S and W alternate
+// between two buffers, so the scores of tile i + 1 run during the softmax of
+// tile i and its value MMAs during the softmax of tile i + 1.
+//
+// Schedule: the tiles of all entries (sequences; or blocks of NH query rows
+// against one shared prefix) form one list, and each CTA takes an equal
+// slice. More than 32 heads: `groups` CTAs, each with 32 heads, walk the same
+// slice at the same time, so the rows come from HBM once and from L2 after.
+#pragma once
+
+#include "cache8.cuh"
+#include "tc_common.cuh"
+
+namespace mla {
+namespace tc {
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+      "[%2];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+// D(tmem) (+)= A * B^T, E4M3 in, fp32 accumulation, K 32.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// kind::f8f6f4: fp32 accumulator, A and B E4M3 (format 0).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major = 0) {
+  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+struct TcAttn8Args {
+  int n_ent, groups, units;   // entries; head groups; slices (grid = units x groups)
+  int flat;                   // 0: entry e is sequence e, its rows e H + NH group ..; 1: query rows e NH .. against one table
+  int H;                      // query rows per sequence (flat = 0)
+  long long rows_total;       // query rows in all
+  const int* ctx;             // lengths (flat = 0)
+  int len, min_ctx, max_ctx;  // length (flat = 1); the valid lengths
+  const int* table;           // block ids; row e at table + e * table_stride
+  long long table_stride;
+  int mbps, bs, box, n_blocks;
+  const uint8_t* cache;
+  long long block_bytes, sc_off;
+  const bf16* q_abs;          // [rows_total, 512]
+  const bf16* q_pe;           // [rows_total, 64]
+  float scale_log2;
+  float* part_o;              // [groups][units + n_ent][NH][512]: unit c + e of group g
+  float* part_ml;             // the same [..][NH][2]
+  int2* seg;                  // [n_ent]: {first slice, slices} of each entry
+  int* flag;
+};
+
+constexpr int A8_MAX_ENT = 1024;   // sequences per launch (their tile prefix in shared memory)
+
+template <int NH>
+struct Attn8Smem {
+  static constexpr int NWG = NH / 16;
+  static constexpr int NPR = NH == 16 ? 5 : 4;   // ring entries of 32 KB: two per tile
+  static constexpr int QB = 2 * NH * 128;         // one k-block [2 NH x 128 B] of Q
+  static constexpr int PB = 2 * NH * 128;         // one buffer of W^T [2 NH x 128 keys]
+  static constexpr int RING_OFF = 0;              // entry: [16 row octets][2 k-blocks][8 rows][128 B]
+  static constexpr int ROPE_OFF = NPR * 32768;    // 2 x [128 x 64] bf16
+  static constexpr int Q_OFF = ROPE_OFF + 2 * 16384;
+  static constexpr int QPE_OFF = Q_OFF + 4 * QB;
+  static constexpr int P_OFF = QPE_OFF + NH * 128;
+  static constexpr int RED_OFF = P_OFF + 2 * PB;  // per warpgroup: maxima [2][4][16], row sums [4][16],
+                                                  // each warp's copy of the tile maxima [4][3][16], q scale [16]
+  static constexpr int RED_WG = 128 + 64 + 192 + 16;
+  static constexpr int PREF_OFF = RED_OFF + NWG * RED_WG * 4;
+  static constexpr int BAR_OFF = PREF_OFF + (A8_MAX_ENT + 4) * 4;
+  static constexpr int SIZE = 1024 + BAR_OFF + 512;
+  static constexpr int THREADS = NWG * 128 + 96;
+  // TMEM: S buffers [hi NH | lo NH | rotary NH], then O^T of the four latent groups [hi NH | lo NH]
+  static constexpr int SB = NH == 16 ? 64 : 128;
+  static constexpr int NOB = NH == 16 ? 2 : 1;    // O^T buffers
+  static constexpr int TM_O = 2 * SB;
+  static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
+  static_assert(TM_O + NOB * 8 * NH <= 512, "tensor memory");
+  static_assert(BAR_OFF % 8 == 0 && P_OFF % 1024 == 0, "alignment");
+};
+
+__device__ __forceinline__ int a8_len(const TcAttn8Args& a, int e) {
+  if (a.flat) return a.len;
+  const int L = a.ctx[e];
+  return (L < a.min_ctx || L > a.max_ctx || (long long)L > (long long)a.mbps * a.bs) ? 0 : L;
+}
+
+// Walks a slice of the tile list: entry e, its tile lt, its length.
+struct Walk8 {
+  const int* pref;   // tiles before entry e (shared memory), or NULL: e * T
+  int T, n, e, lt, len;
+  __device__ __forceinline__ int at(int i) const { return pref ? pref[i] : i * T; }
+  __device__ __forceinline__ void start(const TcAttn8Args& a, int g) {
+    if (pref) {
+      int lo = 0, hi = n - 1;   // the last entry that begins at or before g and is not empty there
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pref[mid] <= g) lo = mid;
+        else hi = mid - 1;
+      }
+      e = lo;
+    } else {
+      e = g / T;
+    }
+    lt = g - at(e);
+    len = a8_len(a, e);
+  }
+  __device__ __forceinline__ bool seg_last() const { return at(e) + lt + 1 == at(e + 1); }
+  __device__ __forceinline__ void next(const TcAttn8Args& a) {
+    if (!seg_last()) { ++lt; return; }
+    ++e;
+    while (e < n && at(e + 1) == at(e)) ++e;
+    lt = 0;
+    len = e < n ? a8_len(a, e) : 0;
+  }
+};
+
+template <int NH>
+__global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
+    tc_attn8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
+                    TcAttn8Args a) {
+  using SM = Attn8Smem<NH>;
+  griddep_wait();   // the inputs all come from the stream's earlier kernels
+  constexpr int NPR = SM::NPR, NWG = SM::NWG, NOB = SM::NOB;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t ring_s = sbase + SM::RING_OFF, rope_s = sbase + SM::ROPE_OFF, q_s = sbase + SM::Q_OFF,
+                 qpe_s = sbase + SM::QPE_OFF, p_s = sbase + SM::P_OFF;
+  int* pref = (int*)(smem + SM::PREF_OFF);
+  const uint32_t bar = sbase + SM::BAR_OFF;
+  const uint32_t full_b = bar, empty_b = full_b + 8 * NPR;       // [NPR] ring entry landed / consumed
+  const uint32_t rfull = empty_b + 8 * NPR, rempty = rfull + 16;  // [2] rotary block landed / consumed
+  const uint32_t s_full = rempty + 16, s_free = s_full + 16;      // [2] scores complete / read
+  const uint32_t p_full = s_free + 16, p_free = p_full + 16;      // [2] weights written / consumed
+  const uint32_t o_full = p_free + 16, o_free = o_full + 16;      // [NOB] O^T complete / read
+  const uint32_t q_ready = o_free + 16;                           // the next entry's query is in shared memory
+  const uint32_t fin_s = q_ready + 8, fin_o = fin_s + 8;
+  const uint32_t wg_b = fin_o + 8;                                // per warpgroup: red[2], query scales, row sums
+  uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 480);
+  volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 484);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x / a.groups, hg = blockIdx.x % a.groups;
+
+  // ---- the schedule ----
+  const int T_flat = a.flat ? (a.len + 127) / 128 : 0;
+  if (!a.flat && warp == 0) {
+    const int each = (a.n_ent + 31) / 32;   // n_ent <= A8_MAX_ENT
+    int sum = 0;
+    for (int k = 0; k < each; ++k) {
+      const int e = each * lane + k;
+      if (e >= a.n_ent) break;
+      const int L = a8_len(a, e);
+      if (blockIdx.x == 0 && (L == 0 && (a.min_ctx > 0 || a.ctx[e] != 0))) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
+      pref[e] = sum;
+      sum += (L + 127) / 128;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    for (int k = 0; k < each; ++k)
+      if (each * lane + k < a.n_ent) pref[each * lane + k] += incl - sum;
+    if (lane == 31) pref[a.n_ent] = incl;
+  }
+  __syncthreads();
+  Walk8 w0{a.flat ? nullptr : pref, T_flat, a.n_ent, 0, 0, 0};
+  const int total = w0.at(a.n_ent);
+  const int per = max(1, (total + a.units - 1) / a.units);
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < a.n_ent; e += blockDim.x) {
+      const int b0 = w0.at(e), b1 = w0.at(e + 1);
+      a.seg[e] = b1 > b0 ? make_int2(b0 / per, (b1 - 1) / per - b0 / per + 1) : make_int2(0, 0);
+    }
+  const long long g0l = (long long)c * per;
+  if (g0l >= total) return;
+  const int g0 = (int)g0l, N = min(total - g0, per);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NPR; ++i) { mbar_init(full_b + 8 * i, 1); mbar_init(empty_b + 8 * i, 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(rfull + 8 * i, 1);
+      mbar_init(rempty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_free + 8 * i, 4 * NWG);
+      mbar_init(p_full + 8 * i, 4 * NWG);
+      mbar_init(p_free + 8 * i, 1);
+      mbar_init(o_full + 8 * i, 1);
+      mbar_init(o_free + 8 * i, 4 * NWG);
+    }
+    mbar_init(q_ready, 4 * NWG);
+    mbar_init(fin_s, 1);
+    mbar_init(fin_o, 1);
+    for (int i = 0; i < 4 * NWG; ++i) mbar_init(wg_b + 8 * i, 4);
+    *abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) { tmem_alloc(smem_u32(tmem_slot), 512); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) griddep_launch_dependents();
+
+  if (warp == 4 * NWG) {
+    // ---------------- TMA: lane k < 128 / box brings rows [box k, box k + box) of each tile ----------------
+    if (lane == 0) {
+      prefetch_tmap(&tm_codes);
+      prefetch_tmap(&tm_rope);
+    }
+    const int nb = 128 / a.box, none = max(a.n_blocks, 1);   // a block id beyond the map
+    Walk8 w = w0;
+    w.start(a, g0);
+    // this lane's box of the walk's tile: its block id (out of range: the load fills zeros)
+    auto box_block = [&](const Walk8& v) {
+      const int j = 128 * v.lt + a.box * lane;
+      if (lane >= nb || j >= v.len) return none;
+      const int b = a.table[v.e * a.table_stride + j / a.bs];
+      if (b >= 0 && b < a.n_blocks) return b;
+      if (hg == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
+      return none;
+    };
+    int blk = box_block(w), i = 0;
+    bool ok = true;
+    for (; i < N; ++i) {
+      const int j = 128 * w.lt + a.box * lane;
+      const int off = j % a.bs, cur = blk;
+      if (i + 1 < N) {
+        w.next(a);
+        blk = box_block(w);   // one tile ahead
+      }
+      if (!mbar_wait_warp(rempty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
+      if (lane == 0) mbar_arrive_expect_tx(rfull + 8 * (i & 1), 16384);
+      __syncwarp();
+      if (lane < nb) tma_load_3d(rope_s + (i & 1) * 16384 + a.box * lane * 128, &tm_rope, rfull + 8 * (i & 1), 0, off, cur);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int e = 2 * i + g, slot = e % NPR;
+        if (!mbar_wait_warp(empty_b + 8 * slot, ((e / NPR) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
+        if (lane == 0) mbar_arrive_expect_tx(full_b + 8 * slot, 32768);
+        __syncwarp();
+        if (lane < nb)
+          tma_load_5d(ring_s + slot * 32768 + (a.box * lane / 8) * 2048, &tm_codes, full_b + 8 * slot, 0, 0, 2 * g,
+                      off / 8, cur);
+      }
+      if (!ok) break;
+    }
+    // drain what is in flight. When a wait gave up, tile i may lack some of its loads, and its
+    // barriers are left alone: the earlier entries' phases have completed or will
+    if (lane == 0 && i > 0) {
+      for (int u = (2 * i > NPR ? 2 * i - NPR : 0); u < 2 * i; ++u) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(full_b + 8 * (u % NPR), (u / NPR) & 1))
+          if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+      }
+      for (int u = (i > 2 ? i - 2 : 0); u < i; ++u) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(rfull + 8 * (u & 1), (u >> 1) & 1))
+          if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+      }
+    }
+    if (!ok && lane == 0) {   // loads of the unfinished tile: let them land before the CTA leaves
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 1000000ull) {}
+    }
+  } else if (warp == 4 * NWG + 1) {
+    // ---------------- score MMAs ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_u = idesc_e4m3(128, 2 * NH), id_r = idesc_bf16(128, NH);
+      const uint64_t d_ring = sdesc_sw128_sbo(ring_s, 2048), d_rope = sdesc_sw128(rope_s);
+      const uint64_t d_q = sdesc_sw128(q_s), d_qpe = sdesc_sw128(qpe_s);
+      Walk8 w = w0;
+      w.start(a, g0);
+      int ks = 0;
+      for (int i = 0; i < N; ++i) {
+        const int b = i & 1;
+        const bool first = i == 0 || w.lt == 0;
+        if ((first && !mbar_wait(q_ready, ks & 1, abort_word, a.flag)) ||
+            !mbar_wait(s_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag) ||
+            !mbar_wait(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag))
+          break;
+        if (first) ++ks;
+        tc_fence_after();
+        const uint32_t d = tmem + SM::SB * b;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16(d + 2 * NH, d_rope + (b * 16384 + 32 * k) / 16, d_qpe + 2 * k, id_r, k > 0 ? 1u : 0u);
+        mma_commit(rempty + 8 * b);
+        bool ok = true;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int e = 2 * i + g, slot = e % NPR;
+          if (!mbar_wait(full_b + 8 * slot, (e / NPR) & 1, abort_word, a.flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t da = d_ring + (uint64_t)(slot * (32768 / 16));
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f8(d, da + (kk * 1024 + 32 * k) / 16, d_q + ((2 * g + kk) * SM::QB + 32 * k) / 16, id_u,
+                     (g > 0 || kk > 0 || k > 0) ? 1u : 0u);
+        }
+        if (!ok) break;
+        mma_commit(s_full + 8 * b);
+        if (i + 1 < N) w.next(a);
+      }
+      mma_commit(fin_s);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(fin_s, 0))
+        if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+    }
+  } else if (warp == 4 * NWG + 2) {
+    // ---------------- value MMAs ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_o = idesc_e4m3(128, 2 * NH, 1);
+      // codes^T: one 128-column group along M, 8-key octets 2048 B apart along K
+      const uint64_t d_v = sdesc_sw128_mn_sbo(ring_s, 1024, 2048), d_p = sdesc_sw128(p_s);
+      for (int i = 0; i < N; ++i) {
+        const int b = i & 1, ob = i % NOB;
+        if (!mbar_wait(p_full + 8 * b, (i >> 1) & 1, abort_word, a.flag) ||
+            !mbar_wait(o_free + 8 * ob, ((i / NOB) & 1) ^ 1, abort_word, a.flag))
+          break;
+        tc_fence_after();
+        const uint64_t dp = d_p + (uint64_t)(b * (SM::PB / 16));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int slot = (2 * i + g) % NPR;
+          const uint64_t dv = d_v + (uint64_t)(slot * (32768 / 16));
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f8(tmem + SM::TM_O + ob * 8 * NH + (2 * g + kk) * 2 * NH, dv + (kk * 1024 + 8192 * k) / 16,
+                     dp + 2 * k, id_o, k > 0 ? 1u : 0u);
+          mma_commit(empty_b + 8 * slot);
+        }
+        mma_commit(o_full + 8 * ob);
+        mma_commit(p_free + 8 * b);
+      }
+      mma_commit(fin_o);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(fin_o, 0))
+        if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+    }
+  } else {
+    // ---------------- softmax and accumulation: thread <-> key of the tile, then <-> latent column ----------------
+    const int wg = warp >> 2, q = warp & 3;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    float* red = (float*)(smem + SM::RED_OFF) + wg * SM::RED_WG;   // [2][4][16]
+    float* rl = red + 128;                                         // [4][16]
+    float* mt = rl + 64 + 48 * q;                                  // [3][16], this warp's
+    float* slq = rl + 64 + 192;                                         // [16] scale log2(e) 2^k_h
+    const uint32_t red_b = wg_b + 32 * wg, qs_b = red_b + 16, l_b = qs_b + 8;
+    int kq = 0, kl = 0;   // phases of qs_b and l_b
+
+    // The 16 heads' query rows of entry e in two E4M3 parts: eight threads per head, 64 columns each.
+    auto load_q = [&](int e) -> bool {
+      const int hh = row >> 3, sub = row & 7, hd = 16 * wg + hh;
+      const long long r0 = a.flat ? (long long)e * NH : (long long)e * a.H + (long long)hg * NH;
+      const bool live = a.flat ? r0 + hd < a.rows_total : hg * NH + hd < a.H;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (live ? r0 + hd : 0) * 512 + 64 * sub);
+      uint4 v[8];
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
+      const uint4 pe = live ? reinterpret_cast<const uint4*>(a.q_pe + (r0 + hd) * 64)[sub] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          m = fmaxf(m, fmaxf(finite_abs(__uint_as_float(u[j] << 16)), finite_abs(__uint_as_float(u[j] & 0xFFFF0000u))));
+      }
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // as a cache row's exponent, over bf16's whole range
+      int k = 0;
+      if (m > 0.f) {
+        const uint32_t mb = __float_as_uint(m);
+        k = (int)(mb >> 23) - 127 - ((mb & 0x7FFFFFu) > 0x600000u ? 7 : 8);
+        k = max(-110, min(119, k));
+      }
+      const float inv = exp2_int(-k);
+      if (sub == 0) slq[hh] = a.scale_log2 * exp2_int(k);
+      uint8_t* qb = smem + SM::Q_OFF + (sub >> 1) * SM::QB;   // columns [128 j, 128 j + 128) are k-block j
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 vv = v[2 * ch + (j >> 1)];
+          const uint32_t u0 = (j & 1) ? vv.z : vv.x, u1 = (j & 1) ? vv.w : vv.y;
+          const float f0 = nan_if_inf(__uint_as_float(u0 << 16)) * inv, f1 = nan_if_inf(__uint_as_float(u0 & 0xFFFF0000u)) * inv;
+          const float f2 = nan_if_inf(__uint_as_float(u1 << 16)) * inv, f3 = nan_if_inf(__uint_as_float(u1 & 0xFFFF0000u)) * inv;
+          const uint16_t a0 = e4m3x2_sat(f0, f1), a1 = e4m3x2_sat(f2, f3);
+          const float2 g0v = e4m3x2_f32(a0), g1v = e4m3x2_f32(a1);
+          hi[j] = (uint32_t)a0 | ((uint32_t)a1 << 16);
+          lo[j] = (uint32_t)e4m3x2_sat(f0 - g0v.x, f1 - g0v.y) | ((uint32_t)e4m3x2_sat(f2 - g1v.x, f3 - g1v.y) << 16);
+        }
+        const int chunk = ((sub & 1) * 4 + ch) ^ (hd & 7);
+        *reinterpret_cast<uint4*>(qb + hd * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(qb + (NH + hd) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      *reinterpret_cast<uint4*>(smem + SM::QPE_OFF + hd * 128 + 16 * (sub ^ (hd & 7))) = pe;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(q_ready); mbar_arrive(qs_b); }
+      return mbar_wait_warp(qs_b, (kq++) & 1, abort_word, a.flag);   // the scales are there for every warp
+    };
+    // this thread's key in the walk's tile: block id (-1: no key), then its row scale
+    auto row_block = [&](const Walk8& v) {
+      const int j = 128 * v.lt + row;
+      if (v.e >= v.n || j >= v.len) return -1;
+      const int b = a.table[v.e * a.table_stride + j / a.bs];
+      return b >= 0 && b < a.n_blocks ? b : -1;
+    };
+    auto row_scale = [&](const Walk8& v, int b) {
+      return b < 0 ? 0.f
+                   : reinterpret_cast<const float*>(a.cache + (long long)b * a.block_bytes + a.sc_off)[(128 * v.lt + row) % a.bs];
+    };
+
+    float O[64], M[16], l[16], lt[16];
+#pragma unroll
+    for (int h = 0; h < 64; ++h) O[h] = 0.f;
+#pragma unroll
+    for (int h = 0; h < 16; ++h) { M[h] = -INFINITY; l[h] = 0.f; lt[h] = 0.f; }
+    // O += O^T(i) out of TMEM, both moved to the reference max(M, m(i)); the row sums likewise
+    auto accumulate = [&](int i) -> bool {
+      const int ob = i % NOB;
+      float al[16], f[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 m4 = *reinterpret_cast<const float4*>(mt + 16 * (i % 3) + 4 * k);
+        const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int h = 4 * k + j;
+          const float mn = fmaxf(M[h], mv[j]);
+          al[h] = M[h] == -INFINITY ? 0.f : ex2_approx(M[h] - mn);
+          f[h] = mv[j] == -INFINITY ? 0.f : ex2_approx(mv[j] - mn);
+          M[h] = mn;
+          l[h] = l[h] * al[h] + lt[h] * f[h];
+        }
+      }
+      if (!mbar_wait_warp(o_full + 8 * ob, (i / NOB) & 1, abort_word, a.flag)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint32_t hi[16], lo[16];
+        const uint32_t oa = tmem + SM::TM_O + ob * 8 * NH + g * 2 * NH + 16 * wg + lane_base;
+        tmem_ld16(oa, hi);
+        tmem_ld16(oa + NH, lo);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 16; ++h)
+          O[16 * g + h] = fmaf(f[h], __uint_as_float(hi[h]) + __uint_as_float(lo[h]), O[16 * g + h] * al[h]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free + 8 * ob);
+      return true;
+    };
+
+    Walk8 w = w0;
+    w.start(a, g0);
+    Walk8 w1 = w;             // one tile ahead: its row scale is in flight; block ids run two ahead
+    w1.next(a);
+    const int blk0 = row_block(w);
+    int blk1 = N > 1 ? row_block(w1) : -1;
+    float s_next = row_scale(w, blk0);
+    bool valid_next = blk0 >= 0, ok = load_q(w.e), pending = false;
+    for (int i = 0; i < N && ok; ++i) {
+      const int b = i & 1;
+      const float sj = s_next;
+      const bool valid = valid_next;
+      const int e = w.e;
+      const bool last = i == N - 1 || w.seg_last();
+      if (i + 1 < N) {
+        s_next = row_scale(w1, blk1);
+        valid_next = blk1 >= 0;
+        w = w1;
+        w1.next(a);
+        blk1 = i + 2 < N ? row_block(w1) : -1;
+      }
+      // 2^k_j; rows never written (scale 0) count as zero rows
+      const int kj = max(C8_KMIN, min(C8_KMAX, (int)(__float_as_uint(sj) >> 23) - 127));
+      if (!mbar_wait_warp(s_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      tc_fence_after();
+      float y[16];
+      {
+        uint32_t hi[16], lo[16], rp[16];
+        const uint32_t sa = tmem + SM::SB * b + 16 * wg + lane_base;
+        tmem_ld16(sa, hi);
+        tmem_ld16(sa + NH, lo);
+        tmem_ld16(sa + 2 * NH, rp);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free + 8 * b);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 s4 = *reinterpret_cast<const float4*>(slq + 4 * k);
+          const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int h = 4 * k + j;
+            const float u = __uint_as_float(hi[h]) + __uint_as_float(lo[h]);
+            const float r = fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj);
+            y[h] = valid ? fmaf(u, sj * sv[j], r) : -INFINITY;
+          }
+        }
+      }
+      // the tile's largest per head: within the warp, then over the warpgroup's four
+      float mx[16];
+#pragma unroll
+      for (int h = 0; h < 16; ++h) mx[h] = warp_max_f32(y[h]);
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float4*>(red + (b * 4 + q) * 16 + 4 * k) =
+              make_float4(mx[4 * k], mx[4 * k + 1], mx[4 * k + 2], mx[4 * k + 3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(red_b + 8 * b);
+      if (!mbar_wait_warp(red_b + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 m4 = *reinterpret_cast<const float4*>(red + b * 64 + 4 * k);
+#pragma unroll
+        for (int o = 1; o < 4; ++o) {
+          const float4 n4 = *reinterpret_cast<const float4*>(red + (b * 4 + o) * 16 + 4 * k);
+          m4.x = fmaxf(m4.x, n4.x); m4.y = fmaxf(m4.y, n4.y); m4.z = fmaxf(m4.z, n4.z); m4.w = fmaxf(m4.w, n4.w);
+        }
+        if (lane == 0) *reinterpret_cast<float4*>(mt + 16 * (i % 3) + 4 * k) = m4;
+        mx[4 * k] = m4.x; mx[4 * k + 1] = m4.y; mx[4 * k + 2] = m4.z; mx[4 * k + 3] = m4.w;
+      }
+      // W(i - 2) has been consumed
+      if (!mbar_wait_warp(p_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
+      const float un = exp2_int(-kj);
+      float ltn[16];
+      {
+        uint8_t* pb = smem + SM::P_OFF + b * SM::PB + wg * 16 * 128 + (row & 15);
+#pragma unroll
+        for (int h = 0; h < 16; h += 2) {
+          const float r0 = 8.f - (mx[h] == -INFINITY ? 0.f : mx[h]), r1 = 8.f - (mx[h + 1] == -INFINITY ? 0.f : mx[h + 1]);
+          const float e0 = ex2_approx(y[h] + r0), e1 = ex2_approx(y[h + 1] + r1);
+          ltn[h] = e0 * un;
+          ltn[h + 1] = e1 * un;
+          const uint16_t c_hi = e4m3x2_sat(e0, e1);
+          const float2 back = e4m3x2_f32(c_hi);
+          const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
+          uint8_t* p0 = pb + h * 128 + (((row >> 4) ^ (h & 7)) << 4);
+          uint8_t* p1 = pb + (h + 1) * 128 + (((row >> 4) ^ ((h + 1) & 7)) << 4);
+          p0[0] = (uint8_t)c_hi;
+          p1[0] = (uint8_t)(c_hi >> 8);
+          p0[NH * 128] = (uint8_t)c_lo;
+          p1[NH * 128] = (uint8_t)(c_lo >> 8);
+        }
+      }
+      if (!valid) {
+        // rows past the end may hold anything (even NaN codes); their weight is 0, but 0 * NaN is not
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (NWG == 2 && g != wg) continue;
+          uint8_t* rp = smem + SM::RING_OFF + ((2 * i + g) % NPR) * 32768 + (row >> 3) * 2048 + (row & 7) * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            *reinterpret_cast<uint4*>(rp + 16 * k) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(rp + 1024 + 16 * k) = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full + 8 * b);
+      // the scores of this entry are all read: the next entry's query may replace it
+      if (last && i + 1 < N && !load_q(w.e)) { ok = false; break; }
+      if (pending && !accumulate(i - 1)) { ok = false; break; }
+      pending = true;
+#pragma unroll
+      for (int h = 0; h < 16; ++h) lt[h] = ltn[h];
+      if (last) {
+        if (!accumulate(i)) { ok = false; break; }
+        const long long unit = (long long)hg * (a.units + a.n_ent) + c + e;
+        const long long r0 = a.flat ? (long long)e * NH : (long long)hg * NH;
+        const int live = (int)min((long long)NH, (a.flat ? a.rows_total : (long long)a.H) - r0) - 16 * wg;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          const float v = warp_sum(l[h]);
+          if (lane == 0) rl[q * 16 + h] = v;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(l_b);
+        float* po = a.part_o + (unit * NH + 16 * wg) * 512 + row;
+#pragma unroll
+        for (int h = 0; h < 16; ++h)
+          if (h < live) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) po[h * 512 + 128 * g] = O[16 * g + h];
+          }
+        if (!mbar_wait_warp(l_b, (kl++) & 1, abort_word, a.flag)) { ok = false; break; }
+        float* ml = a.part_ml + (unit * NH + 16 * wg) * 2;
+#pragma unroll
+        for (int h = 0; h < 16; ++h)
+          if (row == h && h < live)   // natural-log units; w carries the factor 2^8
+            *reinterpret_cast<float2*>(ml + 2 * h) =
+                make_float2((M[h] - 8.f) * 0.69314718055994531f, rl[h] + rl[16 + h] + rl[32 + h] + rl[48 + h]);
+#pragma unroll
+        for (int h = 0; h < 64; ++h) O[h] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) { M[h] = -INFINITY; l[h] = 0.f; lt[h] = 0.f; }
+        pending = false;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace tc
+}  // namespace mla

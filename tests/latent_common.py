@@ -64,6 +64,12 @@ def row_values(shape, rows):
     return out
 
 
+def row_scales(shape, rows):
+    """fp64 [n]: each row's scale once quantised."""
+    lat = rows[:, :shape.kv_lora_rank].double().numpy()
+    return np.array([2.0 ** lr.scale_exponent(x) for x in lat])
+
+
 def tables(rng, lens, bs, prefix_len, spare=2):
     """Random physical blocks: (prefix table, block table [n, width] with -1 beyond, n_blocks)."""
     npb = -(-prefix_len // bs)
@@ -135,10 +141,13 @@ class Case:
           sum in any order, 2 (r + d) 2^-24 sum |q_i c_i|; for a 16-bit act dtype the partial score
           that crosses between two CTAs in f16 adds 2^-11 of a half's score, and a query split in
           two E4M3 parts 2^-18 of its largest element per column, 2^-18 max|q| sum |c_i|.
-        e_p: 16-bit: a probability in bf16, or in two E4M3 parts (2^-4 of 2^-4), 2^-8 either way,
-          the latter with a floor of 2^-18 of the tile's largest: 2^-18 of the heaviest key for every
-          key. fp32 act: exponentials and sums, 64 2^-24.
-        o is then rounded once to its type.
+        e_p: 16-bit: a probability in bf16, or in two E4M3 parts (2^-4 of 2^-4), 2^-8 either way.
+          fp32 act: exponentials and sums, 64 2^-24.
+        The two-part weights w_j = p_j s_j / max_i(p_i s_i) 2^8 (the largest over a tile, at most the
+        largest of all) have an absolute floor besides: the second part's smallest step is 2^-9, so w_j
+        is off by up to 2^-10, that is p_j s_j by up to 2^-18 max_i(p_i s_i), however small p_j is. What
+        it multiplies is the code, so o is off by up to 2^-18 max_i(p_i s_i) sum_j |code_j|; the sums
+        that normalise take the weights unrounded. o is then rounded once to its type.
         """
         s = self.shape
         r = s.kv_lora_rank
@@ -150,15 +159,18 @@ class Case:
             x, ll, p = lr.latent_attention(qa, qp, c, pe, self.scale, self.sink)
             mag = (np.abs(qa) @ np.abs(c).T + np.abs(qp) @ np.abs(pe).T) * self.scale if len(k) else np.zeros_like(p)
             e = 2 * (r + s.qk_rope) * 2.0 ** -24 * mag
+            floor = 0.0
             if s.act_dtype == "bf16":
                 h = r // 2
                 half = np.maximum(np.abs(qa[:, :h] @ c[:, :h].T), np.abs(qa[:, h:] @ c[:, h:].T))
                 e = e + 2.0 ** -11 * (half + np.abs(qp @ pe.T)) * self.scale
                 if self.fp8 and len(k):
                     e = e + 2.0 ** -18 * np.abs(qa).max(1)[:, None] * np.abs(c).sum(1)[None] * self.scale
-                floor = 2.0 ** -18 * len(k) * (p.max(1) if len(k) else np.zeros(len(p)))
-                e = (e.max(1) if len(k) else np.zeros(len(p))) + 2.0 ** -8 + (floor if self.fp8 else 0)
+                e = (e.max(1) if len(k) else np.zeros(len(p))) + 2.0 ** -8
                 step = 2.0 ** -8
+                if self.fp8 and len(k):
+                    sc = row_scales(s, self.rows[torch.from_numpy(self.key_slots(t))])
+                    floor = 2.0 ** -18 * (p * sc).max(1)[:, None] * (np.abs(c) / sc[:, None]).sum(0)[None]
             else:
                 e = (e.max(1) if len(k) else np.zeros(len(p))) + 64 * 2.0 ** -24
                 step = 2.0 ** -24
@@ -166,7 +178,7 @@ class Case:
             a = p @ np.abs(c) if len(k) else np.zeros_like(x)
             o.append(x)
             lse.append(ll)
-            bo.append(2 * (e / (1 - e))[:, None] * a * (1 + step) + step * np.abs(x) + 1e-30)
+            bo.append((2 * (e / (1 - e))[:, None] * a + floor) * (1 + step) + step * np.abs(x) + 1e-30)
             bl.append(e / (1 - e) + 4 * 2.0 ** -24 * np.abs(np.where(np.isfinite(ll), ll, 0.0)) + 2.0 ** -22)
         return np.stack(o), np.stack(lse), np.stack(bo), np.stack(bl)
 
