@@ -26,6 +26,7 @@ struct MergeSrc {
   const float* o;       // [units, rows, r_kv]
   const float* ml;      // [units, rows, 2], and with half > 0 the same again ml_r floats further on
   const int2* seg;      // {first, count} of each entry: its units are first + entry ..; NULL: entry * splits ..
+  const int* nseg;      // seg NULL: the partials in use of each entry's `splits` (NULL: all)
   long long ml_r;
   long long group_units;   // units of one group of `rows` heads (flat = 0)
   int half;             // columns c >= half use the second (m, l) copy (0: one copy)
@@ -57,7 +58,7 @@ __device__ __forceinline__ long long merge_units(const MergeSrc& s, int H, int t
     *row = h % s.rows;
   }
   if (!s.seg) {
-    *count = s.splits;
+    *count = s.nseg ? min(s.nseg[e], s.splits) : s.splits;
     return g * s.group_units + e * s.splits;
   }
   const int2 f = s.seg[e];
@@ -164,11 +165,11 @@ struct LatentCall {
 
 // Which kernels a call takes, how many tokens at a time, and where their partials lie.
 struct LatentPlan {
-  int tc8;                 // the 8-bit tensor-core kernel
+  int tc8, tc16;           // tensor cores: the 8-bit kernel; the 16-bit cache's kernels
   int chunk;               // tokens per pass
   int splits;              // CUDA cores: splits of the keys
   int NH, groups, units;   // tc8: rows per CTA, head groups and slices of the own pass
-  int NHp, ents_p, units_p;   // ... rows per entry, entries and slices of the prefix pass
+  int NHp, ents_p, units_p;   // rows per entry, entries and slices of the prefix pass
   size_t o, ml, seg, o_p, ml_p, seg_p, total;
 };
 
@@ -181,6 +182,9 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   auto put = [&](size_t b) { size_t o = off; off = align_up(off + b, 256); return o; };
   // DeepSeek latent, blocks of a multiple of 16 rows (a TMA box is 16, 32 or 64 rows of one block)
   w.tc8 = h->cache8 && h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64 && c.block_size % 16 == 0;
+  // the kernels of the 16-bit cache: the same latent, boxes of 64 rows
+  w.tc16 = !h->cache8 && h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64 && c.block_size % 64 == 0 &&
+           H <= 128;
   if (w.tc8) {
     // the tile list of a pass is counted in int
     const long long tiles = cdiv(max_ctx, 128), tiles_p = cdiv(prefix_len, 128);
@@ -203,6 +207,26 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
       const size_t rows_p = (size_t)(w.units_p + w.ents_p) * w.NHp;
       w.o_p = put(rows_p * 512 * 4);
       w.ml_p = put(rows_p * 2 * 4);
+      w.seg_p = put((size_t)w.ents_p * 8);
+    }
+  } else if (w.tc16) {
+    // the kernels' tile prefix holds ATT_MAX_SEQ entries: sequences (33 heads or more), or
+    // blocks of 128 query rows
+    const long long most = H <= 32 ? ATT_MAX_SEQ * 128 / H : ATT_MAX_SEQ;
+    w.chunk = (int)(n < most ? n : most);
+    const long long s = cdiv(max_ctx, 256);
+    w.splits = s < 2 ? 2 : (s > 16 ? 16 : (int)s);
+    const size_t rows = (size_t)w.chunk * w.splits * H;
+    w.o = put(rows * 512 * 4);
+    w.ml = put(rows * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
+    w.seg = put((size_t)w.chunk * 4);
+    if (prefix_len > 0) {
+      w.NHp = 128;
+      w.ents_p = (int)cdiv((long long)w.chunk * H, 128);
+      w.units_p = sms / 2 > 0 ? sms / 2 : 1;
+      const size_t rows_p = (size_t)(w.units_p + w.ents_p) * 128;
+      w.o_p = put(rows_p * 512 * 4);
+      w.ml_p = put(rows_p * 2 * 4 * 2);
       w.seg_p = put((size_t)w.ents_p * 8);
     }
   } else {
@@ -306,6 +330,52 @@ static int latent_pass8(const mla_handle* h, const LatentPlan& w, const LatentCa
   return MLA_OK;
 }
 
+// One pass on the 16-bit cache's tensor-core kernels: the prefix on the
+// head-major one, whose 128 MMA rows take 128 query rows of any sequences; the
+// own rows as in mla_decode_attn.
+static int latent_pass16(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
+                         int* flag, cudaStream_t s) {
+  const mla_config& c = h->cfg;
+  const int R = c.kv_lora_rank + c.qk_rope;
+  int st;
+  if (a.prefix_len > 0) {
+    const long long rows = (long long)a.n_blocks * c.block_size;
+    CUtensorMap mc, ml;
+    if ((st = make_map2(&mc, a.cache, R, rows, R, 64)) != MLA_OK) return st;
+    if ((st = make_map_cache_groups(&ml, a.cache, R, rows, 4)) != MLA_OK) return st;
+    TcAttnArgs k{};
+    k.rows_total = (long long)a.n * c.n_heads;
+    k.n = (int)cdiv(k.rows_total, 128); k.H = 128;
+    k.bs = c.block_size; k.n_blocks = a.n_blocks; k.fixed_len = a.prefix_len;
+    k.block_table = a.prefix_table; k.q_abs = (const bf16*)a.q_abs; k.q_pe = (const bf16*)a.q_pe;
+    k.lat_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? 0 : c.qk_rope;
+    k.rope_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? c.kv_lora_rank : 0;
+    k.scale_log2 = h->scale * 1.4426950408889634f;
+    k.part_o = (float*)(scratch + w.o_p); k.part_ml = (float*)(scratch + w.ml_p); k.seg = (int2*)(scratch + w.seg_p);
+    k.flag = flag;
+    k.units = w.units_p; k.min_per = 1;
+    k.ml_r = (long long)(k.units + k.n) * 128 * 2;
+    static std::atomic<bool> attr[64];
+    set_smem_once(attr, tc_attn_decode_kernel<true>, AttnSmem::SIZE);
+    mla_timer_begin("attn_prefix", s);
+    launch_pdl(tc_attn_decode_kernel<true>, 2 * k.units, ATT_THREADS, AttnSmem::SIZE, s, mc, ml, k);
+    mla_timer_end("attn_prefix", s);
+    mla_count_launch(1);
+    MergeSrc& q = m->src[m->n_src++];
+    q.o = k.part_o; q.ml = k.part_ml; q.ml_r = k.ml_r; q.half = 256; q.seg = k.seg; q.rows = 128; q.flat = 1;
+  }
+  AttnParts P{};
+  float* part_o = (float*)(scratch + w.o);
+  float* part_ml = (float*)(scratch + w.ml);
+  st = tc_attention_launch(h, a.q_abs, a.q_pe, a.cache, a.n_blocks, a.table, a.mbps, a.ctx, a.max_ctx, a.n, part_o,
+                           part_ml, w.splits, flag, (int*)(scratch + w.seg), a.prefix_len > 0, &P, s);
+  if (st != MLA_OK) return st;
+  MergeSrc& q = m->src[m->n_src++];
+  q.o = part_o; q.ml = part_ml; q.ml_r = P.ml_r; q.half = P.half_cols; q.nseg = P.seg_counts; q.splits = P.splits;
+  q.rows = c.n_heads;
+  return MLA_OK;
+}
+
 // The same on CUDA cores (any shape, fp32 activations): the prefix rows simply
 // come first in every sequence's list of keys.
 static int latent_pass_simt(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
@@ -359,9 +429,12 @@ static inline int latent_core(const mla_handle* h, const LatentCall& call, void*
     m.lse = lse ? lse + (size_t)t * H : nullptr;
     m.ctx = a.ctx; m.min_ctx = a.prefix_len > 0 ? 0 : 1; m.max_ctx = a.max_ctx;
     m.cap = (long long)a.mbps * c.block_size;
-    const int st = w.tc8 ? latent_pass8(h, w, a, &m, scratch, flag, s) : latent_pass_simt(h, w, a, &m, scratch, flag, s);
+    const int st = w.tc8    ? latent_pass8(h, w, a, &m, scratch, flag, s)
+                   : w.tc16 ? latent_pass16(h, w, a, &m, scratch, flag, s)
+                            : latent_pass_simt(h, w, a, &m, scratch, flag, s);
     if (st != MLA_OK) return st;
     int most = w.splits;   // split partials of one query row, about
+    if (w.tc16 && a.prefix_len > 0) most += (int)(cdiv(w.units_p, w.ents_p) + 1);
     if (w.tc8) {
       const long long own = cdiv(a.max_ctx, 128), pre = cdiv(a.prefix_len, 128);
       most = (int)((own < cdiv(w.units, a.n) + 1 ? own : cdiv(w.units, a.n) + 1) +

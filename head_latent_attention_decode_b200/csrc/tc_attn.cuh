@@ -63,6 +63,13 @@ struct TcAttnArgs {
   const bf16* q_pe;   // [n, H, 64]
   int units, min_per;
   int* nseg;
+  int allow_empty;   // a context length of 0 is valid (the sequence has keys elsewhere)
+  // FLAT: entry b is the 128 query rows 128 b .. of rows_total, all against the
+  // same fixed_len rows of one block table; H is 128 and the partials are units
+  // c + b of [units + n] with seg[b] = {first cluster, clusters}
+  long long rows_total;
+  int fixed_len;
+  int2* seg;
 };
 
 constexpr int ATT_NST = 4;                      // latent ring depth
@@ -107,7 +114,9 @@ struct TileWalk {
 };
 
 // Context length of sequence b as the schedule counts it (0 when invalid).
+template <bool FLAT = false>
 __device__ __forceinline__ int attn_seq_len(const TcAttnArgs& a, int b) {
+  if (FLAT) return a.fixed_len;
   const int L = a.ctx[b];
   return (L < 1 || L > a.max_ctx || L > a.mbps * a.bs) ? 0 : L;
 }
@@ -118,6 +127,7 @@ __device__ __forceinline__ int attn_seq_len(const TcAttnArgs& a, int b) {
 // flattened tile list that cluster c takes (slices of `per` tiles, at least
 // a.min_per). Block 0 of the grid writes each sequence's segment count to
 // a.nseg. Every thread of the CTA calls it; it ends with a __syncthreads.
+template <bool FLAT = false>
 __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows, int* pref, int c, uint32_t r,
                                               int warp, int lane, int* per_out, int* g0_out, int* g1_out) {
   if (warp == 0) {
@@ -127,8 +137,8 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
       const int b = 8 * lane + k;
       int T = 0;
       if (b < a.n) {
-        const int L = attn_seq_len(a, b);
-        if (L == 0 && c == 0 && r == 0) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
+        const int L = attn_seq_len<FLAT>(a, b);
+        if (L == 0 && c == 0 && r == 0 && !(a.allow_empty && a.ctx[b] == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
         T = (L + tile_rows - 1) / tile_rows;
       }
       cnt[k] = T;
@@ -156,7 +166,8 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   if (blockIdx.x == 0) {   // segments of each sequence, for the merge
     for (int b = threadIdx.x; b < a.n; b += blockDim.x) {
       const int T = pref[b + 1] - pref[b];
-      a.nseg[b] = T > 0 ? (pref[b] + T - 1) / per - pref[b] / per + 1 : 0;
+      if (FLAT) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
+      else a.nseg[b] = T > 0 ? (pref[b] + T - 1) / per - pref[b] / per + 1 : 0;
     }
   }
   *per_out = per;
@@ -164,6 +175,7 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   *g1_out = min(total, c * per + per);
 }
 
+template <bool FLAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     tc_attn_decode_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_lat,
                           TcAttnArgs a) {
@@ -202,9 +214,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
 
   // ---- the schedule: tile prefix over the batch, then this cluster's slice ----
   int per, g0, g1;
-  attn_schedule(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
+  attn_schedule<FLAT>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
   if (g0 >= g1) return;   // both CTAs of the cluster take this branch together
   const int N = g1 - g0;
+  const long long tab = FLAT ? 0 : a.mbps;   // block-table row of sequence b: b * tab
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ATT_NST; ++i) { mbar_init(full_b + 8 * i, 1); mbar_init(empty_b + 8 * i, 1); }
@@ -246,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       if ((i & 31) == 0) {   // the block ids of the next 32 tiles, loaded in parallel
         TileWalk wk = w;
         for (int k = 0; k < lane && i + k + 1 < N; ++k) wk.next();
-        blkv = (i + lane < N) ? a.block_table[(long long)wk.b * a.mbps + (64 * wk.lt) / a.bs] : 0;
+        blkv = (i + lane < N) ? a.block_table[wk.b * tab + (64 * wk.lt) / a.bs] : 0;
       }
       const int blk = __shfl_sync(0xffffffffu, blkv, i & 31);
       const int st = i % ATT_NST;
@@ -400,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     // this half's share of sequence b's query: 128 latent values of CTA r's half
     // -> TMEM columns [64 g, 64 g + 64), 32 rotary values -> [128 + 16 g, 128 + 16 g + 16)
     auto load_q = [&](int b) {
-      const bool live = h < a.H;
+      const bool live = FLAT ? b * 128LL + h < a.rows_total : h < a.H;
       const long long qh = (long long)b * a.H + (live ? h : 0);
       const uint4* src = (const uint4*)(a.q_abs + qh * 512 + r * 256 + 128 * g);
 #pragma unroll
@@ -428,9 +441,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     w.start(g0);
     load_q(w.b);
     // block of tile i + 1, loaded one tile ahead (only its validity is needed here)
-    auto tile_block = [&](const TileWalk& t) { return a.block_table[(long long)t.b * a.mbps + (64 * t.lt) / a.bs]; };
+    auto tile_block = [&](const TileWalk& t) { return a.block_table[t.b * tab + (64 * t.lt) / a.bs]; };
     int blk_next = tile_block(w);
-    int seq_len = attn_seq_len(a, w.b);
+    int seq_len = attn_seq_len<FLAT>(a, w.b);
     float m_ref = -INFINITY, l = 0.f;
     int tseg = 0, kseg = 0;   // tile within the segment, segments done
     bool ok = true;
@@ -546,10 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           TileWalk wn = w;
           wn.next();
           load_q(wn.b);
-          seq_len = attn_seq_len(a, wn.b);
+          seq_len = attn_seq_len<FLAT>(a, wn.b);
         }
         const int j = c - pref[b] / per;               // this segment's split slot in sequence b
-        const long long unit = (long long)b * a.splits + j;
+        const long long unit = FLAT ? (long long)c + b : (long long)b * a.splits + j;
+        const bool store = FLAT ? b * 128LL + h < a.rows_total : h < a.H;
         float* const ml = a.part_ml + r * a.ml_r;      // this CTA's (m, l) copy
         if (!mbar_wait_warp(o_seg, kseg & 1, abort_word, a.flag)) { ok = false; break; }
         tc_fence_after();
@@ -558,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           uint32_t o[16];
           tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 16 * k, o);
           tmem_ld_wait();
-          if (h < a.H) {
+          if (store) {
 #pragma unroll
             for (int jj = 0; jj < 16; jj += 4)
               *reinterpret_cast<float4*>(po + 16 * k + jj) =
@@ -575,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(l_done + 8 * q);
         } else if (mbar_wait_warp(l_done + 8 * q, kseg & 1, abort_word, a.flag)) {
-          if (h < a.H) {
+          if (store) {
             ml[(unit * a.H + h) * 2] = m_ref * 0.69314718055994531f;   // natural-log units
             ml[(unit * a.H + h) * 2 + 1] = l + red_l[h];
           }

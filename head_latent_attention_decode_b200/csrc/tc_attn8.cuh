@@ -10,14 +10,15 @@
 // the second part is free.
 //   q_abs_h = 2^k_h (hi + lo): k_h brings the row's largest to at most 448; columns
 //     within 2^-10 of it are exact, smaller ones off by at most 2^-18 of it
-//   p: per head and tile of 128 keys, relative to that tile's own largest
-//     weight, so that no key underflows because of a heavier one elsewhere: a
-//     weight is off by 2^-8 of itself or 2^-18 of the tile's largest
+//   p: relative to a per-head reference R that follows the tiles' maxima both up
+//     and down (within 2^8 of the largest of each 128 keys), so that thousands of
+//     light keys behind a heavy one keep their weight: a weight is off by 2^-8 of
+//     itself or 2^-10 of its tile's largest
 //
 // The row scale s_j = 2^k_j folds into both products: with u_hj = q_h . code_j,
 //   y_hj = scale log2(e) (s_j u_hj + q_pe_h . k_pe_j) + k_j
-//   w_hj = 2^(y_hj - m_h + 8) in [0, 256],  m_h = max over the tile's keys of y_hj
-//   O_h  = sum_j w_hj code_j  (= 2^(8 - m_h) sum_j p_hj s_j code_j)
+//   w_hj = 2^(y_hj - R_h + 8) in [0, 256],  R_h >= max over the tile's keys of y_hj
+//   O_h  = sum_j w_hj code_j  (= 2^(8 - R_h) sum_j p_hj s_j code_j)
 //   l_h  = sum_j w_hj 2^-k_j
 //
 // Transposed tiles as in the 16-bit few-head kernel: 128 cache rows fill the
@@ -27,12 +28,14 @@
 //   R^T [128 keys x NH]        = k_pe . q_pe^T (bf16)  4 MMAs, M 128 x N NH x K 16
 //   O^T [128 latent x (hi | lo)] x 4 = codes^T . W^T  16 MMAs; codes^T is the same
 //                                                     shared-memory tile read MN-major
-// O^T leaves TMEM after every tile and is accumulated in registers (64 per
-// thread), where the change of reference is one multiply; so TMEM holds no
-// running state, and a tile's reference is free to go down as well as up.
+// O^T stays in TMEM; it is rescaled there only when some head's reference moves.
+// A reference is set one to two octaves above the tile's largest and kept while
+// the tiles' largest stay within (R - 8, R], which for most tiles they do (a
+// window of 5 octaves moved some head's reference on most tiles: 424 us against
+// @W us for 64 sequences of 1024 to 16384 rows and 128 heads).
 //
 // Roles: warpgroup g of NH / 16 runs the softmax of heads [16 g, 16 g + 16)
-// (thread <-> key) and accumulates their O^T (thread <-> latent column); then
+// (thread <-> key; for a rescale and at the end thread <-> latent column); then
 // one warp each for TMA, the score MMAs and the value MMAs. S and W alternate
 // between two buffers, so the scores of tile i + 1 run during the softmax of
 // tile i and its value MMAs during the softmax of tile i + 1.
@@ -71,6 +74,19 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major =
   return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// 32 lanes x 32 bit, 32 consecutive columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
 struct TcAttn8Args {
   int n_ent, groups, units;   // entries; head groups; slices (grid = units x groups)
   int flat;                   // 0: entry e is sequence e, its rows e H + NH group ..; 1: query rows e NH .. against one table
@@ -105,19 +121,21 @@ struct Attn8Smem {
   static constexpr int Q_OFF = ROPE_OFF + 2 * 16384;
   static constexpr int QPE_OFF = Q_OFF + 4 * QB;
   static constexpr int P_OFF = QPE_OFF + NH * 128;
-  static constexpr int RED_OFF = P_OFF + 2 * PB;  // per warpgroup: maxima [2][4][16], row sums [4][16],
-                                                  // each warp's copy of the tile maxima [4][3][16], q scale [16]
-  static constexpr int RED_WG = 128 + 64 + 192 + 16;
-  static constexpr int PREF_OFF = RED_OFF + NWG * RED_WG * 4;
+  // maxima [2][4 warps][NH]; per warpgroup row sums [4][16] and query scales [16]; per warp
+  // 8 - R [16] and the factors of a rescale [16]
+  static constexpr int RED_OFF = P_OFF + 2 * PB;
+  static constexpr int RED_MAX = 8 * NH, RED_WG = 64 + 16, RED_WARP = 32;
+  static constexpr int RED_FLOATS = RED_MAX + NWG * RED_WG + 4 * NWG * RED_WARP;
+  static constexpr int PREF_OFF = RED_OFF + RED_FLOATS * 4;
   static constexpr int BAR_OFF = PREF_OFF + (A8_MAX_ENT + 4) * 4;
   static constexpr int SIZE = 1024 + BAR_OFF + 512;
   static constexpr int THREADS = NWG * 128 + 96;
-  // TMEM: S buffers [hi NH | lo NH | rotary NH], then O^T of the four latent groups [hi NH | lo NH]
+  // TMEM: two S buffers [(hi 16 | lo 16) per warpgroup | rotary NH], then O^T of the four latent
+  // groups [(hi 16 | lo 16) per warpgroup]
   static constexpr int SB = NH == 16 ? 64 : 128;
-  static constexpr int NOB = NH == 16 ? 2 : 1;    // O^T buffers
   static constexpr int TM_O = 2 * SB;
   static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
-  static_assert(TM_O + NOB * 8 * NH <= 512, "tensor memory");
+  static_assert(TM_O + 8 * NH <= 512, "tensor memory");
   static_assert(BAR_OFF % 8 == 0 && P_OFF % 1024 == 0, "alignment");
 };
 
@@ -127,14 +145,14 @@ __device__ __forceinline__ int a8_len(const TcAttn8Args& a, int e) {
   return (L < a.min_ctx || L > a.max_ctx || (long long)L > (long long)a.mbps * a.bs) ? 0 : L;
 }
 
-// Walks a slice of the tile list: entry e, its tile lt, its length.
+// Walks a slice of the tile list: entry e, its tile lt, its length and tiles.
 struct Walk8 {
   const int* pref;   // tiles before entry e (shared memory), or NULL: e * T
-  int T, n, e, lt, len;
+  int T, n, e, lt, len, tiles;
   __device__ __forceinline__ int at(int i) const { return pref ? pref[i] : i * T; }
   __device__ __forceinline__ void start(const TcAttn8Args& a, int g) {
     if (pref) {
-      int lo = 0, hi = n - 1;   // the last entry that begins at or before g and is not empty there
+      int lo = 0, hi = n - 1;   // the last entry that begins at or before g: it is not empty
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (pref[mid] <= g) lo = mid;
@@ -145,15 +163,20 @@ struct Walk8 {
       e = g / T;
     }
     lt = g - at(e);
-    len = a8_len(a, e);
+    enter(a);
   }
-  __device__ __forceinline__ bool seg_last() const { return at(e) + lt + 1 == at(e + 1); }
+  __device__ __forceinline__ void enter(const TcAttn8Args& a) {
+    len = a8_len(a, e);
+    tiles = (len + 127) / 128;
+  }
+  __device__ __forceinline__ bool seg_last() const { return lt + 1 == tiles; }
   __device__ __forceinline__ void next(const TcAttn8Args& a) {
     if (!seg_last()) { ++lt; return; }
-    ++e;
-    while (e < n && at(e + 1) == at(e)) ++e;
     lt = 0;
-    len = e < n ? a8_len(a, e) : 0;
+    do {
+      if (++e == n) { len = tiles = 0; return; }
+      enter(a);
+    } while (tiles == 0);
   }
 };
 
@@ -163,7 +186,7 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
                     TcAttn8Args a) {
   using SM = Attn8Smem<NH>;
   griddep_wait();   // the inputs all come from the stream's earlier kernels
-  constexpr int NPR = SM::NPR, NWG = SM::NWG, NOB = SM::NOB;
+  constexpr int NPR = SM::NPR, NWG = SM::NWG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -174,11 +197,12 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
   const uint32_t full_b = bar, empty_b = full_b + 8 * NPR;       // [NPR] ring entry landed / consumed
   const uint32_t rfull = empty_b + 8 * NPR, rempty = rfull + 16;  // [2] rotary block landed / consumed
   const uint32_t s_full = rempty + 16, s_free = s_full + 16;      // [2] scores complete / read
-  const uint32_t p_full = s_free + 16, p_free = p_full + 16;      // [2] weights written / consumed
-  const uint32_t o_full = p_free + 16, o_free = o_full + 16;      // [NOB] O^T complete / read
-  const uint32_t q_ready = o_free + 16;                           // the next entry's query is in shared memory
-  const uint32_t fin_s = q_ready + 8, fin_o = fin_s + 8;
-  const uint32_t wg_b = fin_o + 8;                                // per warpgroup: red[2], query scales, row sums
+  const uint32_t p_full = s_free + 16, p_free = p_full + 16;      // [2] weights written / consumed (O^T holds the tile)
+  const uint32_t q_ready = p_free + 16;                           // the next entry's query is in shared memory
+  const uint32_t o_free = q_ready + 8;                            // O^T of an entry read out
+  const uint32_t fin_s = o_free + 8, fin_o = fin_s + 8;
+  const uint32_t red_b = fin_o + 8;                               // [2] the warps' maxima posted
+  const uint32_t wg_b = red_b + 16;                               // per warpgroup: query scales, row sums
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 480);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 484);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -208,7 +232,7 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
     if (lane == 31) pref[a.n_ent] = incl;
   }
   __syncthreads();
-  Walk8 w0{a.flat ? nullptr : pref, T_flat, a.n_ent, 0, 0, 0};
+  const Walk8 w0{a.flat ? nullptr : pref, T_flat, a.n_ent, 0, 0, 0, 0};
   const int total = w0.at(a.n_ent);
   const int per = max(1, (total + a.units - 1) / a.units);
   if (blockIdx.x == 0)
@@ -229,13 +253,13 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       mbar_init(s_free + 8 * i, 4 * NWG);
       mbar_init(p_full + 8 * i, 4 * NWG);
       mbar_init(p_free + 8 * i, 1);
-      mbar_init(o_full + 8 * i, 1);
-      mbar_init(o_free + 8 * i, 4 * NWG);
+      mbar_init(red_b + 8 * i, 4 * NWG);
     }
+    mbar_init(o_free, 4 * NWG);
     mbar_init(q_ready, 4 * NWG);
     mbar_init(fin_s, 1);
     mbar_init(fin_o, 1);
-    for (int i = 0; i < 4 * NWG; ++i) mbar_init(wg_b + 8 * i, 4);
+    for (int i = 0; i < 2 * NWG; ++i) mbar_init(wg_b + 8 * i, 4);
     *abort_word = 0;
     fence_mbar_init();
   }
@@ -359,11 +383,16 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       constexpr uint32_t id_o = idesc_e4m3(128, 2 * NH, 1);
       // codes^T: one 128-column group along M, 8-key octets 2048 B apart along K
       const uint64_t d_v = sdesc_sw128_mn_sbo(ring_s, 1024, 2048), d_p = sdesc_sw128(p_s);
+      Walk8 w = w0;
+      w.start(a, g0);
+      int ks = 0;
       for (int i = 0; i < N; ++i) {
-        const int b = i & 1, ob = i % NOB;
+        const int b = i & 1;
+        const bool first = i == 0 || w.lt == 0;
         if (!mbar_wait(p_full + 8 * b, (i >> 1) & 1, abort_word, a.flag) ||
-            !mbar_wait(o_free + 8 * ob, ((i / NOB) & 1) ^ 1, abort_word, a.flag))
+            (first && ks > 0 && !mbar_wait(o_free, (ks - 1) & 1, abort_word, a.flag)))
           break;
+        if (first) ++ks;
         tc_fence_after();
         const uint64_t dp = d_p + (uint64_t)(b * (SM::PB / 16));
 #pragma unroll
@@ -374,12 +403,12 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8(tmem + SM::TM_O + ob * 8 * NH + (2 * g + kk) * 2 * NH, dv + (kk * 1024 + 8192 * k) / 16,
-                     dp + 2 * k, id_o, k > 0 ? 1u : 0u);
+              mma_f8(tmem + SM::TM_O + (2 * g + kk) * 2 * NH, dv + (kk * 1024 + 8192 * k) / 16, dp + 2 * k, id_o,
+                     (!first || k > 0) ? 1u : 0u);
           mma_commit(empty_b + 8 * slot);
         }
-        mma_commit(o_full + 8 * ob);
         mma_commit(p_free + 8 * b);
+        if (i + 1 < N) w.next(a);
       }
       mma_commit(fin_o);
       const uint64_t t0 = global_timer_ns();
@@ -387,15 +416,16 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
     }
   } else {
-    // ---------------- softmax and accumulation: thread <-> key of the tile, then <-> latent column ----------------
+    // ---------------- softmax: thread <-> key of the tile ----------------
     const int wg = warp >> 2, q = warp & 3;
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-    float* red = (float*)(smem + SM::RED_OFF) + wg * SM::RED_WG;   // [2][4][16]
-    float* rl = red + 128;                                         // [4][16]
-    float* mt = rl + 64 + 48 * q;                                  // [3][16], this warp's
-    float* slq = rl + 64 + 192;                                         // [16] scale log2(e) 2^k_h
-    const uint32_t red_b = wg_b + 32 * wg, qs_b = red_b + 16, l_b = qs_b + 8;
+    float* red = (float*)(smem + SM::RED_OFF);                       // [2][4][NH]
+    float* rl = red + SM::RED_MAX + wg * SM::RED_WG;                 // [4][16]
+    float* slq = rl + 64;                                            // [16] scale log2(e) 2^k_h
+    float* ref_w = red + SM::RED_MAX + NWG * SM::RED_WG + warp * SM::RED_WARP;   // [16] 8 - R, this warp's copy
+    float* al_w = ref_w + 16;                                        // [16] factors of the last rescale
+    const uint32_t qs_b = wg_b + 16 * wg, l_b = qs_b + 8;
     int kq = 0, kl = 0;   // phases of qs_b and l_b
 
     // The 16 heads' query rows of entry e in two E4M3 parts: eight threads per head, 64 columns each.
@@ -443,8 +473,8 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
           lo[j] = (uint32_t)e4m3x2_sat(f0 - g0v.x, f1 - g0v.y) | ((uint32_t)e4m3x2_sat(f2 - g1v.x, f3 - g1v.y) << 16);
         }
         const int chunk = ((sub & 1) * 4 + ch) ^ (hd & 7);
-        *reinterpret_cast<uint4*>(qb + hd * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(qb + (NH + hd) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(qb + (32 * wg + hh) * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(qb + (32 * wg + 16 + hh) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       *reinterpret_cast<uint4*>(smem + SM::QPE_OFF + hd * 128 + 16 * (sub ^ (hd & 7))) = pe;
       fence_proxy_async_smem();
@@ -452,68 +482,41 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       if (lane == 0) { mbar_arrive(q_ready); mbar_arrive(qs_b); }
       return mbar_wait_warp(qs_b, (kq++) & 1, abort_word, a.flag);   // the scales are there for every warp
     };
-    // this thread's key in the walk's tile: block id (-1: no key), then its row scale
-    auto row_block = [&](const Walk8& v) {
+    // This thread's key, in flight ahead of its tile: the block id as loaded (two tiles ahead, so that
+    // nothing waits for it) and the place within the block, then the row scale (one tile ahead).
+    int raw = -1, off = 0;
+    auto fetch_block = [&](const Walk8& v) {
       const int j = 128 * v.lt + row;
-      if (v.e >= v.n || j >= v.len) return -1;
-      const int b = a.table[v.e * a.table_stride + j / a.bs];
-      return b >= 0 && b < a.n_blocks ? b : -1;
+      raw = -1;
+      if (j < v.len) {
+        const int at = j / a.bs;
+        off = j - at * a.bs;
+        raw = a.table[v.e * a.table_stride + at];
+      }
     };
-    auto row_scale = [&](const Walk8& v, int b) {
-      return b < 0 ? 0.f
-                   : reinterpret_cast<const float*>(a.cache + (long long)b * a.block_bytes + a.sc_off)[(128 * v.lt + row) % a.bs];
+    float s_next = 0.f;
+    bool valid_next = false;
+    auto fetch_scale = [&]() {
+      valid_next = raw >= 0 && raw < a.n_blocks;
+      s_next = 0.f;
+      if (valid_next)
+        s_next = reinterpret_cast<const float*>(a.cache + (long long)raw * a.block_bytes + a.sc_off)[off];
     };
 
-    float O[64], M[16], l[16], lt[16];
+    float l[16];
 #pragma unroll
-    for (int h = 0; h < 64; ++h) O[h] = 0.f;
-#pragma unroll
-    for (int h = 0; h < 16; ++h) { M[h] = -INFINITY; l[h] = 0.f; lt[h] = 0.f; }
-    // O += O^T(i) out of TMEM, both moved to the reference max(M, m(i)); the row sums likewise
-    auto accumulate = [&](int i) -> bool {
-      const int ob = i % NOB;
-      float al[16], f[16];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 m4 = *reinterpret_cast<const float4*>(mt + 16 * (i % 3) + 4 * k);
-        const float mv[4] = {m4.x, m4.y, m4.z, m4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int h = 4 * k + j;
-          const float mn = fmaxf(M[h], mv[j]);
-          al[h] = M[h] == -INFINITY ? 0.f : ex2_approx(M[h] - mn);
-          f[h] = mv[j] == -INFINITY ? 0.f : ex2_approx(mv[j] - mn);
-          M[h] = mn;
-          l[h] = l[h] * al[h] + lt[h] * f[h];
-        }
-      }
-      if (!mbar_wait_warp(o_full + 8 * ob, (i / NOB) & 1, abort_word, a.flag)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint32_t hi[16], lo[16];
-        const uint32_t oa = tmem + SM::TM_O + ob * 8 * NH + g * 2 * NH + 16 * wg + lane_base;
-        tmem_ld16(oa, hi);
-        tmem_ld16(oa + NH, lo);
-        tmem_ld_wait();
-#pragma unroll
-        for (int h = 0; h < 16; ++h)
-          O[16 * g + h] = fmaf(f[h], __uint_as_float(hi[h]) + __uint_as_float(lo[h]), O[16 * g + h] * al[h]);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_free + 8 * ob);
-      return true;
-    };
-
+    for (int h = 0; h < 16; ++h) l[h] = 0.f;
+    float R = -INFINITY, top = -INFINITY;   // lane h: head h's reference and the largest seen (h < NH)
+    if (lane < 16) ref_w[lane] = 8.f;
     Walk8 w = w0;
     w.start(a, g0);
-    Walk8 w1 = w;             // one tile ahead: its row scale is in flight; block ids run two ahead
+    Walk8 w1 = w;
+    fetch_block(w);
+    fetch_scale();
     w1.next(a);
-    const int blk0 = row_block(w);
-    int blk1 = N > 1 ? row_block(w1) : -1;
-    float s_next = row_scale(w, blk0);
-    bool valid_next = blk0 >= 0, ok = load_q(w.e), pending = false;
+    if (N > 1) fetch_block(w1);
+    bool ok = load_q(w.e);
+    bool first = true;
     for (int i = 0; i < N && ok; ++i) {
       const int b = i & 1;
       const float sj = s_next;
@@ -521,23 +524,21 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       const int e = w.e;
       const bool last = i == N - 1 || w.seg_last();
       if (i + 1 < N) {
-        s_next = row_scale(w1, blk1);
-        valid_next = blk1 >= 0;
+        fetch_scale();
         w = w1;
         w1.next(a);
-        blk1 = i + 2 < N ? row_block(w1) : -1;
+        if (i + 2 < N) fetch_block(w1);
       }
-      // 2^k_j; rows never written (scale 0) count as zero rows
-      const int kj = max(C8_KMIN, min(C8_KMAX, (int)(__float_as_uint(sj) >> 23) - 127));
       if (!mbar_wait_warp(s_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       tc_fence_after();
+      // 2^k_j; rows never written (scale 0) count as zero rows
+      const int kj = max(C8_KMIN, min(C8_KMAX, (int)(__float_as_uint(sj) >> 23) - 127));
       float y[16];
       {
-        uint32_t hi[16], lo[16], rp[16];
-        const uint32_t sa = tmem + SM::SB * b + 16 * wg + lane_base;
-        tmem_ld16(sa, hi);
-        tmem_ld16(sa + NH, lo);
-        tmem_ld16(sa + 2 * NH, rp);
+        uint32_t u[32], rp[16];
+        const uint32_t sa = tmem + SM::SB * b + lane_base;
+        tmem_ld32(sa + 32 * wg, u);
+        tmem_ld16(sa + 2 * NH + 16 * wg, rp);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
@@ -549,57 +550,103 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int h = 4 * k + j;
-            const float u = __uint_as_float(hi[h]) + __uint_as_float(lo[h]);
+            const float uu = __uint_as_float(u[h]) + __uint_as_float(u[16 + h]);
             const float r = fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj);
-            y[h] = valid ? fmaf(u, sj * sv[j], r) : -INFINITY;
+            y[h] = valid ? fmaf(uu, sj * sv[j], r) : -INFINITY;
           }
         }
       }
-      // the tile's largest per head: within the warp, then over the warpgroup's four
-      float mx[16];
+      // the tile's largest per head: within the warp, then over the four warps by lane h for head h
+      {
+        float mx[16];
 #pragma unroll
-      for (int h = 0; h < 16; ++h) mx[h] = warp_max_f32(y[h]);
-      if (lane == 0) {
+        for (int h = 0; h < 16; ++h) mx[h] = warp_max_f32(y[h]);
+        if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<float4*>(red + (b * 4 + q) * 16 + 4 * k) =
-              make_float4(mx[4 * k], mx[4 * k + 1], mx[4 * k + 2], mx[4 * k + 3]);
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(red + (b * 4 + q) * NH + 16 * wg + 4 * k) =
+                make_float4(mx[4 * k], mx[4 * k + 1], mx[4 * k + 2], mx[4 * k + 3]);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(red_b + 8 * b);
       if (!mbar_wait_warp(red_b + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float4 m4 = *reinterpret_cast<const float4*>(red + b * 64 + 4 * k);
-#pragma unroll
-        for (int o = 1; o < 4; ++o) {
-          const float4 n4 = *reinterpret_cast<const float4*>(red + (b * 4 + o) * 16 + 4 * k);
-          m4.x = fmaxf(m4.x, n4.x); m4.y = fmaxf(m4.y, n4.y); m4.z = fmaxf(m4.z, n4.z); m4.w = fmaxf(m4.w, n4.w);
+      {
+        float m = -INFINITY;
+        if (lane < NH) {
+          const float* rr = red + b * 4 * NH + lane;
+          m = fmaxf(fmaxf(rr[0], rr[NH]), fmaxf(rr[2 * NH], rr[3 * NH]));
         }
-        if (lane == 0) *reinterpret_cast<float4*>(mt + 16 * (i % 3) + 4 * k) = m4;
-        mx[4 * k] = m4.x; mx[4 * k + 1] = m4.y; mx[4 * k + 2] = m4.z; mx[4 * k + 3] = m4.w;
+        // Move R when the tile's largest leaves (R - 8, R]; not below 2^-40 of the largest seen, where a
+        // tile no longer counts (and 2^(old - new) stays far from overflow). Every warp decides alike.
+        top = fmaxf(top, m);
+        const float want = fmaxf(ceilf(m) + 1.f, top - 40.f);
+        const bool move = m > -INFINITY && (m > R || want < R - 6.f);
+        if (__any_sync(0xffffffffu, move)) {
+          float al = 1.f;
+          if (move) {
+            if (R > -INFINITY) al = ex2_approx(R - want);
+            R = want;
+          }
+          if (lane < NH && (lane >> 4) == wg) {
+            ref_w[lane & 15] = R == -INFINITY ? 8.f : 8.f - R;
+            al_w[lane & 15] = al;
+          }
+          __syncwarp();
+          if (!first) {
+            // P.V(i - 1) has to be complete; its buffer's barrier says so, and nothing later is under way
+            if (!mbar_wait_warp(p_free + 8 * (b ^ 1), ((i - 1) >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+            tc_fence_after();
+            float f[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = *reinterpret_cast<const float4*>(al_w + 4 * k);
+              f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
+            }
+#pragma unroll
+            for (int h = 0; h < 16; ++h) l[h] *= f[h];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t o[32];
+              const uint32_t oa = tmem + SM::TM_O + g * 2 * NH + 32 * wg + lane_base;
+              tmem_ld32(oa, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * f[h & 15]);
+              tmem_st16(oa, o);
+              tmem_st16(oa + 16, o + 16);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
       }
+      first = last;
       // W(i - 2) has been consumed
       if (!mbar_wait_warp(p_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
       const float un = exp2_int(-kj);
-      float ltn[16];
       {
-        uint8_t* pb = smem + SM::P_OFF + b * SM::PB + wg * 16 * 128 + (row & 15);
+        uint8_t* pb = smem + SM::P_OFF + b * SM::PB + wg * 32 * 128 + (row & 15);
 #pragma unroll
-        for (int h = 0; h < 16; h += 2) {
-          const float r0 = 8.f - (mx[h] == -INFINITY ? 0.f : mx[h]), r1 = 8.f - (mx[h + 1] == -INFINITY ? 0.f : mx[h + 1]);
-          const float e0 = ex2_approx(y[h] + r0), e1 = ex2_approx(y[h + 1] + r1);
-          ltn[h] = e0 * un;
-          ltn[h + 1] = e1 * un;
-          const uint16_t c_hi = e4m3x2_sat(e0, e1);
-          const float2 back = e4m3x2_f32(c_hi);
-          const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
-          uint8_t* p0 = pb + h * 128 + (((row >> 4) ^ (h & 7)) << 4);
-          uint8_t* p1 = pb + (h + 1) * 128 + (((row >> 4) ^ ((h + 1) & 7)) << 4);
-          p0[0] = (uint8_t)c_hi;
-          p1[0] = (uint8_t)(c_hi >> 8);
-          p0[NH * 128] = (uint8_t)c_lo;
-          p1[NH * 128] = (uint8_t)(c_lo >> 8);
+        for (int k = 0; k < 4; ++k) {
+          const float4 r4 = *reinterpret_cast<const float4*>(ref_w + 4 * k);
+          const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const int h = 4 * k + j;
+            const float e0 = ex2_approx(y[h] + rv[j]), e1 = ex2_approx(y[h + 1] + rv[j + 1]);
+            l[h] = fmaf(e0, un, l[h]);
+            l[h + 1] = fmaf(e1, un, l[h + 1]);
+            const uint16_t c_hi = e4m3x2_sat(e0, e1);
+            const float2 back = e4m3x2_f32(c_hi);
+            const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
+            uint8_t* p0 = pb + h * 128 + (((row >> 4) ^ (h & 7)) << 4);
+            uint8_t* p1 = pb + (h + 1) * 128 + (((row >> 4) ^ ((h + 1) & 7)) << 4);
+            p0[0] = (uint8_t)c_hi;
+            p1[0] = (uint8_t)(c_hi >> 8);
+            p0[16 * 128] = (uint8_t)c_lo;
+            p1[16 * 128] = (uint8_t)(c_lo >> 8);
+          }
         }
       }
       if (!valid) {
@@ -618,14 +665,9 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * b);
-      // the scores of this entry are all read: the next entry's query may replace it
-      if (last && i + 1 < N && !load_q(w.e)) { ok = false; break; }
-      if (pending && !accumulate(i - 1)) { ok = false; break; }
-      pending = true;
-#pragma unroll
-      for (int h = 0; h < 16; ++h) lt[h] = ltn[h];
       if (last) {
-        if (!accumulate(i)) { ok = false; break; }
+        // the scores of this entry are all read: the next entry's query may replace its own
+        if (i + 1 < N && !load_q(w.e)) { ok = false; break; }
         const long long unit = (long long)hg * (a.units + a.n_ent) + c + e;
         const long long r0 = a.flat ? (long long)e * NH : (long long)hg * NH;
         const int live = (int)min((long long)NH, (a.flat ? a.rows_total : (long long)a.H) - r0) - 16 * wg;
@@ -633,28 +675,36 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         for (int h = 0; h < 16; ++h) {
           const float v = warp_sum(l[h]);
           if (lane == 0) rl[q * 16 + h] = v;
+          l[h] = 0.f;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(l_b);
+        // thread <-> latent column
+        if (!mbar_wait_warp(p_free + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+        tc_fence_after();
         float* po = a.part_o + (unit * NH + 16 * wg) * 512 + row;
+        for (int g = 0; g < 4; ++g) {
+          uint32_t o[32];
+          tmem_ld32(tmem + SM::TM_O + g * 2 * NH + 32 * wg + lane_base, o);
+          tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < 16; ++h)
-          if (h < live) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) po[h * 512 + 128 * g] = O[16 * g + h];
-          }
+          for (int h = 0; h < 16; ++h)
+            if (h < live) po[h * 512 + 128 * g] = __uint_as_float(o[h]) + __uint_as_float(o[16 + h]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
         if (!mbar_wait_warp(l_b, (kl++) & 1, abort_word, a.flag)) { ok = false; break; }
-        float* ml = a.part_ml + (unit * NH + 16 * wg) * 2;
-#pragma unroll
-        for (int h = 0; h < 16; ++h)
-          if (row == h && h < live)   // natural-log units; w carries the factor 2^8
-            *reinterpret_cast<float2*>(ml + 2 * h) =
-                make_float2((M[h] - 8.f) * 0.69314718055994531f, rl[h] + rl[16 + h] + rl[32 + h] + rl[48 + h]);
-#pragma unroll
-        for (int h = 0; h < 64; ++h) O[h] = 0.f;
-#pragma unroll
-        for (int h = 0; h < 16; ++h) { M[h] = -INFINITY; l[h] = 0.f; lt[h] = 0.f; }
-        pending = false;
+        if (q == 0 && lane < NH && (lane >> 4) == wg) {
+          const int h = lane & 15;
+          if (h < live)   // natural-log units; w carries the factor 2^8
+            *reinterpret_cast<float2*>(a.part_ml + (unit * NH + 16 * wg + h) * 2) =
+                make_float2((R - 8.f) * 0.69314718055994531f, rl[h] + rl[16 + h] + rl[32 + h] + rl[48 + h]);
+        }
+        R = -INFINITY;
+        top = -INFINITY;
+        if (lane < 16) ref_w[lane] = 8.f;
+        __syncwarp();
       }
     }
   }

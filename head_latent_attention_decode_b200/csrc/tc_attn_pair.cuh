@@ -83,7 +83,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int L = a.ctx[b];
   if (L < 1 || L > a.max_ctx || L > a.mbps * a.bs) {
-    if (threadIdx.x == 0 && r == 0 && sp == 0) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
+    if (threadIdx.x == 0 && r == 0 && sp == 0 && !(a.allow_empty && L == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
     L = 0;
   }
   const int r0 = sp * a.chunk, r1 = min(L, r0 + a.chunk);

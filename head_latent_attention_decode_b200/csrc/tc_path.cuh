@@ -709,20 +709,27 @@ struct LatentExt {
 
 // Split-KV absorbed attention and the LSE merge of the splits -> o_lat (bf16).
 // tcgen05 kernel for the DeepSeek latent dims, CUDA-core kernel otherwise.
-static inline int tc_attention_core(const mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache,
-                                    int n_blocks, const int32_t* block_table, int mbps, const int32_t* ctx,
-                                    int max_ctx, int n, float* part_o, float* part_ml, int splits, bf16* o_lat,
-                                    int* flag, int* nseg, cudaStream_t s, int olat_f16 = 0) {
+// tc_attention_launch leaves the split partials and says in *out how they lie;
+// tc_attention_core merges them.
+struct AttnParts {
+  long long ml_r;       // offset of the second CTA's (m, l) copy (tensor-core kernels)
+  int half_cols;        // latent columns per (m, l) copy (0: one copy)
+  int splits;           // split slots per sequence
+  const int* seg_counts;   // split partials per sequence, when a kernel reports them
+};
+static inline int tc_attention_launch(const mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache,
+                                      int n_blocks, const int32_t* block_table, int mbps, const int32_t* ctx,
+                                      int max_ctx, int n, float* part_o, float* part_ml, int splits, int* flag,
+                                      int* nseg, int allow_empty, AttnParts* out, cudaStream_t s) {
   const mla_config& c = h->cfg;
   const TcState& T = h->tc;
   const int H = c.n_heads, dr = c.qk_rope, rkv = c.kv_lora_rank;
   int st;
   // 1. split-KV absorbed attention and the LSE merge -> o_lat (bf16)
   const int R = rkv + dr;
-  const float* sink = h->has_sink ? (const float*)(h->base + h->L.sink) : nullptr;
-  long long ml_r = 0;         // offset of the second CTA's (m, l) copy (tensor-core kernels)
-  int half_cols = 0;          // latent columns per (m, l) copy (0: one copy)
-  int* seg_counts = nullptr;  // split partials per sequence, when a kernel reports them
+  long long ml_r = 0;
+  int half_cols = 0;
+  int* seg_counts = nullptr;
   const bool latent_ok = rkv == 512 && dr == 64 && c.block_size % 64 == 0 && (((uintptr_t)q_abs) & 15) == 0 &&
                          (((uintptr_t)q_pe) & 15) == 0;
   if (latent_ok && H <= 32) {
@@ -749,6 +756,7 @@ static inline int tc_attention_core(const mla_handle* h, const void* q_abs, cons
     if ((st = make_map2(&mc, kv_cache, R, (long long)n_blocks * c.block_size, R, 64)) != MLA_OK) return st;
     if ((st = make_map_cache_groups(&ml, kv_cache, R, (long long)n_blocks * c.block_size, 2)) != MLA_OK) return st;
     TcAttnArgs ta{};
+    ta.allow_empty = allow_empty;
     ta.n = n; ta.H = H; ta.splits = sp; ta.chunk = chunk;
     ta.bs = c.block_size; ta.n_blocks = n_blocks; ta.mbps = mbps; ta.max_ctx = max_ctx;
     ta.block_table = block_table; ta.ctx = ctx; ta.q_abs = (const bf16*)q_abs;
@@ -779,6 +787,7 @@ static inline int tc_attention_core(const mla_handle* h, const void* q_abs, cons
     if ((st = make_map2(&mc, kv_cache, R, (long long)n_blocks * c.block_size, R, 64)) != MLA_OK) return st;
     if ((st = make_map_cache_groups(&ml, kv_cache, R, (long long)n_blocks * c.block_size, 4)) != MLA_OK) return st;
     TcAttnArgs ta{};
+    ta.allow_empty = allow_empty;
     ta.n = n; ta.H = H; ta.splits = splits; ta.chunk = 0;
     ta.bs = c.block_size; ta.n_blocks = n_blocks; ta.mbps = mbps; ta.max_ctx = max_ctx;
     ta.block_table = block_table; ta.ctx = ctx; ta.q_abs = (const bf16*)q_abs; ta.q_pe = (const bf16*)q_pe;
@@ -793,9 +802,9 @@ static inline int tc_attention_core(const mla_handle* h, const void* q_abs, cons
     half_cols = 256;
     seg_counts = nseg;
     static std::atomic<bool> attr[64];
-    set_smem_once(attr, tc_attn_decode_kernel, AttnSmem::SIZE);
+    set_smem_once(attr, tc_attn_decode_kernel<false>, AttnSmem::SIZE);
     mla_timer_begin("attn", s);
-    launch_pdl(tc_attn_decode_kernel, 2 * pairs, ATT_THREADS, AttnSmem::SIZE, s, mc, ml, ta);
+    launch_pdl(tc_attn_decode_kernel<false>, 2 * pairs, ATT_THREADS, AttnSmem::SIZE, s, mc, ml, ta);
     mla_timer_end("attn", s);
     mla_count_launch(1);
   } else {
@@ -812,12 +821,30 @@ static inline int tc_attention_core(const mla_handle* h, const void* q_abs, cons
     mla_timer_end("attn", s);
     mla_count_launch(1);
   }
+  out->ml_r = ml_r;
+  out->half_cols = half_cols;
+  out->splits = splits;
+  out->seg_counts = seg_counts;
+  return MLA_OK;
+}
+
+static inline int tc_attention_core(const mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache,
+                                    int n_blocks, const int32_t* block_table, int mbps, const int32_t* ctx,
+                                    int max_ctx, int n, float* part_o, float* part_ml, int splits, bf16* o_lat,
+                                    int* flag, int* nseg, cudaStream_t s, int olat_f16 = 0) {
+  const int H = h->cfg.n_heads, rkv = h->cfg.kv_lora_rank;
+  const float* sink = h->has_sink ? (const float*)(h->base + h->L.sink) : nullptr;
+  AttnParts P{};
+  const int st = tc_attention_launch(h, q_abs, q_pe, kv_cache, n_blocks, block_table, mbps, ctx, max_ctx, n, part_o,
+                                     part_ml, splits, flag, nseg, 0, &P, s);
+  if (st != MLA_OK) return st;
+  splits = P.splits;
   if (olat_f16)   // its only reader is an FP8-weight GEMM
     launch_pdl(attn_combine_kernel<__half>, dim3(n, H), 128, 0, s, (const float*)part_o, (const float*)part_ml, splits,
-               H, rkv, (__half*)o_lat, sink, ml_r, half_cols, (const int*)seg_counts);
+               H, rkv, (__half*)o_lat, sink, P.ml_r, P.half_cols, P.seg_counts);
   else
     launch_pdl(attn_combine_kernel<bf16>, dim3(n, H), 128, 0, s, (const float*)part_o, (const float*)part_ml, splits,
-               H, rkv, o_lat, sink, ml_r, half_cols, (const int*)seg_counts);
+               H, rkv, o_lat, sink, P.ml_r, P.half_cols, P.seg_counts);
   mla_count_launch(1);
   return MLA_OK;
 }

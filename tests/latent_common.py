@@ -143,12 +143,13 @@ class Case:
           two E4M3 parts 2^-18 of its largest element per column, 2^-18 max|q| sum |c_i|.
         e_p: 16-bit: a probability in bf16, or in two E4M3 parts (2^-4 of 2^-4), 2^-8 either way.
           fp32 act: exponentials and sums, 64 2^-24.
-        The two-part weights w_j = p_j s_j / max_i(p_i s_i) 2^8 (the largest over a tile, at most the
-        largest of all) have an absolute floor besides: the second part's smallest step is 2^-9, so w_j
-        is off by up to 2^-10, that is p_j s_j by up to 2^-18 max_i(p_i s_i), however small p_j is. What
-        it multiplies is the code, so o is off by up to 2^-18 max_i(p_i s_i) sum_j |code_j|; the sums
-        that normalise take the weights unrounded. o is then rounded once to its type.
-        """
+        The two-part weights w_j = 2^8 p_j s_j / 2^R have an absolute floor besides: the second part's
+        smallest step is 2^-9, so w_j is off by up to 2^-10 however light the key; the reference 2^R is
+        at most 2^8 of the largest p_i s_i among the tile's 128 keys (or 2^-40 of the largest of all), so
+        p_j s_j is off by up to 2^-10 of the tile's largest. What it multiplies is the code, so o is off
+        by up to the sum over tiles of 2^-10 max_i(p_i s_i) sum_j |code_j|; the sums that normalise take
+        the weights unrounded. o is then rounded once to its type.
+    """
         s = self.shape
         r = s.kv_lora_rank
         o, lse, bo, bl = [], [], [], []
@@ -170,7 +171,12 @@ class Case:
                 step = 2.0 ** -8
                 if self.fp8 and len(k):
                     sc = row_scales(s, self.rows[torch.from_numpy(self.key_slots(t))])
-                    floor = 2.0 ** -18 * (p * sc).max(1)[:, None] * (np.abs(c) / sc[:, None]).sum(0)[None]
+                    code, ps = np.abs(c) / sc[:, None], p * sc
+                    floor = 2.0 ** -50 * ps.max(1)[:, None] * code.sum(0)[None]
+                    for a0, a1 in ((0, self.prefix_len), (self.prefix_len, len(k))):   # the passes' tiles
+                        for j in range(a0, a1, 128):
+                            m = min(j + 128, a1)
+                            floor = floor + 2.0 ** -10 * ps[:, j:m].max(1)[:, None] * code[j:m].sum(0)[None]
             else:
                 e = (e.max(1) if len(k) else np.zeros(len(p))) + 64 * 2.0 ** -24
                 step = 2.0 ** -24

@@ -391,7 +391,8 @@ def test_repeats_graphs_and_other_streams_give_the_same_bits(heads, fp8):
     check(case, want, wl_)
     for _ in range(3):
         o, lse = layer.latent_attn(want_lse=True, **x)
-        assert same_bytes(o, want) and same_bytes(lse, wl_)
+        same = same_bytes(o, want) and same_bytes(lse, wl_)
+        assert same
     # a stream of its own with a workspace of its own, at the same time
     other = case.layer()
     torch.cuda.synchronize()
@@ -402,11 +403,16 @@ def test_repeats_graphs_and_other_streams_give_the_same_bits(heads, fp8):
         with torch.cuda.stream(st):
             outs.append(other.latent_attn(**x)[0])
     torch.cuda.synchronize()
-    assert all(same_bytes(o, want) for o in outs)
+    same = [same_bytes(o, want) for o in outs]
+    assert all(same)
     # two graphs that share a workspace, replayed in turn on changed inputs
     outs, graphs = [torch.empty_like(want) for _ in range(2)], []
     xs = [x, dict(x, q_abs=x["q_abs"].flip(0).contiguous(), q_pe=x["q_pe"].flip(0).contiguous(),
                   context_lens=x["context_lens"].flip(0).contiguous(), block_table=x["block_table"].flip(0).contiguous())]
+    # (the schedule cuts the flipped batch at other rows, so its bits are those of its own eager call)
+    wants = [want, layer.latent_attn(**xs[1])[0]]
+    a, _, ba, _ = case.oracle()
+    assert (np.abs(wants[1].flip(0).double().cpu().numpy() - a) <= ba).all()
     for y, o in zip(xs, outs):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
@@ -418,7 +424,8 @@ def test_repeats_graphs_and_other_streams_give_the_same_bits(heads, fp8):
         graphs[0].replay()
         graphs[1].replay()
         torch.cuda.synchronize()
-        assert same_bytes(outs[0], want) and same_bytes(outs[1], want.flip(0).contiguous())
+        same = [same_bytes(o, y) for o, y in zip(outs, wants)]
+        assert same == [True, True]
     assert mla.mla_read_device_flag(layer.ws) == 0
 
 
