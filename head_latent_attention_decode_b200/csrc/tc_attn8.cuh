@@ -11,9 +11,9 @@
 //   q_abs_h = 2^k_h (hi + lo): k_h brings the row's largest to at most 448; columns
 //     within 2^-10 of it are exact, smaller ones off by at most 2^-18 of it
 //   p: relative to a per-head reference R that follows the tiles' maxima both up
-//     and down (within 2^8 of the largest of each 128 keys), so that thousands of
+//     and down (within 2^9 of the largest of each 128 keys), so that thousands of
 //     light keys behind a heavy one keep their weight: a weight is off by 2^-8 of
-//     itself or 2^-10 of its tile's largest
+//     itself or 2^-9 of its tile's largest
 //
 // The row scale s_j = 2^k_j folds into both products: with u_hj = q_h . code_j,
 //   y_hj = scale log2(e) (s_j u_hj + q_pe_h . k_pe_j) + k_j
@@ -29,16 +29,19 @@
 //   O^T [128 latent x (hi | lo)] x 4 = codes^T . W^T  16 MMAs; codes^T is the same
 //                                                     shared-memory tile read MN-major
 // O^T stays in TMEM; it is rescaled there only when some head's reference moves.
-// A reference is set one to two octaves above the tile's largest and kept while
-// the tiles' largest stay within (R - 8, R], which for most tiles they do (a
-// window of 5 octaves moved some head's reference on most tiles: 424 us against
-// @W us for 64 sequences of 1024 to 16384 rows and 128 heads).
+// A reference is set four to five octaves above the tile's largest and kept
+// while the tiles' largest stay within [R - 9, R]; set closer, one head or
+// another moved its reference on most tiles.
 //
-// Roles: warpgroup g of NH / 16 runs the softmax of heads [16 g, 16 g + 16)
-// (thread <-> key; for a rescale and at the end thread <-> latent column); then
-// one warp each for TMA, the score MMAs and the value MMAs. S and W alternate
-// between two buffers, so the scores of tile i + 1 run during the softmax of
-// tile i and its value MMAs during the softmax of tile i + 1.
+// Roles: warpgroup g of NH / 8 runs the softmax of heads [8 g, 8 g + 8) (thread
+// <-> key; for a rescale and at the end thread <-> latent column); then one warp
+// each for TMA, the score MMAs and the value MMAs. S and W alternate between two
+// buffers, so the scores of tile i + 1 run during the softmax of tile i and its
+// value MMAs during the softmax of tile i + 1. The softmax is a chain of short
+// dependent steps, so few heads per warp and many warps hide it best.
+// The TMA warp also brings the tile's row scales (a bulk copy per box) and
+// writes what the softmax has to know of the tile, so that the softmax warps
+// touch no table.
 //
 // Schedule: the tiles of all entries (sequences; or blocks of NH query rows
 // against one shared prefix) form one list, and each CTA takes an equal
@@ -74,19 +77,19 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major =
   return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 32 lanes x 32 bit, 32 consecutive columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
+// 32 lanes x 32 bit, 8 consecutive columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
-
+// Global to shared memory, 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 struct TcAttn8Args {
   int n_ent, groups, units;   // entries; head groups; slices (grid = units x groups)
   int flat;                   // 0: entry e is sequence e, its rows e H + NH group ..; 1: query rows e NH .. against one table
@@ -112,7 +115,7 @@ constexpr int A8_MAX_ENT = 1024;   // sequences per launch (their tile prefix in
 
 template <int NH>
 struct Attn8Smem {
-  static constexpr int NWG = NH / 16;
+  static constexpr int NWG = NH / 8;
   static constexpr int NPR = NH == 16 ? 5 : 4;   // ring entries of 32 KB: two per tile
   static constexpr int QB = 2 * NH * 128;         // one k-block [2 NH x 128 B] of Q
   static constexpr int PB = 2 * NH * 128;         // one buffer of W^T [2 NH x 128 keys]
@@ -121,17 +124,18 @@ struct Attn8Smem {
   static constexpr int Q_OFF = ROPE_OFF + 2 * 16384;
   static constexpr int QPE_OFF = Q_OFF + 4 * QB;
   static constexpr int P_OFF = QPE_OFF + NH * 128;
-  // maxima [2][4 warps][NH]; per warpgroup row sums [4][16] and query scales [16]; per warp
-  // 8 - R [16] and the factors of a rescale [16]
-  static constexpr int RED_OFF = P_OFF + 2 * PB;
-  static constexpr int RED_MAX = 8 * NH, RED_WG = 64 + 16, RED_WARP = 32;
+  // row scales [2][128]; maxima [2][4 warps][NH]; per warpgroup row sums [4][8] and query scales [8];
+  // per warp 8 - R [8] and the factors of a rescale [8]
+  static constexpr int SC_OFF = P_OFF + 2 * PB;
+  static constexpr int RED_OFF = SC_OFF + 2 * 128 * 4;
+  static constexpr int RED_MAX = 8 * NH, RED_WG = 32 + 8, RED_WARP = 16;
   static constexpr int RED_FLOATS = RED_MAX + NWG * RED_WG + 4 * NWG * RED_WARP;
   static constexpr int PREF_OFF = RED_OFF + RED_FLOATS * 4;
   static constexpr int BAR_OFF = PREF_OFF + (A8_MAX_ENT + 4) * 4;
   static constexpr int SIZE = 1024 + BAR_OFF + 512;
   static constexpr int THREADS = NWG * 128 + 96;
-  // TMEM: two S buffers [(hi 16 | lo 16) per warpgroup | rotary NH], then O^T of the four latent
-  // groups [(hi 16 | lo 16) per warpgroup]
+  // TMEM: two S buffers [(hi 8 | lo 8) per warpgroup | rotary NH], then O^T of the four latent
+  // groups [(hi 8 | lo 8) per warpgroup]
   static constexpr int SB = NH == 16 ? 64 : 128;
   static constexpr int TM_O = 2 * SB;
   static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
@@ -203,6 +207,7 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
   const uint32_t fin_s = o_free + 8, fin_o = fin_s + 8;
   const uint32_t red_b = fin_o + 8;                               // [2] the warps' maxima posted
   const uint32_t wg_b = red_b + 16;                               // per warpgroup: query scales, row sums
+  int4* tile_s = (int4*)(smem + SM::BAR_OFF + 384);                // [2]: {keys in the tile, boxes loaded, last of its entry here, entry}
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 480);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 484);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -248,7 +253,7 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
     for (int i = 0; i < NPR; ++i) { mbar_init(full_b + 8 * i, 1); mbar_init(empty_b + 8 * i, 1); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, 1);
+      mbar_init(rempty + 8 * i, 1 + 4 * NWG);   // read by the MMAs, and the scales by the softmax warps
       mbar_init(s_full + 8 * i, 1);
       mbar_init(s_free + 8 * i, 4 * NWG);
       mbar_init(p_full + 8 * i, 4 * NWG);
@@ -279,28 +284,43 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
     const int nb = 128 / a.box, none = max(a.n_blocks, 1);   // a block id beyond the map
     Walk8 w = w0;
     w.start(a, g0);
-    // this lane's box of the walk's tile: its block id (out of range: the load fills zeros)
-    auto box_block = [&](const Walk8& v) {
+    // this lane's box of the walk's tile, one tile ahead of its use: the block id as loaded (so that
+    // nothing waits for it) and the first row within the block
+    int raw = 0, off = 0;
+    bool has = false;
+    auto fetch_box = [&](const Walk8& v) {
       const int j = 128 * v.lt + a.box * lane;
-      if (lane >= nb || j >= v.len) return none;
-      const int b = a.table[v.e * a.table_stride + j / a.bs];
-      if (b >= 0 && b < a.n_blocks) return b;
-      if (hg == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
-      return none;
+      has = lane < nb && j < v.len;
+      if (has) {
+        const int at = j / a.bs;
+        off = j - at * a.bs;
+        raw = a.table[v.e * a.table_stride + at];
+      }
     };
-    int blk = box_block(w), i = 0;
+    fetch_box(w);
+    int i = 0;
     bool ok = true;
     for (; i < N; ++i) {
-      const int j = 128 * w.lt + a.box * lane;
-      const int off = j % a.bs, cur = blk;
+      const bool good = has && raw >= 0 && raw < a.n_blocks;
+      if (has && !good && hg == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
+      const int cur = good ? raw : none, row0 = good ? off : 0;   // a block beyond the map: the load fills zeros
+      const uint32_t boxes = __ballot_sync(0xffffffffu, good);
+      const int4 tile = make_int4(min(128, w.len - 128 * w.lt), (int)boxes, i == N - 1 || w.seg_last(), w.e);
       if (i + 1 < N) {
         w.next(a);
-        blk = box_block(w);   // one tile ahead
+        fetch_box(w);
       }
+      const uint32_t rb = rfull + 8 * (i & 1);
       if (!mbar_wait_warp(rempty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
-      if (lane == 0) mbar_arrive_expect_tx(rfull + 8 * (i & 1), 16384);
+      if (lane == 0) {
+        tile_s[i & 1] = tile;
+        mbar_arrive_expect_tx(rb, 16384 + __popc(boxes) * a.box * 4);
+      }
       __syncwarp();
-      if (lane < nb) tma_load_3d(rope_s + (i & 1) * 16384 + a.box * lane * 128, &tm_rope, rfull + 8 * (i & 1), 0, off, cur);
+      if (lane < nb) tma_load_3d(rope_s + (i & 1) * 16384 + a.box * lane * 128, &tm_rope, rb, 0, row0, cur);
+      if (good)
+        bulk_load(sbase + SM::SC_OFF + (i & 1) * 512 + a.box * lane * 4,
+                  a.cache + (long long)cur * a.block_bytes + a.sc_off + row0 * 4, a.box * 4, rb);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int e = 2 * i + g, slot = e % NPR;
@@ -309,7 +329,7 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         __syncwarp();
         if (lane < nb)
           tma_load_5d(ring_s + slot * 32768 + (a.box * lane / 8) * 2048, &tm_codes, full_b + 8 * slot, 0, 0, 2 * g,
-                      off / 8, cur);
+                      row0 / 8, cur);
       }
       if (!ok) break;
     }
@@ -337,17 +357,16 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       constexpr uint32_t id_u = idesc_e4m3(128, 2 * NH), id_r = idesc_bf16(128, NH);
       const uint64_t d_ring = sdesc_sw128_sbo(ring_s, 2048), d_rope = sdesc_sw128(rope_s);
       const uint64_t d_q = sdesc_sw128(q_s), d_qpe = sdesc_sw128(qpe_s);
-      Walk8 w = w0;
-      w.start(a, g0);
       int ks = 0;
+      bool first = true;
       for (int i = 0; i < N; ++i) {
         const int b = i & 1;
-        const bool first = i == 0 || w.lt == 0;
         if ((first && !mbar_wait(q_ready, ks & 1, abort_word, a.flag)) ||
             !mbar_wait(s_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag) ||
             !mbar_wait(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag))
           break;
         if (first) ++ks;
+        first = tile_s[b].z != 0;   // the next tile begins another entry
         tc_fence_after();
         const uint32_t d = tmem + SM::SB * b;
 #pragma unroll
@@ -370,7 +389,6 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         }
         if (!ok) break;
         mma_commit(s_full + 8 * b);
-        if (i + 1 < N) w.next(a);
       }
       mma_commit(fin_s);
       const uint64_t t0 = global_timer_ns();
@@ -421,33 +439,34 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     float* red = (float*)(smem + SM::RED_OFF);                       // [2][4][NH]
-    float* rl = red + SM::RED_MAX + wg * SM::RED_WG;                 // [4][16]
-    float* slq = rl + 64;                                            // [16] scale log2(e) 2^k_h
-    float* ref_w = red + SM::RED_MAX + NWG * SM::RED_WG + warp * SM::RED_WARP;   // [16] 8 - R, this warp's copy
-    float* al_w = ref_w + 16;                                        // [16] factors of the last rescale
+    float* rl = red + SM::RED_MAX + wg * SM::RED_WG;                 // [4][8]
+    float* slq = rl + 32;                                            // [8] scale log2(e) 2^k_h
+    float* ref_w = red + SM::RED_MAX + NWG * SM::RED_WG + warp * SM::RED_WARP;   // [8] 8 - R, this warp's copy
+    float* al_w = ref_w + 8;                                         // [8] factors of the last rescale
     const uint32_t qs_b = wg_b + 16 * wg, l_b = qs_b + 8;
     int kq = 0, kl = 0;   // phases of qs_b and l_b
 
-    // The 16 heads' query rows of entry e in two E4M3 parts: eight threads per head, 64 columns each.
+    // The 8 heads' query rows of entry e in two E4M3 parts: 16 threads per head, 32 columns each.
     auto load_q = [&](int e) -> bool {
-      const int hh = row >> 3, sub = row & 7, hd = 16 * wg + hh;
+      const int hh = row >> 4, sub = row & 15, hd = 8 * wg + hh;
       const long long r0 = a.flat ? (long long)e * NH : (long long)e * a.H + (long long)hg * NH;
       const bool live = a.flat ? r0 + hd < a.rows_total : hg * NH + hd < a.H;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (live ? r0 + hd : 0) * 512 + 64 * sub);
-      uint4 v[8];
+      const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (live ? r0 + hd : 0) * 512 + 32 * sub);
+      uint4 v[4];
       float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
-      const uint4 pe = live ? reinterpret_cast<const uint4*>(a.q_pe + (r0 + hd) * 64)[sub] : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 4; ++k) v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
+      uint4 pe = make_uint4(0, 0, 0, 0);
+      if (live && sub < 8) pe = reinterpret_cast<const uint4*>(a.q_pe + (r0 + hd) * 64)[sub];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           m = fmaxf(m, fmaxf(finite_abs(__uint_as_float(u[j] << 16)), finite_abs(__uint_as_float(u[j] & 0xFFFF0000u))));
       }
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       // as a cache row's exponent, over bf16's whole range
       int k = 0;
       if (m > 0.f) {
@@ -457,9 +476,9 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       }
       const float inv = exp2_int(-k);
       if (sub == 0) slq[hh] = a.scale_log2 * exp2_int(k);
-      uint8_t* qb = smem + SM::Q_OFF + (sub >> 1) * SM::QB;   // columns [128 j, 128 j + 128) are k-block j
+      uint8_t* qb = smem + SM::Q_OFF + (sub >> 2) * SM::QB;   // columns [128 j, 128 j + 128) are k-block j
 #pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
+      for (int ch = 0; ch < 2; ++ch) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -472,85 +491,58 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
           hi[j] = (uint32_t)a0 | ((uint32_t)a1 << 16);
           lo[j] = (uint32_t)e4m3x2_sat(f0 - g0v.x, f1 - g0v.y) | ((uint32_t)e4m3x2_sat(f2 - g1v.x, f3 - g1v.y) << 16);
         }
-        const int chunk = ((sub & 1) * 4 + ch) ^ (hd & 7);
-        *reinterpret_cast<uint4*>(qb + (32 * wg + hh) * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(qb + (32 * wg + 16 + hh) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int chunk = ((sub & 3) * 2 + ch) ^ hh;
+        *reinterpret_cast<uint4*>(qb + (16 * wg + hh) * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(qb + (16 * wg + 8 + hh) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-      *reinterpret_cast<uint4*>(smem + SM::QPE_OFF + hd * 128 + 16 * (sub ^ (hd & 7))) = pe;
+      if (sub < 8) *reinterpret_cast<uint4*>(smem + SM::QPE_OFF + hd * 128 + 16 * (sub ^ hh)) = pe;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) { mbar_arrive(q_ready); mbar_arrive(qs_b); }
       return mbar_wait_warp(qs_b, (kq++) & 1, abort_word, a.flag);   // the scales are there for every warp
     };
-    // This thread's key, in flight ahead of its tile: the block id as loaded (two tiles ahead, so that
-    // nothing waits for it) and the place within the block, then the row scale (one tile ahead).
-    int raw = -1, off = 0;
-    auto fetch_block = [&](const Walk8& v) {
-      const int j = 128 * v.lt + row;
-      raw = -1;
-      if (j < v.len) {
-        const int at = j / a.bs;
-        off = j - at * a.bs;
-        raw = a.table[v.e * a.table_stride + at];
-      }
-    };
-    float s_next = 0.f;
-    bool valid_next = false;
-    auto fetch_scale = [&]() {
-      valid_next = raw >= 0 && raw < a.n_blocks;
-      s_next = 0.f;
-      if (valid_next)
-        s_next = reinterpret_cast<const float*>(a.cache + (long long)raw * a.block_bytes + a.sc_off)[off];
-    };
 
-    float l[16];
+    const int box_log = 31 - __clz(a.box);
+    float l[8];
 #pragma unroll
-    for (int h = 0; h < 16; ++h) l[h] = 0.f;
+    for (int h = 0; h < 8; ++h) l[h] = 0.f;
     float R = -INFINITY, top = -INFINITY;   // lane h: head h's reference and the largest seen (h < NH)
-    if (lane < 16) ref_w[lane] = 8.f;
-    Walk8 w = w0;
-    w.start(a, g0);
-    Walk8 w1 = w;
-    fetch_block(w);
-    fetch_scale();
-    w1.next(a);
-    if (N > 1) fetch_block(w1);
-    bool ok = load_q(w.e);
-    bool first = true;
+    if (lane < 8) ref_w[lane] = 8.f;
+    bool ok, first = true;
+    {
+      Walk8 w = w0;
+      w.start(a, g0);
+      ok = load_q(w.e);
+    }
     for (int i = 0; i < N && ok; ++i) {
       const int b = i & 1;
-      const float sj = s_next;
-      const bool valid = valid_next;
-      const int e = w.e;
-      const bool last = i == N - 1 || w.seg_last();
-      if (i + 1 < N) {
-        fetch_scale();
-        w = w1;
-        w1.next(a);
-        if (i + 2 < N) fetch_block(w1);
-      }
-      if (!mbar_wait_warp(s_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
-      tc_fence_after();
+      if (!mbar_wait_warp(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      const int4 tile = tile_s[b];
+      const float sj = *reinterpret_cast<const float*>(smem + SM::SC_OFF + b * 512 + row * 4);
+      const bool valid = row < tile.x && (((uint32_t)tile.y >> (row >> box_log)) & 1u);
+      const bool last = tile.z != 0;
       // 2^k_j; rows never written (scale 0) count as zero rows
       const int kj = max(C8_KMIN, min(C8_KMAX, (int)(__float_as_uint(sj) >> 23) - 127));
-      float y[16];
+      if (!mbar_wait_warp(s_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      tc_fence_after();
+      float y[8];
       {
-        uint32_t u[32], rp[16];
+        uint32_t u[16], rp[8];
         const uint32_t sa = tmem + SM::SB * b + lane_base;
-        tmem_ld32(sa + 32 * wg, u);
-        tmem_ld16(sa + 2 * NH + 16 * wg, rp);
+        tmem_ld16(sa + 16 * wg, u);
+        tmem_ld8(sa + 2 * NH + 8 * wg, rp);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free + 8 * b);
+        if (lane == 0) { mbar_arrive(s_free + 8 * b); mbar_arrive(rempty + 8 * b); }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const float4 s4 = *reinterpret_cast<const float4*>(slq + 4 * k);
           const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int h = 4 * k + j;
-            const float uu = __uint_as_float(u[h]) + __uint_as_float(u[16 + h]);
+            const float uu = __uint_as_float(u[h]) + __uint_as_float(u[8 + h]);
             const float r = fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj);
             y[h] = valid ? fmaf(uu, sj * sv[j], r) : -INFINITY;
           }
@@ -558,14 +550,13 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       }
       // the tile's largest per head: within the warp, then over the four warps by lane h for head h
       {
-        float mx[16];
+        float mx[8];
 #pragma unroll
-        for (int h = 0; h < 16; ++h) mx[h] = warp_max_f32(y[h]);
+        for (int h = 0; h < 8; ++h) mx[h] = warp_max_f32(y[h]);
         if (lane == 0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<float4*>(red + (b * 4 + q) * NH + 16 * wg + 4 * k) =
-                make_float4(mx[4 * k], mx[4 * k + 1], mx[4 * k + 2], mx[4 * k + 3]);
+          float4* rr = reinterpret_cast<float4*>(red + (b * 4 + q) * NH + 8 * wg);
+          rr[0] = make_float4(mx[0], mx[1], mx[2], mx[3]);
+          rr[1] = make_float4(mx[4], mx[5], mx[6], mx[7]);
         }
       }
       __syncwarp();
@@ -577,44 +568,46 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
           const float* rr = red + b * 4 * NH + lane;
           m = fmaxf(fmaxf(rr[0], rr[NH]), fmaxf(rr[2 * NH], rr[3 * NH]));
         }
-        // Move R when the tile's largest leaves (R - 8, R]; not below 2^-40 of the largest seen, where a
-        // tile no longer counts (and 2^(old - new) stays far from overflow). Every warp decides alike.
+        // Move R when some head's largest leaves [R - 9, R], and with it the heads that are about to;
+        // not below 2^-40 of the largest seen, where a tile no longer counts (and 2^(old - new) stays
+        // far from overflow). Every warp decides alike.
         top = fmaxf(top, m);
-        const float want = fmaxf(ceilf(m) + 1.f, top - 40.f);
-        const bool move = m > -INFINITY && (m > R || want < R - 6.f);
+        const float want = fmaxf(ceilf(m) + 5.f, top - 40.f);
+        const bool move = m > -INFINITY && (m > R || (m < R - 9.f && want < R));
         if (__any_sync(0xffffffffu, move)) {
           float al = 1.f;
-          if (move) {
+          if (move || m > R - 2.f) {
             if (R > -INFINITY) al = ex2_approx(R - want);
             R = want;
           }
-          if (lane < NH && (lane >> 4) == wg) {
-            ref_w[lane & 15] = R == -INFINITY ? 8.f : 8.f - R;
-            al_w[lane & 15] = al;
+          if ((lane >> 3) == wg) {
+            ref_w[lane & 7] = R == -INFINITY ? 8.f : 8.f - R;
+            al_w[lane & 7] = al;
           }
           __syncwarp();
           if (!first) {
             // P.V(i - 1) has to be complete; its buffer's barrier says so, and nothing later is under way
             if (!mbar_wait_warp(p_free + 8 * (b ^ 1), ((i - 1) >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
             tc_fence_after();
-            float f[16];
+            float f[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
               const float4 v = *reinterpret_cast<const float4*>(al_w + 4 * k);
               f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
             }
 #pragma unroll
-            for (int h = 0; h < 16; ++h) l[h] *= f[h];
+            for (int h = 0; h < 8; ++h) l[h] *= f[h];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < 4; g += 2) {
               uint32_t o[32];
-              const uint32_t oa = tmem + SM::TM_O + g * 2 * NH + 32 * wg + lane_base;
-              tmem_ld32(oa, o);
+              const uint32_t oa = tmem + SM::TM_O + g * 2 * NH + 16 * wg + lane_base;
+              tmem_ld16(oa, o);
+              tmem_ld16(oa + 2 * NH, o + 16);
               tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * f[h & 15]);
+              for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * f[h & 7]);
               tmem_st16(oa, o);
-              tmem_st16(oa + 16, o + 16);
+              tmem_st16(oa + 2 * NH, o + 16);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -626,9 +619,9 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       if (!mbar_wait_warp(p_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
       const float un = exp2_int(-kj);
       {
-        uint8_t* pb = smem + SM::P_OFF + b * SM::PB + wg * 32 * 128 + (row & 15);
+        uint8_t* pb = smem + SM::P_OFF + b * SM::PB + wg * 16 * 128 + (row & 15);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           const float4 r4 = *reinterpret_cast<const float4*>(ref_w + 4 * k);
           const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
@@ -640,41 +633,47 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
             const uint16_t c_hi = e4m3x2_sat(e0, e1);
             const float2 back = e4m3x2_f32(c_hi);
             const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
-            uint8_t* p0 = pb + h * 128 + (((row >> 4) ^ (h & 7)) << 4);
-            uint8_t* p1 = pb + (h + 1) * 128 + (((row >> 4) ^ ((h + 1) & 7)) << 4);
+            uint8_t* p0 = pb + h * 128 + (((row >> 4) ^ h) << 4);
+            uint8_t* p1 = pb + (h + 1) * 128 + (((row >> 4) ^ (h + 1)) << 4);
             p0[0] = (uint8_t)c_hi;
             p1[0] = (uint8_t)(c_hi >> 8);
-            p0[16 * 128] = (uint8_t)c_lo;
-            p1[16 * 128] = (uint8_t)(c_lo >> 8);
+            p0[8 * 128] = (uint8_t)c_lo;
+            p1[8 * 128] = (uint8_t)(c_lo >> 8);
           }
         }
       }
       if (!valid) {
-        // rows past the end may hold anything (even NaN codes); their weight is 0, but 0 * NaN is not
+        // rows past the end may hold anything (even NaN codes); their weight is 0, but 0 * NaN is not.
+        // Four 128-byte runs per row, shared out over the warpgroups
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (NWG == 2 && g != wg) continue;
-          uint8_t* rp = smem + SM::RING_OFF + ((2 * i + g) % NPR) * 32768 + (row >> 3) * 2048 + (row & 7) * 128;
+        for (int g = 0; g < 4; ++g) {
+          if (g % NWG != wg) continue;
+          uint8_t* rp = smem + SM::RING_OFF + ((2 * i + (g >> 1)) % NPR) * 32768 + (row >> 3) * 2048 + (g & 1) * 1024 +
+                        (row & 7) * 128;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            *reinterpret_cast<uint4*>(rp + 16 * k) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(rp + 1024 + 16 * k) = make_uint4(0, 0, 0, 0);
-          }
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(rp + 16 * k) = make_uint4(0, 0, 0, 0);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full + 8 * b);
       if (last) {
-        // the scores of this entry are all read: the next entry's query may replace its own
-        if (i + 1 < N && !load_q(w.e)) { ok = false; break; }
+        // the scores of this entry are all read: the next entry's query may replace its own. What the
+        // TMA warp says of the next tile comes first
+        const int e = tile.w;
+        if (i + 1 < N) {
+          if (!mbar_wait_warp(rfull + 8 * (b ^ 1), ((i + 1) >> 1) & 1, abort_word, a.flag) || !load_q(tile_s[b ^ 1].w)) {
+            ok = false;
+            break;
+          }
+        }
         const long long unit = (long long)hg * (a.units + a.n_ent) + c + e;
         const long long r0 = a.flat ? (long long)e * NH : (long long)hg * NH;
-        const int live = (int)min((long long)NH, (a.flat ? a.rows_total : (long long)a.H) - r0) - 16 * wg;
+        const int live = (int)min((long long)NH, (a.flat ? a.rows_total : (long long)a.H) - r0) - 8 * wg;
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
+        for (int h = 0; h < 8; ++h) {
           const float v = warp_sum(l[h]);
-          if (lane == 0) rl[q * 16 + h] = v;
+          if (lane == 0) rl[q * 8 + h] = v;
           l[h] = 0.f;
         }
         __syncwarp();
@@ -682,28 +681,29 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         // thread <-> latent column
         if (!mbar_wait_warp(p_free + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
         tc_fence_after();
-        float* po = a.part_o + (unit * NH + 16 * wg) * 512 + row;
+        float* po = a.part_o + (unit * NH + 8 * wg) * 512 + row;
+#pragma unroll
         for (int g = 0; g < 4; ++g) {
-          uint32_t o[32];
-          tmem_ld32(tmem + SM::TM_O + g * 2 * NH + 32 * wg + lane_base, o);
+          uint32_t o[16];
+          tmem_ld16(tmem + SM::TM_O + g * 2 * NH + 16 * wg + lane_base, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < 16; ++h)
-            if (h < live) po[h * 512 + 128 * g] = __uint_as_float(o[h]) + __uint_as_float(o[16 + h]);
+          for (int h = 0; h < 8; ++h)
+            if (h < live) po[h * 512 + 128 * g] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
         if (!mbar_wait_warp(l_b, (kl++) & 1, abort_word, a.flag)) { ok = false; break; }
-        if (q == 0 && lane < NH && (lane >> 4) == wg) {
-          const int h = lane & 15;
+        if (q == 0 && (lane >> 3) == wg) {
+          const int h = lane & 7;
           if (h < live)   // natural-log units; w carries the factor 2^8
-            *reinterpret_cast<float2*>(a.part_ml + (unit * NH + 16 * wg + h) * 2) =
-                make_float2((R - 8.f) * 0.69314718055994531f, rl[h] + rl[16 + h] + rl[32 + h] + rl[48 + h]);
+            *reinterpret_cast<float2*>(a.part_ml + (unit * NH + 8 * wg + h) * 2) =
+                make_float2((R - 8.f) * 0.69314718055994531f, rl[h] + rl[8 + h] + rl[16 + h] + rl[24 + h]);
         }
         R = -INFINITY;
         top = -INFINITY;
-        if (lane < 16) ref_w[lane] = 8.f;
+        if (lane < 8) ref_w[lane] = 8.f;
         __syncwarp();
       }
     }

@@ -145,9 +145,9 @@ class Case:
           fp32 act: exponentials and sums, 64 2^-24.
         The two-part weights w_j = 2^8 p_j s_j / 2^R have an absolute floor besides: the second part's
         smallest step is 2^-9, so w_j is off by up to 2^-10 however light the key; the reference 2^R is
-        at most 2^8 of the largest p_i s_i among the tile's 128 keys (or 2^-40 of the largest of all), so
-        p_j s_j is off by up to 2^-10 of the tile's largest. What it multiplies is the code, so o is off
-        by up to the sum over tiles of 2^-10 max_i(p_i s_i) sum_j |code_j|; the sums that normalise take
+        at most 2^9 of the largest p_i s_i among the tile's 128 keys (or 2^-40 of the largest of all), so
+        p_j s_j is off by up to 2^-9 of the tile's largest. What it multiplies is the code, so o is off
+        by up to the sum over tiles of 2^-9 max_i(p_i s_i) sum_j |code_j|; the sums that normalise take
         the weights unrounded. o is then rounded once to its type.
     """
         s = self.shape
@@ -176,7 +176,7 @@ class Case:
                     for a0, a1 in ((0, self.prefix_len), (self.prefix_len, len(k))):   # the passes' tiles
                         for j in range(a0, a1, 128):
                             m = min(j + 128, a1)
-                            floor = floor + 2.0 ** -10 * ps[:, j:m].max(1)[:, None] * code[j:m].sum(0)[None]
+                            floor = floor + 2.0 ** -9 * ps[:, j:m].max(1)[:, None] * code[j:m].sum(0)[None]
             else:
                 e = (e.max(1) if len(k) else np.zeros(len(p))) + 64 * 2.0 ** -24
                 step = 2.0 ** -24
