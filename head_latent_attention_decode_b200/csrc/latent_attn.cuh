@@ -87,24 +87,24 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(MergeArgs p) {
   cnt[0] = min(cnt[0], MERGE_MAX);
   const int total = min(cnt[0] + cnt[1], MERGE_MAX);
   if (warp < 2) {   // warp w: the weights from (m, l) copy w
-    float M = -INFINITY;
-    for (int i = lane; i < total; i += 32) {
+    auto stats = [&](int i) {
       const int k = i >= cnt[0];
       const MergeSrc& s = p.src[k];
-      const float* ml = s.ml + (warp && s.half ? s.ml_r : 0) + ((unit[k] + i - (k ? cnt[0] : 0)) * s.rows + row[k]) * 2;
-      const float2 v = *reinterpret_cast<const float2*>(ml);
-      if (v.y > 0.f || v.y != v.y) M = fmaxf(M, v.x);
+      const long long at = (unit[k] + i - (k ? cnt[0] : 0)) * s.rows + row[k];
+      return *reinterpret_cast<const float2*>(s.ml + (warp && s.half ? s.ml_r : 0) + at * 2);
+    };
+    float M = -INFINITY;
+    for (int i = lane; i < total; i += 32) {
+      const float2 v = stats(i);
+      if (v.y > 0.f) M = fmaxf(M, v.x);
     }
     M = warp_max(M);
     const float z = p.sink ? p.sink[h] : -INFINITY;
     M = fmaxf(M, z);
     float den = 0.f;
     for (int i = lane; i < total; i += 32) {
-      const int k = i >= cnt[0];
-      const MergeSrc& s = p.src[k];
-      const float* ml = s.ml + (warp && s.half ? s.ml_r : 0) + ((unit[k] + i - (k ? cnt[0] : 0)) * s.rows + row[k]) * 2;
-      const float2 v = *reinterpret_cast<const float2*>(ml);
-      const float w = (v.y > 0.f) ? __expf(v.x - M) : (v.y != v.y ? v.y : 0.f);   // a NaN sum stays NaN
+      const float2 v = stats(i);
+      const float w = v.y > 0.f ? __expf(v.x - M) : (v.y != v.y ? v.y : 0.f);   // a NaN sum stays NaN
       wsh[warp][i] = w;
       den += w == 0.f ? 0.f : w * v.y;
     }
@@ -164,78 +164,79 @@ struct LatentCall {
 };
 
 // Which kernels a call takes, how many tokens at a time, and where their partials lie.
+enum LatentOwn { OWN_SIMT, OWN_TC16, OWN_FEW8, OWN_HEADS8 };     // the own rows
+enum LatentPre { PRE_NONE, PRE_HEADS16, PRE_FEW8, PRE_HEADS8 };  // the prefix
 struct LatentPlan {
-  int tc8, tc16;           // tensor cores: the 8-bit kernel; the 16-bit cache's kernels
-  int chunk;               // tokens per pass
-  int splits;              // CUDA cores: splits of the keys
-  int NH, groups, units;   // tc8: rows per CTA, head groups and slices of the own pass
-  int NHp, ents_p, units_p;   // rows per entry, entries and slices of the prefix pass
+  int own, pre, chunk;     // chunk: tokens per pass
+  int splits;              // OWN_SIMT, OWN_TC16: splits of the keys
+  int units, units_p;      // slices of the tile list
+  int rows, rows_p;        // query rows per partial (own: per head group; prefix: per entry)
+  int groups, ents_p;      // OWN_FEW8: head groups; prefix entries
   size_t o, ml, seg, o_p, ml_p, seg_p, total;
 };
 
 static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads;
-  const int sms = h->tc.num_sms > 0 ? h->tc.num_sms : 148;
+  const int sms = h->tc.num_sms > 0 ? h->tc.num_sms : 148, pairs = sms / 2 > 0 ? sms / 2 : 1;
   LatentPlan w{};
   size_t off = 0;
   auto put = [&](size_t b) { size_t o = off; off = align_up(off + b, 256); return o; };
-  // DeepSeek latent, blocks of a multiple of 16 rows (a TMA box is 16, 32 or 64 rows of one block)
-  w.tc8 = h->cache8 && h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64 && c.block_size % 16 == 0;
-  // the kernels of the 16-bit cache: the same latent, boxes of 64 rows
-  w.tc16 = !h->cache8 && h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64 && c.block_size % 64 == 0 &&
-           H <= 128;
-  if (w.tc8) {
-    // the tile list of a pass is counted in int
-    const long long tiles = cdiv(max_ctx, 128), tiles_p = cdiv(prefix_len, 128);
-    long long most = A8_MAX_ENT;
-    if (tiles * most > (1 << 30)) most = (1 << 30) / tiles;
-    if (tiles_p > 0 && tiles_p * cdiv(most * H, 16) > (1 << 30)) most = (1 << 30) / tiles_p * 16 / H - 1;
-    w.chunk = (int)(n < most ? n : (most < 1 ? 1 : most));
-    w.NH = H <= 16 ? 16 : 32;
-    w.groups = (int)cdiv(H, w.NH);
+  // the tensor-core kernels: the DeepSeek latent, TMA boxes of whole parts of a block
+  const bool tc = h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64;
+  const bool b64 = c.block_size % 64 == 0;
+  if (tc && h->cache8 && c.block_size % 16 == 0) {
+    // Per 128 keys the few-head kernel takes about 5 k cycles of one SM for every 16 heads, the
+    // head-major one about 5.6 k of two SMs whatever the number of heads up to 128 (blocks of 64 rows only)
+    w.own = b64 && H > 32 && H <= 128 ? OWN_HEADS8 : OWN_FEW8;
+    w.pre = prefix_len <= 0 ? PRE_NONE : (b64 && n * H > 32 ? PRE_HEADS8 : PRE_FEW8);
+  } else if (tc && !h->cache8 && b64 && H <= 128) {
+    w.own = OWN_TC16;
+    w.pre = prefix_len > 0 ? PRE_HEADS16 : PRE_NONE;
+  }
+  // tokens per pass: the kernels' entries (sequences; blocks of query rows) and tile lists
+  long long most = n;
+  if (w.own == OWN_FEW8) most = A8_MAX_ENT;
+  if (w.own == OWN_HEADS8 || (w.own == OWN_TC16 && H > 32)) most = ATT_MAX_SEQ;
+  if ((w.pre == PRE_HEADS16 || w.pre == PRE_HEADS8) && most * H > ATT_MAX_SEQ * 128LL) most = ATT_MAX_SEQ * 128LL / H;
+  if (w.own != OWN_SIMT) {   // tiles are counted in int
+    const long long tiles = cdiv(max_ctx, 64), tiles_p = cdiv(prefix_len, 64) * cdiv(H, 16);
+    const long long fit = (1 << 30) / (tiles > tiles_p ? tiles : tiles_p);
+    if (most > fit) most = fit > 0 ? fit : 1;
+  }
+  w.chunk = (int)(n < most ? n : most);
+  if (w.own == OWN_FEW8) {
+    w.rows = 16;
+    w.groups = (int)cdiv(H, 16);
     w.units = sms / w.groups > 0 ? sms / w.groups : 1;
-    const size_t rows = (size_t)w.groups * (w.units + w.chunk) * w.NH;
+    const size_t rows = (size_t)w.groups * (w.units + w.chunk) * 16;
     w.o = put(rows * 512 * 4);
     w.ml = put(rows * 2 * 4);
     w.seg = put((size_t)w.chunk * 8);
-    if (prefix_len > 0) {
-      const long long q = (long long)w.chunk * H;
-      w.NHp = q <= 16 ? 16 : 32;
-      w.ents_p = (int)cdiv(q, w.NHp);
-      w.units_p = sms;
-      const size_t rows_p = (size_t)(w.units_p + w.ents_p) * w.NHp;
-      w.o_p = put(rows_p * 512 * 4);
-      w.ml_p = put(rows_p * 2 * 4);
-      w.seg_p = put((size_t)w.ents_p * 8);
-    }
-  } else if (w.tc16) {
-    // the kernels' tile prefix holds ATT_MAX_SEQ entries: sequences (33 heads or more), or
-    // blocks of 128 query rows
-    const long long most = H <= 32 ? ATT_MAX_SEQ * 128 / H : ATT_MAX_SEQ;
-    w.chunk = (int)(n < most ? n : most);
-    const long long s = cdiv(max_ctx, 256);
-    w.splits = s < 2 ? 2 : (s > 16 ? 16 : (int)s);
-    const size_t rows = (size_t)w.chunk * w.splits * H;
+  } else if (w.own == OWN_HEADS8) {
+    w.rows = H;
+    w.units = pairs;
+    const size_t rows = (size_t)(pairs + w.chunk) * H;
     w.o = put(rows * 512 * 4);
     w.ml = put(rows * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
-    w.seg = put((size_t)w.chunk * 4);
-    if (prefix_len > 0) {
-      w.NHp = 128;
-      w.ents_p = (int)cdiv((long long)w.chunk * H, 128);
-      w.units_p = sms / 2 > 0 ? sms / 2 : 1;
-      const size_t rows_p = (size_t)(w.units_p + w.ents_p) * 128;
-      w.o_p = put(rows_p * 512 * 4);
-      w.ml_p = put(rows_p * 2 * 4 * 2);
-      w.seg_p = put((size_t)w.ents_p * 8);
-    }
+    w.seg = put((size_t)w.chunk * 8);
   } else {
-    w.chunk = (int)n;
-    const long long s = cdiv((long long)prefix_len + max_ctx, 256);
+    const long long s = cdiv((long long)(w.own == OWN_SIMT ? prefix_len : 0) + max_ctx, 256);
+    w.rows = H;
     w.splits = s < 2 ? 2 : (s > 16 ? 16 : (int)s);
-    const size_t rows = (size_t)n * w.splits * H;
+    const size_t rows = (size_t)w.chunk * w.splits * H;
     w.o = put(rows * c.kv_lora_rank * 4);
-    w.ml = put(rows * 2 * 4);
+    w.ml = put(rows * 2 * 4 * 2);
+    w.seg = put((size_t)w.chunk * 4);
+  }
+  if (w.pre != PRE_NONE) {
+    w.rows_p = w.pre == PRE_FEW8 ? 16 : 128;
+    w.ents_p = (int)cdiv((long long)w.chunk * H, w.rows_p);
+    w.units_p = w.pre == PRE_FEW8 ? sms : pairs;
+    const size_t rows = (size_t)(w.units_p + w.ents_p) * w.rows_p;
+    w.o_p = put(rows * 512 * 4);
+    w.ml_p = put(rows * 2 * 4 * 2);
+    w.seg_p = put((size_t)w.ents_p * 8);
   }
   w.total = off;
   return w;
@@ -278,21 +279,23 @@ static int make_maps_cache8(CUtensorMap* codes, CUtensorMap* rope, const void* b
   return r == CUDA_SUCCESS ? MLA_OK : MLA_ERR_CUDA;
 }
 
-template <int NH>
 static void launch_attn8(const CUtensorMap& codes, const CUtensorMap& rope, const TcAttn8Args& a, cudaStream_t s) {
   static std::atomic<bool> attr[64];
-  set_smem_once(attr, tc_attn8_kernel<NH>, Attn8Smem<NH>::SIZE);
-  launch_pdl(tc_attn8_kernel<NH>, (unsigned)(a.units * a.groups), Attn8Smem<NH>::THREADS, Attn8Smem<NH>::SIZE, s, codes,
-             rope, a);
+  set_smem_once(attr, tc_attn8_kernel, Attn8Smem::SIZE);
+  launch_pdl(tc_attn8_kernel, (unsigned)(a.units * a.groups), A8_THREADS, Attn8Smem::SIZE, s, codes, rope, a);
   mla_count_launch(1);
 }
 
-// One pass of at most plan.chunk tokens on the 8-bit tensor-core kernel.
-static int latent_pass8(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
-                        int* flag, cudaStream_t s) {
+// Largest part of a block that is a TMA box.
+static int cache8_box(int bs) { return bs % 64 == 0 ? 64 : (bs % 32 == 0 ? 32 : 16); }
+
+// A pass on the few-head 8-bit kernel: over the prefix (blocks of 16 query rows against its one
+// table) or over each sequence's own rows.
+static int pass_few8(const mla_handle* h, const LatentPlan& w, const LatentCall& a, bool pre, MergeArgs* m, char* scratch,
+                     int* flag, cudaStream_t s) {
   const mla_config& c = h->cfg;
   const Cache8 c8 = cache8_of(h);
-  const int box = c.block_size % 64 == 0 ? 64 : (c.block_size % 32 == 0 ? 32 : 16);
+  const int box = cache8_box(c.block_size);
   CUtensorMap codes, rope;
   const int st = make_maps_cache8(&codes, &rope, a.cache, c8, a.n_blocks > 0 ? a.n_blocks : 1, box);
   if (st != MLA_OK) return st;
@@ -303,83 +306,103 @@ static int latent_pass8(const mla_handle* h, const LatentPlan& w, const LatentCa
   k.q_abs = (const bf16*)a.q_abs; k.q_pe = (const bf16*)a.q_pe;
   k.scale_log2 = h->scale * 1.4426950408889634f;
   k.flag = flag;
-  if (a.prefix_len > 0) {
-    TcAttn8Args p = k;
-    p.flat = 1; p.groups = 1; p.units = w.units_p;
-    p.n_ent = (int)cdiv(p.rows_total, w.NHp);
-    p.len = a.prefix_len; p.table = a.prefix_table;
-    p.part_o = (float*)(scratch + w.o_p); p.part_ml = (float*)(scratch + w.ml_p); p.seg = (int2*)(scratch + w.seg_p);
-    mla_timer_begin("attn_prefix", s);
-    if (w.NHp == 16) launch_attn8<16>(codes, rope, p, s);
-    else launch_attn8<32>(codes, rope, p, s);
-    mla_timer_end("attn_prefix", s);
-    MergeSrc& q = m->src[m->n_src++];
-    q.o = p.part_o; q.ml = p.part_ml; q.seg = p.seg; q.rows = w.NHp; q.flat = 1;
-  }
-  k.groups = w.groups; k.units = w.units; k.n_ent = a.n;
-  k.ctx = a.ctx; k.min_ctx = m->min_ctx; k.max_ctx = a.max_ctx;
-  k.table = a.table; k.table_stride = a.mbps;
-  k.part_o = (float*)(scratch + w.o); k.part_ml = (float*)(scratch + w.ml); k.seg = (int2*)(scratch + w.seg);
-  mla_timer_begin("attn", s);
-  if (w.NH == 16) launch_attn8<16>(codes, rope, k, s);
-  else launch_attn8<32>(codes, rope, k, s);
-  mla_timer_end("attn", s);
   MergeSrc& q = m->src[m->n_src++];
-  q.o = k.part_o; q.ml = k.part_ml; q.seg = k.seg; q.rows = w.NH;
-  q.group_units = k.units + k.n_ent;
+  if (pre) {
+    k.flat = 1; k.groups = 1; k.units = w.units_p;
+    k.n_ent = (int)cdiv(k.rows_total, 16);
+    k.len = a.prefix_len; k.table = a.prefix_table;
+    k.part_o = (float*)(scratch + w.o_p); k.part_ml = (float*)(scratch + w.ml_p); k.seg = (int2*)(scratch + w.seg_p);
+    q.flat = 1;
+  } else {
+    k.groups = w.groups; k.units = w.units; k.n_ent = a.n;
+    k.ctx = a.ctx; k.min_ctx = m->min_ctx; k.max_ctx = a.max_ctx;
+    k.table = a.table; k.table_stride = a.mbps;
+    k.part_o = (float*)(scratch + w.o); k.part_ml = (float*)(scratch + w.ml); k.seg = (int2*)(scratch + w.seg);
+    q.group_units = k.units + k.n_ent;
+  }
+  q.o = k.part_o; q.ml = k.part_ml; q.seg = k.seg; q.rows = 16;
+  mla_timer_begin(pre ? "attn_prefix" : "attn", s);
+  launch_attn8(codes, rope, k, s);
+  mla_timer_end(pre ? "attn_prefix" : "attn", s);
   return MLA_OK;
 }
 
-// One pass on the 16-bit cache's tensor-core kernels: the prefix on the
-// head-major one, whose 128 MMA rows take 128 query rows of any sequences; the
-// own rows as in mla_decode_attn.
-static int latent_pass16(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
-                         int* flag, cudaStream_t s) {
+template <bool FLAT, bool C8>
+static void launch_heads(const CUtensorMap& m0, const CUtensorMap& m1, const TcAttnArgs& k, cudaStream_t s) {
+  static std::atomic<bool> attr[64];
+  set_smem_once(attr, tc_attn_decode_kernel<FLAT, C8>, AttnSmemT<C8>::SIZE);
+  mla_timer_begin(FLAT ? "attn_prefix" : "attn", s);
+  launch_pdl(tc_attn_decode_kernel<FLAT, C8>, 2 * k.units, ATT_THREADS, AttnSmemT<C8>::SIZE, s, m0, m1, k);
+  mla_timer_end(FLAT ? "attn_prefix" : "attn", s);
+  mla_count_launch(1);
+}
+
+// A pass on the head-major kernel with packed partials: over the prefix, where its 128 MMA rows take
+// 128 query rows of any sequences, or (8-bit cache) over each sequence's own rows.
+static int pass_heads(const mla_handle* h, const LatentPlan& w, const LatentCall& a, bool pre, MergeArgs* m, char* scratch,
+                      int* flag, cudaStream_t s) {
   const mla_config& c = h->cfg;
   const int R = c.kv_lora_rank + c.qk_rope;
+  const long long blocks = a.n_blocks > 0 ? a.n_blocks : 1;
+  CUtensorMap mc, ml;
   int st;
-  if (a.prefix_len > 0) {
-    const long long rows = (long long)a.n_blocks * c.block_size;
-    CUtensorMap mc, ml;
-    if ((st = make_map2(&mc, a.cache, R, rows, R, 64)) != MLA_OK) return st;
-    if ((st = make_map_cache_groups(&ml, a.cache, R, rows, 4)) != MLA_OK) return st;
-    TcAttnArgs k{};
-    k.rows_total = (long long)a.n * c.n_heads;
-    k.n = (int)cdiv(k.rows_total, 128); k.H = 128;
-    k.bs = c.block_size; k.n_blocks = a.n_blocks; k.fixed_len = a.prefix_len;
-    k.block_table = a.prefix_table; k.q_abs = (const bf16*)a.q_abs; k.q_pe = (const bf16*)a.q_pe;
+  TcAttnArgs k{};
+  if (h->cache8) {
+    const Cache8 c8 = cache8_of(h);
+    if ((st = make_maps_cache8(&ml, &mc, a.cache, c8, blocks, 64)) != MLA_OK) return st;
+    k.c8 = (const uint8_t*)a.cache; k.c8_block = c8.block_bytes; k.c8_scales = c8.sc_off;
+  } else {
+    if ((st = make_map2(&mc, a.cache, R, blocks * c.block_size, R, 64)) != MLA_OK) return st;
+    if ((st = make_map_cache_groups(&ml, a.cache, R, blocks * c.block_size, 4)) != MLA_OK) return st;
     k.lat_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? 0 : c.qk_rope;
     k.rope_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? c.kv_lora_rank : 0;
-    k.scale_log2 = h->scale * 1.4426950408889634f;
-    k.part_o = (float*)(scratch + w.o_p); k.part_ml = (float*)(scratch + w.ml_p); k.seg = (int2*)(scratch + w.seg_p);
-    k.flag = flag;
-    k.units = w.units_p; k.min_per = 1;
-    k.ml_r = (long long)(k.units + k.n) * 128 * 2;
-    static std::atomic<bool> attr[64];
-    set_smem_once(attr, tc_attn_decode_kernel<true>, AttnSmem::SIZE);
-    mla_timer_begin("attn_prefix", s);
-    launch_pdl(tc_attn_decode_kernel<true>, 2 * k.units, ATT_THREADS, AttnSmem::SIZE, s, mc, ml, k);
-    mla_timer_end("attn_prefix", s);
-    mla_count_launch(1);
-    MergeSrc& q = m->src[m->n_src++];
-    q.o = k.part_o; q.ml = k.part_ml; q.ml_r = k.ml_r; q.half = 256; q.seg = k.seg; q.rows = 128; q.flat = 1;
   }
+  k.bs = c.block_size; k.n_blocks = a.n_blocks;
+  k.q_abs = (const bf16*)a.q_abs; k.q_pe = (const bf16*)a.q_pe;
+  k.scale_log2 = h->scale * 1.4426950408889634f;
+  k.flag = flag; k.min_per = 1;
+  MergeSrc& q = m->src[m->n_src++];
+  if (pre) {
+    k.rows_total = (long long)a.n * c.n_heads;
+    k.n = (int)cdiv(k.rows_total, 128); k.H = 128;
+    k.fixed_len = a.prefix_len; k.block_table = a.prefix_table;
+    k.units = w.units_p;
+    k.part_o = (float*)(scratch + w.o_p); k.part_ml = (float*)(scratch + w.ml_p); k.seg = (int2*)(scratch + w.seg_p);
+    q.flat = 1;
+  } else {
+    k.n = a.n; k.H = c.n_heads;
+    k.block_table = a.table; k.mbps = a.mbps; k.ctx = a.ctx; k.max_ctx = a.max_ctx;
+    k.allow_empty = m->min_ctx == 0;
+    k.units = w.units;
+    k.part_o = (float*)(scratch + w.o); k.part_ml = (float*)(scratch + w.ml); k.seg = (int2*)(scratch + w.seg);
+  }
+  k.ml_r = (long long)(k.units + k.n) * k.H * 2;
+  q.o = k.part_o; q.ml = k.part_ml; q.ml_r = k.ml_r; q.half = 256; q.seg = k.seg; q.rows = k.H;
+  if (!h->cache8) launch_heads<true, false>(mc, ml, k, s);
+  else if (pre) launch_heads<true, true>(mc, ml, k, s);
+  else launch_heads<false, true>(mc, ml, k, s);
+  return MLA_OK;
+}
+
+// The own rows of a 16-bit cache, as in mla_decode_attn.
+static int pass_own16(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
+                      int* flag, cudaStream_t s) {
   AttnParts P{};
   float* part_o = (float*)(scratch + w.o);
   float* part_ml = (float*)(scratch + w.ml);
-  st = tc_attention_launch(h, a.q_abs, a.q_pe, a.cache, a.n_blocks, a.table, a.mbps, a.ctx, a.max_ctx, a.n, part_o,
-                           part_ml, w.splits, flag, (int*)(scratch + w.seg), a.prefix_len > 0, &P, s);
+  const int st = tc_attention_launch(h, a.q_abs, a.q_pe, a.cache, a.n_blocks, a.table, a.mbps, a.ctx, a.max_ctx, a.n,
+                                     part_o, part_ml, w.splits, flag, (int*)(scratch + w.seg), a.prefix_len > 0, &P, s);
   if (st != MLA_OK) return st;
   MergeSrc& q = m->src[m->n_src++];
   q.o = part_o; q.ml = part_ml; q.ml_r = P.ml_r; q.half = P.half_cols; q.nseg = P.seg_counts; q.splits = P.splits;
-  q.rows = c.n_heads;
+  q.rows = h->cfg.n_heads;
   return MLA_OK;
 }
 
 // The same on CUDA cores (any shape, fp32 activations): the prefix rows simply
 // come first in every sequence's list of keys.
-static int latent_pass_simt(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch,
-                            int* flag, cudaStream_t s) {
+static int pass_simt(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch, int* flag,
+                     cudaStream_t s) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads, rkv = c.kv_lora_rank, dr = c.qk_rope, R = rkv + dr;
   AttnArgs p{};
@@ -429,17 +452,19 @@ static inline int latent_core(const mla_handle* h, const LatentCall& call, void*
     m.lse = lse ? lse + (size_t)t * H : nullptr;
     m.ctx = a.ctx; m.min_ctx = a.prefix_len > 0 ? 0 : 1; m.max_ctx = a.max_ctx;
     m.cap = (long long)a.mbps * c.block_size;
-    const int st = w.tc8    ? latent_pass8(h, w, a, &m, scratch, flag, s)
-                   : w.tc16 ? latent_pass16(h, w, a, &m, scratch, flag, s)
-                            : latent_pass_simt(h, w, a, &m, scratch, flag, s);
+    int st = MLA_OK;
+    if (w.pre == PRE_FEW8) st = pass_few8(h, w, a, true, &m, scratch, flag, s);
+    else if (w.pre != PRE_NONE) st = pass_heads(h, w, a, true, &m, scratch, flag, s);
     if (st != MLA_OK) return st;
-    int most = w.splits;   // split partials of one query row, about
-    if (w.tc16 && a.prefix_len > 0) most += (int)(cdiv(w.units_p, w.ents_p) + 1);
-    if (w.tc8) {
-      const long long own = cdiv(a.max_ctx, 128), pre = cdiv(a.prefix_len, 128);
-      most = (int)((own < cdiv(w.units, a.n) + 1 ? own : cdiv(w.units, a.n) + 1) +
-                   (pre < cdiv(w.units_p, w.ents_p ? w.ents_p : 1) + 1 ? pre : cdiv(w.units_p, w.ents_p ? w.ents_p : 1) + 1));
-    }
+    if (w.own == OWN_FEW8) st = pass_few8(h, w, a, false, &m, scratch, flag, s);
+    else if (w.own == OWN_HEADS8) st = pass_heads(h, w, a, false, &m, scratch, flag, s);
+    else if (w.own == OWN_TC16) st = pass_own16(h, w, a, &m, scratch, flag, s);
+    else st = pass_simt(h, w, a, &m, scratch, flag, s);
+    if (st != MLA_OK) return st;
+    // split partials of one query row, about
+    const long long own = w.splits ? w.splits : cdiv(w.units, a.n) + 1, pre = w.pre ? cdiv(w.units_p, w.ents_p) + 1 : 0;
+    const long long t_own = cdiv(a.max_ctx, 64), t_pre = cdiv(a.prefix_len, 64);
+    const int most = (int)((own < t_own ? own : t_own) + (pre < t_pre ? pre : t_pre));
     launch_merge(m, a.n, most, o_dt, s);
   }
   return MLA_OK;

@@ -35,8 +35,20 @@
 // issues TMA, warp 9 the score MMAs and warp 14 the P.V MMAs (one thread each,
 // so a P.V never waits behind the issue of a later S), and warps 10-13 send
 // each tile's partial scores to the peer as soon as S lands.
+//
+// FLAT: the entries of the schedule are not sequences but blocks of 128 query
+// rows of any sequences, all against one block table (a shared prefix).
+// C8: the cache is 8-bit (cache8.cuh). TMA brings the CTA's 256 codes of each
+// row (16 KB a tile, two raw buffers) and the row scales; the sender warps, idle
+// for most of a tile, turn them into the bf16 latent stage (scale * code is
+// exact there), two tiles ahead and after each tile's send, so that everything
+// behind the stage is the 16-bit kernel. The latent ring is three deep then, in
+// the same shared memory. (Feeding the codes to kind::f8f6f4 MMAs instead would
+// take as many MMAs, the query and the weights being split in two there, and
+// put their splitting into the softmax, which bounds this kernel.)
 #pragma once
 
+#include "cache8.cuh"
 #include "tc_common.cuh"
 
 namespace mla {
@@ -66,29 +78,38 @@ struct TcAttnArgs {
   int allow_empty;   // a context length of 0 is valid (the sequence has keys elsewhere)
   // FLAT: entry b is the 128 query rows 128 b .. of rows_total, all against the
   // same fixed_len rows of one block table; H is 128 and the partials are units
-  // c + b of [units + n] with seg[b] = {first cluster, clusters}
+  // c + b of [units + n] with seg[b] = {first cluster, clusters}. C8: the partials
+  // lie so too, with H rows per unit
   long long rows_total;
   int fixed_len;
   int2* seg;
+  // C8: the cache, its blocks' size and where their scales begin
+  const uint8_t* c8;
+  long long c8_block, c8_scales;
 };
 
-constexpr int ATT_NST = 4;                      // latent ring depth
 constexpr int ATT_NRP = 3;                      // rotary slots (the tiles of this CTA's parity)
 constexpr int ATT_THREADS = 480;                // 8 softmax, 1 TMA, 1 S-MMA, 4 sender, 1 P.V-MMA warps
 constexpr int ATT_MAX_SEQ = 256;                // sequences per call (the prefix table in shared memory)
-struct AttnSmem {
+template <bool C8>
+struct AttnSmemT {
+  static constexpr int NST = C8 ? 3 : 4;        // latent ring depth
   static constexpr int STAGE = 4 * 8192;        // the 4 latent k-blocks of [64 rows x 64 cols] bf16
   static constexpr int TILE_OFF = 0;
-  static constexpr int ROPE_OFF = ATT_NST * STAGE;          // ATT_NRP x [64 x 64] bf16 rotary blocks
+  static constexpr int RAW_OFF = NST * STAGE;   // C8: 2 x 64 rows x 256 codes, [octet][2 k-blocks][8 rows][128 B]
+  static constexpr int ROPE_OFF = 4 * STAGE;                // ATT_NRP x [64 x 64] bf16 rotary blocks
   static constexpr int QPE_OFF = ROPE_OFF + ATT_NRP * 8192;   // [128 x 64] bf16 q_pe (MMA operand layout)
   static constexpr int X_OFF = QPE_OFF + 16384;   // 2 x [128 x 64] f16 peer partial S, then P (bf16) over it
   static constexpr int STG_OFF = X_OFF + 32768;   // [128 x 64] f16, our partial on its way out
   static constexpr int RED_OFF = STG_OFF + 16384; // [2 tiles][2 halves][128] fp32 half-row maxima, then [128] l
   static constexpr int PREF_OFF = RED_OFF + 2 * 2 * 128 * 4 + 128 * 4;   // [ATT_MAX_SEQ + 1] tile prefix sums
-  static constexpr int BAR_OFF = PREF_OFF + (ATT_MAX_SEQ + 4) * 4;
+  static constexpr int SC_OFF = PREF_OFF + (ATT_MAX_SEQ + 4) * 4;        // C8: row scales [2][64]
+  static constexpr int BAR_OFF = SC_OFF + (C8 ? 512 : 0);
   static constexpr int SIZE = 1024 + BAR_OFF + 512;
   static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
+  static_assert(SC_OFF % 16 == 0, "bulk copies");
 };
+using AttnSmem = AttnSmemT<false>;
 // TMEM columns: Q latent [0,128) (bf16 pairs), S buffers [128,192) [192,256), O [256,512)
 constexpr uint32_t ATT_TM_Q = 0, ATT_TM_S = 128, ATT_TM_O = 256;
 
@@ -127,7 +148,7 @@ __device__ __forceinline__ int attn_seq_len(const TcAttnArgs& a, int b) {
 // flattened tile list that cluster c takes (slices of `per` tiles, at least
 // a.min_per). Block 0 of the grid writes each sequence's segment count to
 // a.nseg. Every thread of the CTA calls it; it ends with a __syncthreads.
-template <bool FLAT = false>
+template <bool FLAT = false, bool C8 = false>
 __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows, int* pref, int c, uint32_t r,
                                               int warp, int lane, int* per_out, int* g0_out, int* g1_out) {
   if (warp == 0) {
@@ -166,7 +187,7 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   if (blockIdx.x == 0) {   // segments of each sequence, for the merge
     for (int b = threadIdx.x; b < a.n; b += blockDim.x) {
       const int T = pref[b + 1] - pref[b];
-      if (FLAT) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
+      if (FLAT || C8) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
       else a.nseg[b] = T > 0 ? (pref[b] + T - 1) / per - pref[b] / per + 1 : 0;
     }
   }
@@ -175,11 +196,12 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   *g1_out = min(total, c * per + per);
 }
 
-template <bool FLAT>
+template <bool FLAT, bool C8 = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     tc_attn_decode_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_lat,
                           TcAttnArgs a) {
-  using SM = AttnSmem;
+  using SM = AttnSmemT<C8>;
+  constexpr int ATT_NST = SM::NST;
   griddep_wait();   // the inputs all come from the stream's earlier kernels
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -205,6 +227,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
   const uint32_t xch_b = fin + 8;                     // [4 quarters][2] the two halves' maxima posted
   const uint32_t l_done = xch_b + 64;                 // [4] the second half's row sums posted
   const uint32_t rope_empty = l_done + 32;            // [ATT_NRP] rotary block consumed by S
+  const uint32_t rope_full = rope_empty + 8 * ATT_NRP;   // C8: [ATT_NRP] rotary block landed
+  const uint32_t raw_full = rope_full + 8 * ATT_NRP;     // C8: [2] codes and scales landed
+  const uint32_t raw_empty = raw_full + 16;              // C8: [2] codes converted
+  volatile int* raw_rows = (volatile int*)(smem + SM::BAR_OFF + 456);   // C8: [2] rows that count
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 448);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 452);
 
@@ -214,13 +240,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
 
   // ---- the schedule: tile prefix over the batch, then this cluster's slice ----
   int per, g0, g1;
-  attn_schedule<FLAT>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
+  attn_schedule<FLAT, C8>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
   if (g0 >= g1) return;   // both CTAs of the cluster take this branch together
   const int N = g1 - g0;
   const long long tab = FLAT ? 0 : a.mbps;   // block-table row of sequence b: b * tab
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ATT_NST; ++i) { mbar_init(full_b + 8 * i, 1); mbar_init(empty_b + 8 * i, 1); }
+    for (int i = 0; i < ATT_NST; ++i) { mbar_init(full_b + 8 * i, C8 ? 4 : 1); mbar_init(empty_b + 8 * i, 1); }
+    if (C8) {
+      for (int i = 0; i < ATT_NRP; ++i) mbar_init(rope_full + 8 * i, 1);
+      for (int i = 0; i < 2; ++i) { mbar_init(raw_full + 8 * i, 1); mbar_init(raw_empty + 8 * i, 4); }
+    }
     for (int i = 0; i < 2; ++i) { mbar_init(s_full + 8 * i, 1); mbar_init(s_free + 8 * i, 12); }
     for (int i = 0; i < ATT_NRP; ++i) mbar_init(rope_empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
@@ -265,8 +295,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       const int st = i % ATT_NST;
       const bool rope = (i & 1) == (int)r;
       const int ri = (i >> 1) % ATT_NRP;
-      if (!mbar_wait_warp(empty_b + 8 * st, ((i / ATT_NST) & 1) ^ 1, abort_word, a.flag)) break;
+      if (C8 ? !mbar_wait_warp(raw_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)
+             : !mbar_wait_warp(empty_b + 8 * st, ((i / ATT_NST) & 1) ^ 1, abort_word, a.flag))
+        break;
       if (rope && !mbar_wait_warp(rope_empty + 8 * ri, (((i >> 1) / ATT_NRP) & 1) ^ 1, abort_word, a.flag)) break;
+      if (C8) {
+        if (lane == 0) {
+          const int j0 = 64 * w.lt, off = j0 % a.bs, rb = i & 1;
+          const bool good = blk >= 0 && blk < a.n_blocks;
+          if (!good && r == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
+          const int cur = good ? blk : max(a.n_blocks, 1);   // a block beyond the map: the load fills zeros
+          raw_rows[rb] = good ? min(64, attn_seq_len<FLAT>(a, w.b) - j0) : 0;
+          mbar_arrive_expect_tx(raw_full + 8 * rb, 16384 + (good ? 256 : 0));
+          tma_load_5d(sbase + SM::RAW_OFF + rb * 16384, &tm_lat, raw_full + 8 * rb, 0, 0, 2 * (int)r, good ? off / 8 : 0, cur);
+          if (good) bulk_load(sbase + SM::SC_OFF + rb * 256, a.c8 + cur * a.c8_block + a.c8_scales + off * 4, 256, raw_full + 8 * rb);
+          if (rope) {
+            mbar_arrive_expect_tx(rope_full + 8 * ri, 8192);
+            tma_load_3d(sbase + SM::ROPE_OFF + ri * 8192, &tm_cache, rope_full + 8 * ri, 0, good ? off : 0, cur);
+          }
+        }
+        continue;
+      }
       if (lane == 0) {
         const int j0 = 64 * w.lt;
         long long row = -64;
@@ -280,7 +329,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       }
     }
     // drain the loads still in flight
-    if (lane == 0) {
+    if (C8 && lane == 0) {
+      for (int u = (i > 2 ? i - 2 : 0); u < i; ++u) {
+        const uint64_t t1 = global_timer_ns();
+        while (!mbar_try_wait(raw_full + 8 * (u & 1), (u >> 1) & 1))
+          if (global_timer_ns() - t1 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+      }
+      const int nr = (i + 1 - (int)r) >> 1;   // rotary blocks loaded
+      for (int u = (nr > ATT_NRP ? nr - ATT_NRP : 0); u < nr; ++u) {
+        const uint64_t t1 = global_timer_ns();
+        while (!mbar_try_wait(rope_full + 8 * (u % ATT_NRP), (u / ATT_NRP) & 1))
+          if (global_timer_ns() - t1 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+      }
+    }
+    if (!C8 && lane == 0) {
       for (int u = (i > ATT_NST ? i - ATT_NST : 0); u < i; ++u) {
         const uint64_t t1 = global_timer_ns();
         while (!mbar_try_wait(full_b + 8 * (u % ATT_NST), (u / ATT_NST) & 1))
@@ -315,6 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
                         (j > 0 || k > 0) ? 1u : 0u);
         if ((t & 1) == (int)r) {
           const int ri = (t >> 1) % ATT_NRP;
+          if (C8 && !mbar_wait(rope_full + 8 * ri, ((t >> 1) / ATT_NRP) & 1, abort_word, a.flag)) break;
+          if (C8) tc_fence_after();
           const uint64_t dr = d_rope + (uint64_t)(ri * (8192 / 16));
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_bf16(d, d_qpe + 2 * k, dr + 2 * k, idesc_s, 1u);
@@ -367,7 +431,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     const uint32_t peer_x = mapa_shared(x_s, peer), peer_x_full = mapa_shared(x_full_b, peer);
     const uint32_t stg_s = sbase + SM::STG_OFF + 4096 * qs;   // this warp's rows, 4 KB
     uint4* stg_row = (uint4*)(smem + SM::STG_OFF + h * 128);
-    for (int i = 0; i < N; ++i) {
+    // C8: tile t's codes -> its bf16 stage. This warp takes chunks [4 (cw & 1), +4) of 16 codes of k-block
+    // cw >> 1 of every row: lane = row of an octet + 8 x chunk, so that the 128-byte swizzle spreads loads
+    // and stores over all banks. Rows that do not count become zeros.
+    auto convert = [&](int t) -> bool {
+      const int rb = t & 1, st = t % ATT_NST, cw = warp - 10;
+      if (!mbar_wait_warp(raw_full + 8 * rb, (t >> 1) & 1, abort_word, a.flag) ||
+          !mbar_wait_warp(empty_b + 8 * st, ((t / ATT_NST) & 1) ^ 1, abort_word, a.flag))
+        return false;
+      const int rows = raw_rows[rb], ro = lane & 7, cc = 4 * (cw & 1) + (lane >> 3);
+      const uint8_t* src = smem + SM::RAW_OFF + rb * 16384 + (cw >> 1) * 1024 + ro * 128 + ((cc ^ ro) << 4);
+      uint8_t* dst = smem + SM::TILE_OFF + st * SM::STAGE + (2 * (cw >> 1) + (cc >> 2)) * 1024 + ro * 128;
+      const int o0 = ((2 * (cc & 3)) ^ ro) << 4, o1 = ((2 * (cc & 3) + 1) ^ ro) << 4;
+      const float* sc = reinterpret_cast<const float*>(smem + SM::SC_OFF + rb * 256);
+#pragma unroll 4
+      for (int oct = 0; oct < 8; ++oct) {
+        const uint4 cv = *reinterpret_cast<const uint4*>(src + oct * 2048);
+        const bool live = 8 * oct + ro < rows;
+        const float s = sc[8 * oct + ro];
+        const uint32_t w[4] = {cv.x, cv.y, cv.z, cv.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = e4m3x2_f32((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+          o[k] = live ? pack_bf16x2(f.x * s, f.y * s) : 0u;
+        }
+        *reinterpret_cast<uint4*>(dst + oct * 4096 + o0) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + oct * 4096 + o1) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(full_b + 8 * st); mbar_arrive(raw_empty + 8 * rb); }
+      return true;
+    };
+    bool live_s = true;
+    if (C8) live_s = convert(0) && (N < 2 || convert(1));
+    for (int i = 0; i < N && live_s; ++i) {
       if (!mbar_wait_warp(s_full + 8 * (i & 1), (i >> 1) & 1, abort_word, a.flag)) break;
       tc_fence_after();
       float v[64];
@@ -402,6 +501,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           bulk_copy_to_peer(peer_x + xb * 16384 + 4096 * qs, stg_s, 4096, peer_x_full + 8 * (4 * xb + qs));
           bulk_commit_group();
         }
+      }
+      if (C8 && i + 2 < N) {
+        __syncwarp();
+        live_s = convert(i + 2);
       }
     }
     if (lane == 0) bulk_wait_read_all();
@@ -534,7 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
         tc_fence_before();
       }
       l = l * alpha + psum;
-      if (valid < 64) {
+      if (!C8 && valid < 64) {
         // rows past the context may hold anything (even NaN); P is 0 there, but
         // 0 * NaN is not, so clear them in the four latent slots before P.V
         // (latent rows are laid out [8 row octets][4 k-blocks][8 rows][128 B])
@@ -562,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           seq_len = attn_seq_len<FLAT>(a, wn.b);
         }
         const int j = c - pref[b] / per;               // this segment's split slot in sequence b
-        const long long unit = FLAT ? (long long)c + b : (long long)b * a.splits + j;
+        const long long unit = FLAT || C8 ? (long long)c + b : (long long)b * a.splits + j;
         const bool store = FLAT ? b * 128LL + h < a.rows_total : h < a.H;
         float* const ml = a.part_ml + r * a.ml_r;      // this CTA's (m, l) copy
         if (!mbar_wait_warp(o_seg, kseg & 1, abort_word, a.flag)) { ok = false; break; }

@@ -1,19 +1,20 @@
-// Latent attention over the 8-bit cache on tcgen05, for the DeepSeek latent
-// (kv_lora_rank 512, qk_rope 64) and blocks of a multiple of 16 rows. The E4M3
-// codes go to the tensor cores as they are (kind::f8f6f4); no value is ever
-// widened in shared memory.
+// Latent attention over the 8-bit cache on tcgen05 for up to 64 heads, with the
+// DeepSeek latent (kv_lora_rank 512, qk_rope 64) and blocks of a multiple of 16
+// rows. The E4M3 codes go to the tensor cores as they are (kind::f8f6f4); no
+// value is ever widened in shared memory.
 //
 // The other operand of each product would lose accuracy in E4M3, so it is split
 // in two E4M3 parts, x = hi + lo with hi = e4m3(x) and lo = e4m3(x - hi): two 4-bit
 // significands carry the 8 bits of a bf16 value, and both parts ride in one MMA
-// as extra columns (N = 2 NH). A small-N MMA costs its issue whatever N is, so
+// as extra columns (N = 32 for 16 heads). An MMA of M 128 costs 49 cycles for any
+// N up to 64 (62 for 128, 121 for 256; K- or MN-major and 8- or 16-bit alike), so
 // the second part is free.
 //   q_abs_h = 2^k_h (hi + lo): k_h brings the row's largest to at most 448; columns
 //     within 2^-10 of it are exact, smaller ones off by at most 2^-18 of it
 //   p: relative to a per-head reference R that follows the tiles' maxima both up
-//     and down (within 2^9 of the largest of each 128 keys), so that thousands of
-//     light keys behind a heavy one keep their weight: a weight is off by 2^-8 of
-//     itself or 2^-9 of its tile's largest
+//     and down, so that thousands of light keys behind a heavy one keep their
+//     weight: a weight is off by 2^-8 of itself or 2^-12 of the largest of the
+//     last few tiles
 //
 // The row scale s_j = 2^k_j folds into both products: with u_hj = q_h . code_j,
 //   y_hj = scale log2(e) (s_j u_hj + q_pe_h . k_pe_j) + k_j
@@ -24,29 +25,25 @@
 // Transposed tiles as in the 16-bit few-head kernel: 128 cache rows fill the
 // MMA's M. One CTA takes whole rows (an 8-bit tile is 64 KB of codes and 16 KB
 // of rotary keys, so nothing has to be exchanged between CTAs):
-//   U^T [128 keys x (hi | lo)] = codes . Q^T          16 MMAs, M 128 x N 2 NH x K 32
-//   R^T [128 keys x NH]        = k_pe . q_pe^T (bf16)  4 MMAs, M 128 x N NH x K 16
+//   U^T [128 keys x (hi | lo)] = codes . Q^T          16 MMAs, M 128 x N 32 x K 32
+//   R^T [128 keys x 16]        = k_pe . q_pe^T (bf16)  4 MMAs, M 128 x N 16 x K 16
 //   O^T [128 latent x (hi | lo)] x 4 = codes^T . W^T  16 MMAs; codes^T is the same
 //                                                     shared-memory tile read MN-major
-// O^T stays in TMEM; it is rescaled there only when some head's reference moves.
-// A reference is set four to five octaves above the tile's largest and kept
-// while the tiles' largest stay within [R - 9, R]; set closer, one head or
-// another moved its reference on most tiles.
 //
-// Roles: warpgroup g of NH / 8 runs the softmax of heads [8 g, 8 g + 8) (thread
-// <-> key; for a rescale and at the end thread <-> latent column); then one warp
-// each for TMA, the score MMAs and the value MMAs. S and W alternate between two
-// buffers, so the scores of tile i + 1 run during the softmax of tile i and its
-// value MMAs during the softmax of tile i + 1. The softmax is a chain of short
-// dependent steps, so few heads per warp and many warps hide it best.
-// The TMA warp also brings the tile's row scales (a bulk copy per box) and
-// writes what the softmax has to know of the tile, so that the softmax warps
-// touch no table.
+// Two sets of four softmax warps (thread <-> key; for a rescale and at the end
+// thread <-> latent column) take the tiles of either parity, each with S, W and
+// rotary buffers, an O^T in TMEM, references and row sums of its own. A tile's
+// softmax is a chain of short dependent steps, about as long as HBM takes for
+// the tile, so two chains run at a time; and as the sets share nothing until an
+// entry ends, a set's O^T is at rest when its next tile moves a reference. One
+// warp each issues TMA, the score MMAs and the value MMAs. The TMA warp also
+// brings the tile's row scales (a bulk copy per box) and writes what the softmax
+// has to know of the tile, so that the softmax warps touch no table.
 //
-// Schedule: the tiles of all entries (sequences; or blocks of NH query rows
-// against one shared prefix) form one list, and each CTA takes an equal
-// slice. More than 32 heads: `groups` CTAs, each with 32 heads, walk the same
-// slice at the same time, so the rows come from HBM once and from L2 after.
+// Schedule: the tiles of all entries (sequences; or blocks of 16 query rows
+// against one shared prefix) form one list, and each CTA takes an equal slice.
+// More than 16 heads: `groups` CTAs, each with 16 heads, walk the same slice at
+// the same time, so the rows come from HBM once and from L2 after.
 #pragma once
 
 #include "cache8.cuh"
@@ -55,14 +52,6 @@
 namespace mla {
 namespace tc {
 
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                            int c3, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
-      "[%2];" ::"r"(dst),
-      "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-      : "memory");
-}
 // D(tmem) (+)= A * B^T, E4M3 in, fp32 accumulation, K 32.
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -77,22 +66,29 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major =
   return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 32 lanes x 32 bit, 8 consecutive columns.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
+// mbar_wait without a look at the clock before the first polls fail: the softmax warps wait often
+// and briefly.
+__device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity, volatile int* abort_word, int* flag) {
+  bool ok = true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63) == 0) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (*abort_word || t - t0 > WAIT_LIMIT_NS) {
+        if (!*abort_word) set_flag(flag, MLA_FLAG_WAIT_TIMEOUT);
+        *abort_word = 1;
+        ok = false;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
-// Global to shared memory, 16-byte aligned, a multiple of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
+
 struct TcAttn8Args {
   int n_ent, groups, units;   // entries; head groups; slices (grid = units x groups)
-  int flat;                   // 0: entry e is sequence e, its rows e H + NH group ..; 1: query rows e NH .. against one table
+  int flat;                   // 0: entry e is sequence e, its rows e H + 16 group ..; 1: query rows 16 e .. against one table
   int H;                      // query rows per sequence (flat = 0)
   long long rows_total;       // query rows in all
   const int* ctx;             // lengths (flat = 0)
@@ -105,42 +101,37 @@ struct TcAttn8Args {
   const bf16* q_abs;          // [rows_total, 512]
   const bf16* q_pe;           // [rows_total, 64]
   float scale_log2;
-  float* part_o;              // [groups][units + n_ent][NH][512]: unit c + e of group g
-  float* part_ml;             // the same [..][NH][2]
+  float* part_o;              // [groups][units + n_ent][16][512]: unit c + e of group g
+  float* part_ml;             // the same [..][16][2]
   int2* seg;                  // [n_ent]: {first slice, slices} of each entry
   int* flag;
 };
 
-constexpr int A8_MAX_ENT = 1024;   // sequences per launch (their tile prefix in shared memory)
+constexpr int A8_MAX_ENT = 768;   // sequences per launch (their tile prefix in shared memory)
 
-template <int NH>
+constexpr int A8_THREADS = 8 * 32 + 96;   // two sets of four softmax warps; TMA, score and value MMA warps
 struct Attn8Smem {
-  static constexpr int NWG = NH / 8;
-  static constexpr int NPR = NH == 16 ? 5 : 4;   // ring entries of 32 KB: two per tile
-  static constexpr int QB = 2 * NH * 128;         // one k-block [2 NH x 128 B] of Q
-  static constexpr int PB = 2 * NH * 128;         // one buffer of W^T [2 NH x 128 keys]
+  static constexpr int NPR = 5;                   // ring entries of 32 KB: two per tile
+  static constexpr int QB = 32 * 128;             // one k-block [32 x 128 B] of Q
+  static constexpr int PB = 32 * 128;             // one buffer of W^T [32 x 128 keys]
   static constexpr int RING_OFF = 0;              // entry: [16 row octets][2 k-blocks][8 rows][128 B]
   static constexpr int ROPE_OFF = NPR * 32768;    // 2 x [128 x 64] bf16
   static constexpr int Q_OFF = ROPE_OFF + 2 * 16384;
   static constexpr int QPE_OFF = Q_OFF + 4 * QB;
-  static constexpr int P_OFF = QPE_OFF + NH * 128;
-  // row scales [2][128]; maxima [2][4 warps][NH]; per warpgroup row sums [4][8] and query scales [8];
-  // per warp 8 - R [8] and the factors of a rescale [8]
-  static constexpr int SC_OFF = P_OFF + 2 * PB;
+  static constexpr int P_OFF = QPE_OFF + 16 * 128;
+  static constexpr int SC_OFF = P_OFF + 2 * PB;   // row scales [2][128]
   static constexpr int RED_OFF = SC_OFF + 2 * 128 * 4;
-  static constexpr int RED_MAX = 8 * NH, RED_WG = 32 + 8, RED_WARP = 16;
-  static constexpr int RED_FLOATS = RED_MAX + NWG * RED_WG + 4 * NWG * RED_WARP;
+  // floats: maxima [2 sets][2][4 warps][16]; query scales [2 entries][16]; posted row sums [4 tiles][4 warps][16]
+  // and references [4][16]; per warp 8 - R and the factors of a rescale [2][16]
+  static constexpr int RED_SLQ = 256, RED_RL = RED_SLQ + 32, RED_RP = RED_RL + 256, RED_WARP = RED_RP + 64;
+  static constexpr int RED_FLOATS = RED_WARP + 8 * 32;
   static constexpr int PREF_OFF = RED_OFF + RED_FLOATS * 4;
   static constexpr int BAR_OFF = PREF_OFF + (A8_MAX_ENT + 4) * 4;
   static constexpr int SIZE = 1024 + BAR_OFF + 512;
-  static constexpr int THREADS = NWG * 128 + 96;
-  // TMEM: two S buffers [(hi 8 | lo 8) per warpgroup | rotary NH], then O^T of the four latent
-  // groups [(hi 8 | lo 8) per warpgroup]
-  static constexpr int SB = NH == 16 ? 64 : 128;
-  static constexpr int TM_O = 2 * SB;
+  // TMEM: per set S [(hi 8 | lo 8) x 2 | rotary 16], then per set O^T of the four latent groups [(hi 8 | lo 8) x 2]
+  static constexpr int TM_S = 0, TM_O = 128;
   static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
-  static_assert(TM_O + 8 * NH <= 512, "tensor memory");
-  static_assert(BAR_OFF % 8 == 0 && P_OFF % 1024 == 0, "alignment");
+  static_assert(BAR_OFF % 16 == 0 && P_OFF % 1024 == 0, "alignment");
 };
 
 __device__ __forceinline__ int a8_len(const TcAttn8Args& a, int e) {
@@ -184,13 +175,16 @@ struct Walk8 {
   }
 };
 
-template <int NH>
-__global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
+// What the TMA warp says of a tile: how many tiles of its entry follow in this slice (2: two or
+// more), whether it or the tile before it is its entry's first here, and the parity of the entry.
+constexpr int TILE_LEFT = 3, TILE_FIRST = 4, TILE_PREV_FIRST = 8, TILE_ODD = 16;
+
+__global__ void __launch_bounds__(A8_THREADS, 1)
     tc_attn8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
                     TcAttn8Args a) {
-  using SM = Attn8Smem<NH>;
+  using SM = Attn8Smem;
   griddep_wait();   // the inputs all come from the stream's earlier kernels
-  constexpr int NPR = SM::NPR, NWG = SM::NWG;
+  constexpr int NPR = SM::NPR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -202,17 +196,38 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
   const uint32_t rfull = empty_b + 8 * NPR, rempty = rfull + 16;  // [2] rotary block landed / consumed
   const uint32_t s_full = rempty + 16, s_free = s_full + 16;      // [2] scores complete / read
   const uint32_t p_full = s_free + 16, p_free = p_full + 16;      // [2] weights written / consumed (O^T holds the tile)
-  const uint32_t q_ready = p_free + 16;                           // the next entry's query is in shared memory
-  const uint32_t o_free = q_ready + 8;                            // O^T of an entry read out
-  const uint32_t fin_s = o_free + 8, fin_o = fin_s + 8;
-  const uint32_t red_b = fin_o + 8;                               // [2] the warps' maxima posted
-  const uint32_t wg_b = red_b + 16;                               // per warpgroup: query scales, row sums
-  int4* tile_s = (int4*)(smem + SM::BAR_OFF + 384);                // [2]: {keys in the tile, boxes loaded, last of its entry here, entry}
+  const uint32_t o_free = p_free + 16;                            // [2] a set's O^T of an entry read out
+  const uint32_t q_ready = o_free + 16;                           // the next entry's query is in shared memory
+  const uint32_t fin_s = q_ready + 8, fin_o = fin_s + 8;
+  const uint32_t red_b = fin_o + 8;                               // [2 sets][2] a tile's maxima posted
+  const uint32_t post_b = red_b + 32;                             // [4 tiles] a tile's warps are done
+  int4* tile_s = (int4*)(smem + SM::BAR_OFF + 384);   // [2]: {keys in the tile, boxes loaded, TILE_ bits, entry}
+  volatile int* pv_fresh = (volatile int*)(smem + SM::BAR_OFF + 416);   // [2]: the set's first tile of an entry
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 480);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 484);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x / a.groups, hg = blockIdx.x % a.groups;
 
+  // ---- barriers (thread 64) and tensor memory (warp 1), beside the schedule (warp 0) ----
+  if (threadIdx.x == 64) {
+    for (int i = 0; i < NPR; ++i) { mbar_init(full_b + 8 * i, 1); mbar_init(empty_b + 8 * i, 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(rfull + 8 * i, 1);
+      mbar_init(rempty + 8 * i, 5);   // read by the MMAs, and the scales by the set's warps
+      mbar_init(s_full + 8 * i, 2);   // the MMAs, and the issuing thread (it has seen the query's scales)
+      mbar_init(s_free + 8 * i, 4);
+      mbar_init(p_full + 8 * i, 4);
+      mbar_init(p_free + 8 * i, 1);
+      mbar_init(o_free + 8 * i, 4);
+    }
+    for (int i = 0; i < 4; ++i) { mbar_init(red_b + 8 * i, 4); mbar_init(post_b + 8 * i, 4); }
+    mbar_init(q_ready, 4);
+    mbar_init(fin_s, 1);
+    mbar_init(fin_o, 1);
+    *abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), 512); tmem_relinquish(); }
   // ---- the schedule ----
   const int T_flat = a.flat ? (a.len + 127) / 128 : 0;
   if (!a.flat && warp == 0) {
@@ -236,7 +251,11 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       if (each * lane + k < a.n_ent) pref[each * lane + k] += incl - sum;
     if (lane == 31) pref[a.n_ent] = incl;
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) griddep_launch_dependents();
   const Walk8 w0{a.flat ? nullptr : pref, T_flat, a.n_ent, 0, 0, 0, 0};
   const int total = w0.at(a.n_ent);
   const int per = max(1, (total + a.units - 1) / a.units);
@@ -246,36 +265,13 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       a.seg[e] = b1 > b0 ? make_int2(b0 / per, (b1 - 1) / per - b0 / per + 1) : make_int2(0, 0);
     }
   const long long g0l = (long long)c * per;
-  if (g0l >= total) return;
+  if (g0l >= total) {
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
   const int g0 = (int)g0l, N = min(total - g0, per);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NPR; ++i) { mbar_init(full_b + 8 * i, 1); mbar_init(empty_b + 8 * i, 1); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(rfull + 8 * i, 1);
-      mbar_init(rempty + 8 * i, 1 + 4 * NWG);   // read by the MMAs, and the scales by the softmax warps
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(s_free + 8 * i, 4 * NWG);
-      mbar_init(p_full + 8 * i, 4 * NWG);
-      mbar_init(p_free + 8 * i, 1);
-      mbar_init(red_b + 8 * i, 4 * NWG);
-    }
-    mbar_init(o_free, 4 * NWG);
-    mbar_init(q_ready, 4 * NWG);
-    mbar_init(fin_s, 1);
-    mbar_init(fin_o, 1);
-    for (int i = 0; i < 2 * NWG; ++i) mbar_init(wg_b + 8 * i, 4);
-    *abort_word = 0;
-    fence_mbar_init();
-  }
-  if (warp == 0) { tmem_alloc(smem_u32(tmem_slot), 512); tmem_relinquish(); }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  if (threadIdx.x == 0) griddep_launch_dependents();
-
-  if (warp == 4 * NWG) {
+  if (warp == 8) {
     // ---------------- TMA: lane k < 128 / box brings rows [box k, box k + box) of each tile ----------------
     if (lane == 0) {
       prefetch_tmap(&tm_codes);
@@ -298,14 +294,20 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       }
     };
     fetch_box(w);
-    int i = 0;
-    bool ok = true;
+    int i = 0, odd = 0;
+    bool ok = true, prev_first = false;
     for (; i < N; ++i) {
       const bool good = has && raw >= 0 && raw < a.n_blocks;
       if (has && !good && hg == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
       const int cur = good ? raw : none, row0 = good ? off : 0;   // a block beyond the map: the load fills zeros
       const uint32_t boxes = __ballot_sync(0xffffffffu, good);
-      const int4 tile = make_int4(min(128, w.len - 128 * w.lt), (int)boxes, i == N - 1 || w.seg_last(), w.e);
+      const bool first = i == 0 || w.lt == 0;
+      if (first && i > 0) odd ^= TILE_ODD;
+      const int4 tile = make_int4(min(128, w.len - 128 * w.lt), (int)boxes,
+                                  min(2, min(w.tiles - 1 - w.lt, N - 1 - i)) | (first ? TILE_FIRST : 0) |
+                                      (prev_first ? TILE_PREV_FIRST : 0) | odd,
+                                  w.e);
+      prev_first = first;
       if (i + 1 < N) {
         w.next(a);
         fetch_box(w);
@@ -351,27 +353,27 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 1000000ull) {}
     }
-  } else if (warp == 4 * NWG + 1) {
+  } else if (warp == 8 + 1) {
     // ---------------- score MMAs ----------------
     if (lane == 0) {
-      constexpr uint32_t id_u = idesc_e4m3(128, 2 * NH), id_r = idesc_bf16(128, NH);
+      constexpr uint32_t id_u = idesc_e4m3(128, 32), id_r = idesc_bf16(128, 16);
       const uint64_t d_ring = sdesc_sw128_sbo(ring_s, 2048), d_rope = sdesc_sw128(rope_s);
       const uint64_t d_q = sdesc_sw128(q_s), d_qpe = sdesc_sw128(qpe_s);
       int ks = 0;
-      bool first = true;
       for (int i = 0; i < N; ++i) {
         const int b = i & 1;
-        if ((first && !mbar_wait(q_ready, ks & 1, abort_word, a.flag)) ||
-            !mbar_wait(s_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag) ||
-            !mbar_wait(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag))
+        if (!mbar_wait(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag) ||
+            !mbar_wait(s_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag))
           break;
-        if (first) ++ks;
-        first = tile_s[b].z != 0;   // the next tile begins another entry
+        if (tile_s[b].z & TILE_FIRST) {
+          if (!mbar_wait(q_ready, ks & 1, abort_word, a.flag)) break;
+          ++ks;
+        }
         tc_fence_after();
-        const uint32_t d = tmem + SM::SB * b;
+        const uint32_t d = tmem + SM::TM_S + 64 * b;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_bf16(d + 2 * NH, d_rope + (b * 16384 + 32 * k) / 16, d_qpe + 2 * k, id_r, k > 0 ? 1u : 0u);
+          mma_bf16(d + 32, d_rope + (b * 16384 + 32 * k) / 16, d_qpe + 2 * k, id_r, k > 0 ? 1u : 0u);
         mma_commit(rempty + 8 * b);
         bool ok = true;
 #pragma unroll
@@ -389,28 +391,28 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         }
         if (!ok) break;
         mma_commit(s_full + 8 * b);
+        mbar_arrive(s_full + 8 * b);
       }
       mma_commit(fin_s);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(fin_s, 0))
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
     }
-  } else if (warp == 4 * NWG + 2) {
+  } else if (warp == 8 + 2) {
     // ---------------- value MMAs ----------------
     if (lane == 0) {
-      constexpr uint32_t id_o = idesc_e4m3(128, 2 * NH, 1);
+      constexpr uint32_t id_o = idesc_e4m3(128, 32, 1);
       // codes^T: one 128-column group along M, 8-key octets 2048 B apart along K
       const uint64_t d_v = sdesc_sw128_mn_sbo(ring_s, 1024, 2048), d_p = sdesc_sw128(p_s);
-      Walk8 w = w0;
-      w.start(a, g0);
-      int ks = 0;
+      int ko[2] = {0, 0};   // entries whose O^T the set has begun
       for (int i = 0; i < N; ++i) {
         const int b = i & 1;
-        const bool first = i == 0 || w.lt == 0;
-        if (!mbar_wait(p_full + 8 * b, (i >> 1) & 1, abort_word, a.flag) ||
-            (first && ks > 0 && !mbar_wait(o_free, (ks - 1) & 1, abort_word, a.flag)))
-          break;
-        if (first) ++ks;
+        if (!mbar_wait(p_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) break;
+        const bool fresh = pv_fresh[b] != 0;
+        if (fresh) {
+          const int k = b ? ko[1]++ : ko[0]++;
+          if (k > 0 && !mbar_wait(o_free + 8 * b, (k - 1) & 1, abort_word, a.flag)) break;
+        }
         tc_fence_after();
         const uint64_t dp = d_p + (uint64_t)(b * (SM::PB / 16));
 #pragma unroll
@@ -421,12 +423,11 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8(tmem + SM::TM_O + (2 * g + kk) * 2 * NH, dv + (kk * 1024 + 8192 * k) / 16, dp + 2 * k, id_o,
-                     (!first || k > 0) ? 1u : 0u);
+              mma_f8(tmem + SM::TM_O + 128 * b + (2 * g + kk) * 32, dv + (kk * 1024 + 8192 * k) / 16, dp + 2 * k, id_o,
+                     (!fresh || k > 0) ? 1u : 0u);
           mma_commit(empty_b + 8 * slot);
         }
         mma_commit(p_free + 8 * b);
-        if (i + 1 < N) w.next(a);
       }
       mma_commit(fin_o);
       const uint64_t t0 = global_timer_ns();
@@ -434,39 +435,41 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
     }
   } else {
-    // ---------------- softmax: thread <-> key of the tile ----------------
-    const int wg = warp >> 2, q = warp & 3;
+    // ---------------- softmax: set b takes the tiles of parity b; thread <-> key of the tile ----------------
+    const int set = warp >> 2, q = warp & 3;
     const int row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-    float* red = (float*)(smem + SM::RED_OFF);                       // [2][4][NH]
-    float* rl = red + SM::RED_MAX + wg * SM::RED_WG;                 // [4][8]
-    float* slq = rl + 32;                                            // [8] scale log2(e) 2^k_h
-    float* ref_w = red + SM::RED_MAX + NWG * SM::RED_WG + warp * SM::RED_WARP;   // [8] 8 - R, this warp's copy
-    float* al_w = ref_w + 8;                                         // [8] factors of the last rescale
-    const uint32_t qs_b = wg_b + 16 * wg, l_b = qs_b + 8;
-    int kq = 0, kl = 0;   // phases of qs_b and l_b
+    float* red = (float*)(smem + SM::RED_OFF);                        // [2 sets][2][4][16]
+    float* slq = red + SM::RED_SLQ;                                   // [2][16]: scale log2(e) 2^k_h
+    float* rl = red + SM::RED_RL;                                     // [4][4][16]
+    float* rp_s = red + SM::RED_RP;                                   // [4][16]
+    float* ref_w = red + SM::RED_WARP + warp * 32;                    // [16] 8 - R, this warp's copy
+    float* al_w = ref_w + 16;                                         // [16] factors of a rescale
+    const uint32_t tm_o = tmem + SM::TM_O + lane_base;                // + 128 set + 32 group
+    uint8_t* const pb = smem + SM::P_OFF + set * SM::PB + (row & 15);
 
-    // The 8 heads' query rows of entry e in two E4M3 parts: 16 threads per head, 32 columns each.
-    auto load_q = [&](int e) -> bool {
-      const int hh = row >> 4, sub = row & 15, hd = 8 * wg + hh;
-      const long long r0 = a.flat ? (long long)e * NH : (long long)e * a.H + (long long)hg * NH;
-      const bool live = a.flat ? r0 + hd < a.rows_total : hg * NH + hd < a.H;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (live ? r0 + hd : 0) * 512 + 32 * sub);
-      uint4 v[4];
+    // The 16 heads' query rows of entry e in two E4M3 parts: eight threads per head, 64 columns each,
+    // in two halves.
+    auto load_q = [&](int e, int odd) {
+      const int hd = row >> 3, sub = row & 7;
+      const int r_hi = 16 * (hd >> 3) + (hd & 7);   // operand row of the first part; the second is 8 further on
+      const long long r0 = a.flat ? (long long)e * 16 : (long long)e * a.H + 16LL * hg;
+      const bool live = a.flat ? r0 + hd < a.rows_total : 16 * hg + hd < a.H;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q_abs + (live ? r0 + hd : 0) * 512 + 64 * sub);
+      uint4 v[8];
       float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
-      uint4 pe = make_uint4(0, 0, 0, 0);
-      if (live && sub < 8) pe = reinterpret_cast<const uint4*>(a.q_pe + (r0 + hd) * 64)[sub];
+      for (int k = 0; k < 8; ++k) v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
+      const uint4 pe = live ? reinterpret_cast<const uint4*>(a.q_pe + (r0 + hd) * 64)[sub] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           m = fmaxf(m, fmaxf(finite_abs(__uint_as_float(u[j] << 16)), finite_abs(__uint_as_float(u[j] & 0xFFFF0000u))));
       }
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       // as a cache row's exponent, over bf16's whole range
       int k = 0;
       if (m > 0.f) {
@@ -475,10 +478,10 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
         k = max(-110, min(119, k));
       }
       const float inv = exp2_int(-k);
-      if (sub == 0) slq[hh] = a.scale_log2 * exp2_int(k);
-      uint8_t* qb = smem + SM::Q_OFF + (sub >> 2) * SM::QB;   // columns [128 j, 128 j + 128) are k-block j
+      if (sub == 0) slq[(odd ? 16 : 0) + hd] = a.scale_log2 * exp2_int(k);
+      uint8_t* qb = smem + SM::Q_OFF + (sub >> 1) * SM::QB;   // columns [128 j, 128 j + 128) are k-block j
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
+      for (int ch = 0; ch < 4; ++ch) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -491,226 +494,250 @@ __global__ void __launch_bounds__(Attn8Smem<NH>::THREADS, 1)
           hi[j] = (uint32_t)a0 | ((uint32_t)a1 << 16);
           lo[j] = (uint32_t)e4m3x2_sat(f0 - g0v.x, f1 - g0v.y) | ((uint32_t)e4m3x2_sat(f2 - g1v.x, f3 - g1v.y) << 16);
         }
-        const int chunk = ((sub & 3) * 2 + ch) ^ hh;
-        *reinterpret_cast<uint4*>(qb + (16 * wg + hh) * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(qb + (16 * wg + 8 + hh) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int chunk = ((sub & 1) * 4 + ch) ^ (hd & 7);
+        *reinterpret_cast<uint4*>(qb + r_hi * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(qb + (r_hi + 8) * 128 + 16 * chunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
-      if (sub < 8) *reinterpret_cast<uint4*>(smem + SM::QPE_OFF + hd * 128 + 16 * (sub ^ hh)) = pe;
+      *reinterpret_cast<uint4*>(smem + SM::QPE_OFF + hd * 128 + 16 * (sub ^ (hd & 7))) = pe;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) { mbar_arrive(q_ready); mbar_arrive(qs_b); }
-      return mbar_wait_warp(qs_b, (kq++) & 1, abort_word, a.flag);   // the scales are there for every warp
+      if (lane == 0) mbar_arrive(q_ready);
     };
 
     const int box_log = 31 - __clz(a.box);
-    float l[8];
+    const uint32_t all_boxes = (1u << (128 / a.box)) - 1u;
+    // lane h < 16: head h's reference, the largest seen and the largest of late, over this set's tiles
+    float R = -INFINITY, top = -INFINITY, recent = -INFINITY;
+    float l[16];
 #pragma unroll
-    for (int h = 0; h < 8; ++h) l[h] = 0.f;
-    float R = -INFINITY, top = -INFINITY;   // lane h: head h's reference and the largest seen (h < NH)
-    if (lane < 8) ref_w[lane] = 8.f;
-    bool ok, first = true;
-    {
+    for (int h = 0; h < 16; ++h) l[h] = 0.f;
+    bool ok = true;
+    if (set == 0) {   // while the first tile is on its way
       Walk8 w = w0;
       w.start(a, g0);
-      ok = load_q(w.e);
+      load_q(w.e, 0);
     }
-    for (int i = 0; i < N && ok; ++i) {
-      const int b = i & 1;
-      if (!mbar_wait_warp(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
-      const int4 tile = tile_s[b];
-      const float sj = *reinterpret_cast<const float*>(smem + SM::SC_OFF + b * 512 + row * 4);
+    for (int i = set; i < N && ok; i += 2) {
+      if (!mbar_poll_warp(rfull + 8 * set, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      const int4 tile = tile_s[set];
+      const bool first = tile.z & TILE_FIRST, prev_first = tile.z & TILE_PREV_FIRST;
+      const int left = tile.z & TILE_LEFT;
+      if (first && i > 0) {
+        // the scores of the entry before are complete: its query may be replaced
+        if (!mbar_poll_warp(s_full + 8 * (set ^ 1), ((i - 1) >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+        load_q(tile.w, tile.z & TILE_ODD);
+      }
+      const float sj = *reinterpret_cast<const float*>(smem + SM::SC_OFF + set * 512 + row * 4);
       const bool valid = row < tile.x && (((uint32_t)tile.y >> (row >> box_log)) & 1u);
-      const bool last = tile.z != 0;
       // 2^k_j; rows never written (scale 0) count as zero rows
       const int kj = max(C8_KMIN, min(C8_KMAX, (int)(__float_as_uint(sj) >> 23) - 127));
-      if (!mbar_wait_warp(s_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      if (!mbar_poll_warp(s_full + 8 * set, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       tc_fence_after();
-      float y[8];
+      float y[16];
       {
-        uint32_t u[16], rp[8];
-        const uint32_t sa = tmem + SM::SB * b + lane_base;
-        tmem_ld16(sa + 16 * wg, u);
-        tmem_ld8(sa + 2 * NH + 8 * wg, rp);
+        const float* sq = slq + (tile.z & TILE_ODD ? 16 : 0);
+        const uint32_t sa = tmem + SM::TM_S + 64 * set + lane_base;
+        uint32_t u[32], rp[16];
+        tmem_ld16(sa, u);
+        tmem_ld16(sa + 16, u + 16);
+        tmem_ld16(sa + 32, rp);
         tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) { mbar_arrive(s_free + 8 * b); mbar_arrive(rempty + 8 * b); }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float4 s4 = *reinterpret_cast<const float4*>(slq + 4 * k);
+        for (int k = 0; k < 4; ++k) {
+          const float4 s4 = *reinterpret_cast<const float4*>(sq + 4 * k);
           const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int h = 4 * k + j;
-            const float uu = __uint_as_float(u[h]) + __uint_as_float(u[8 + h]);
-            const float r = fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj);
-            y[h] = valid ? fmaf(uu, sj * sv[j], r) : -INFINITY;
+            const int h = 4 * k + j, at = 16 * (h >> 3) + (h & 7);
+            const float uu = __uint_as_float(u[at]) + __uint_as_float(u[at + 8]);
+            y[h] = fmaf(uu, sj * sv[j], fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj));
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) { mbar_arrive(s_free + 8 * set); mbar_arrive(rempty + 8 * set); }
       }
-      // the tile's largest per head: within the warp, then over the four warps by lane h for head h
-      {
-        float mx[8];
+      if (tile.x < 128 || (uint32_t)tile.y != all_boxes) {   // also drops NaN in rows that are no keys
 #pragma unroll
-        for (int h = 0; h < 8; ++h) mx[h] = warp_max_f32(y[h]);
-        if (lane == 0) {
-          float4* rr = reinterpret_cast<float4*>(red + (b * 4 + q) * NH + 8 * wg);
-          rr[0] = make_float4(mx[0], mx[1], mx[2], mx[3]);
-          rr[1] = make_float4(mx[4], mx[5], mx[6], mx[7]);
-        }
+        for (int h = 0; h < 16; ++h) y[h] = valid ? y[h] : -INFINITY;
+      }
+      // the tile's largest per head: within the warp here, over the set's four warps by lane h for head h
+      const int slot = set * 2 + ((i >> 1) & 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 mx;
+        mx.x = warp_max_f32(y[4 * k]);
+        mx.y = warp_max_f32(y[4 * k + 1]);
+        mx.z = warp_max_f32(y[4 * k + 2]);
+        mx.w = warp_max_f32(y[4 * k + 3]);
+        if (lane == 0) *reinterpret_cast<float4*>(red + (slot * 4 + q) * 16 + 4 * k) = mx;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(red_b + 8 * b);
-      if (!mbar_wait_warp(red_b + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      if (lane == 0) mbar_arrive(red_b + 8 * slot);
+      // W(i - 2) has been consumed, and O^T of this set is at rest
+      if (!mbar_poll_warp(p_free + 8 * set, ((i >> 1) & 1) ^ 1, abort_word, a.flag) ||
+          !mbar_poll_warp(red_b + 8 * slot, (i >> 2) & 1, abort_word, a.flag)) {
+        ok = false;
+        break;
+      }
+      const bool fresh = first || prev_first;   // this set's first tile of the entry
       {
+        // Move R up when a head's largest is above it, down when the largest of late (`recent` forgets an
+        // octave a tile) is below R - 6; then to two to three octaves above, and with it the heads that
+        // are about to move up; not below 2^-40 of the largest seen, where a tile no longer counts (and
+        // 2^(old - new) stays far from overflow). The four warps decide alike.
         float m = -INFINITY;
-        if (lane < NH) {
-          const float* rr = red + b * 4 * NH + lane;
-          m = fmaxf(fmaxf(rr[0], rr[NH]), fmaxf(rr[2 * NH], rr[3 * NH]));
+        if (lane < 16) {
+          const float* rr = red + slot * 64 + lane;
+          m = fmaxf(fmaxf(rr[0], rr[16]), fmaxf(rr[32], rr[48]));
         }
-        // Move R when some head's largest leaves [R - 9, R], and with it the heads that are about to;
-        // not below 2^-40 of the largest seen, where a tile no longer counts (and 2^(old - new) stays
-        // far from overflow). Every warp decides alike.
+        if (fresh) R = top = recent = -INFINITY;
         top = fmaxf(top, m);
-        const float want = fmaxf(ceilf(m) + 5.f, top - 40.f);
-        const bool move = m > -INFINITY && (m > R || (m < R - 9.f && want < R));
-        if (__any_sync(0xffffffffu, move)) {
+        recent = fmaxf(recent - 1.f, m);
+        const float want = fmaxf(ceilf(recent) + 2.f, top - 40.f);
+        const bool move = recent > -INFINITY && (m > R || (recent < R - 6.f && want < R));
+        if (__any_sync(0xffffffffu, move) || fresh) {
           float al = 1.f;
-          if (move || m > R - 2.f) {
+          if (move || m > R - 1.f) {
             if (R > -INFINITY) al = ex2_approx(R - want);
             R = want;
           }
-          if ((lane >> 3) == wg) {
-            ref_w[lane & 7] = R == -INFINITY ? 8.f : 8.f - R;
-            al_w[lane & 7] = al;
+          if (lane < 16) {
+            ref_w[lane] = R == -INFINITY ? 8.f : 8.f - R;
+            al_w[lane] = al;
           }
           __syncwarp();
-          if (!first) {
-            // P.V(i - 1) has to be complete; its buffer's barrier says so, and nothing later is under way
-            if (!mbar_wait_warp(p_free + 8 * (b ^ 1), ((i - 1) >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+          if (!fresh) {
             tc_fence_after();
-            float f[8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float4 v = *reinterpret_cast<const float4*>(al_w + 4 * k);
-              f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
-            }
+            for (int o = 0; o < 2; ++o) {
+              const float4 f0 = *reinterpret_cast<const float4*>(al_w + 8 * o), f1 = *reinterpret_cast<const float4*>(al_w + 8 * o + 4);
+              const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-            for (int h = 0; h < 8; ++h) l[h] *= f[h];
+              for (int h = 0; h < 8; ++h) l[8 * o + h] *= f[h];
+              uint32_t v[64];
 #pragma unroll
-            for (int g = 0; g < 4; g += 2) {
-              uint32_t o[32];
-              const uint32_t oa = tmem + SM::TM_O + g * 2 * NH + 16 * wg + lane_base;
-              tmem_ld16(oa, o);
-              tmem_ld16(oa + 2 * NH, o + 16);
+              for (int g = 0; g < 4; ++g) tmem_ld16(tm_o + 128 * set + 32 * g + 16 * o, v + 16 * g);
               tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < 32; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * f[h & 7]);
-              tmem_st16(oa, o);
-              tmem_st16(oa + 2 * NH, o + 16);
+              for (int h = 0; h < 64; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h & 7]);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) tmem_st16(tm_o + 128 * set + 32 * g + 16 * o, v + 16 * g);
             }
             tmem_st_wait();
             tc_fence_before();
           }
         }
       }
-      first = last;
-      // W(i - 2) has been consumed
-      if (!mbar_wait_warp(p_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
       const float un = exp2_int(-kj);
-      {
-        uint8_t* pb = smem + SM::P_OFF + b * SM::PB + wg * 16 * 128 + (row & 15);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float4 r4 = *reinterpret_cast<const float4*>(ref_w + 4 * k);
-          const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
+      for (int k = 0; k < 4; ++k) {
+        const float4 r4 = *reinterpret_cast<const float4*>(ref_w + 4 * k);
+        const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            const int h = 4 * k + j;
-            const float e0 = ex2_approx(y[h] + rv[j]), e1 = ex2_approx(y[h + 1] + rv[j + 1]);
-            l[h] = fmaf(e0, un, l[h]);
-            l[h + 1] = fmaf(e1, un, l[h + 1]);
-            const uint16_t c_hi = e4m3x2_sat(e0, e1);
-            const float2 back = e4m3x2_f32(c_hi);
-            const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
-            uint8_t* p0 = pb + h * 128 + (((row >> 4) ^ h) << 4);
-            uint8_t* p1 = pb + (h + 1) * 128 + (((row >> 4) ^ (h + 1)) << 4);
-            p0[0] = (uint8_t)c_hi;
-            p1[0] = (uint8_t)(c_hi >> 8);
-            p0[8 * 128] = (uint8_t)c_lo;
-            p1[8 * 128] = (uint8_t)(c_lo >> 8);
-          }
+        for (int j = 0; j < 4; j += 2) {
+          const int h = 4 * k + j;
+          const float e0 = ex2_approx(y[h] + rv[j]), e1 = ex2_approx(y[h + 1] + rv[j + 1]);
+          l[h] = fmaf(e0, un, l[h]);
+          l[h + 1] = fmaf(e1, un, l[h + 1]);
+          const uint16_t c_hi = e4m3x2_sat(e0, e1);
+          const float2 back = e4m3x2_f32(c_hi);
+          const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
+          uint8_t* p0 = pb + (16 * (h >> 3) + (h & 7)) * 128 + (((row >> 4) ^ (h & 7)) << 4);
+          uint8_t* p1 = pb + (16 * (h >> 3) + (h & 7) + 1) * 128 + (((row >> 4) ^ ((h & 7) + 1)) << 4);
+          p0[0] = (uint8_t)c_hi;
+          p1[0] = (uint8_t)(c_hi >> 8);
+          p0[8 * 128] = (uint8_t)c_lo;
+          p1[8 * 128] = (uint8_t)(c_lo >> 8);
         }
       }
       if (!valid) {
-        // rows past the end may hold anything (even NaN codes); their weight is 0, but 0 * NaN is not.
-        // Four 128-byte runs per row, shared out over the warpgroups
+        // rows past the end may hold anything (even NaN codes); their weight is 0, but 0 * NaN is not
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          if (g % NWG != wg) continue;
           uint8_t* rp = smem + SM::RING_OFF + ((2 * i + (g >> 1)) % NPR) * 32768 + (row >> 3) * 2048 + (g & 1) * 1024 +
                         (row & 7) * 128;
 #pragma unroll
           for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(rp + 16 * k) = make_uint4(0, 0, 0, 0);
         }
       }
+      if (row == 0) pv_fresh[set] = fresh;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * b);
-      if (last) {
-        // the scores of this entry are all read: the next entry's query may replace its own. What the
-        // TMA warp says of the next tile comes first
-        const int e = tile.w;
-        if (i + 1 < N) {
-          if (!mbar_wait_warp(rfull + 8 * (b ^ 1), ((i + 1) >> 1) & 1, abort_word, a.flag) || !load_q(tile_s[b ^ 1].w)) {
-            ok = false;
-            break;
-          }
-        }
-        const long long unit = (long long)hg * (a.units + a.n_ent) + c + e;
-        const long long r0 = a.flat ? (long long)e * NH : (long long)hg * NH;
-        const int live = (int)min((long long)NH, (a.flat ? a.rows_total : (long long)a.H) - r0) - 8 * wg;
+      if (lane == 0) mbar_arrive(p_full + 8 * set);
+      if (left <= 1) {   // the set's last tile of the entry: its row sums and references, for the end
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
+        for (int h = 0; h < 16; ++h) {
           const float v = warp_sum(l[h]);
-          if (lane == 0) rl[q * 8 + h] = v;
+          if (lane == 0) rl[((i & 3) * 4 + q) * 16 + h] = v;
           l[h] = 0.f;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(l_b);
-        // thread <-> latent column
-        if (!mbar_wait_warp(p_free + 8 * b, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
-        tc_fence_after();
-        float* po = a.part_o + (unit * NH + 8 * wg) * 512 + row;
+        if (q == 0 && lane < 16) rp_s[(i & 3) * 16 + lane] = R;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(post_b + 8 * (i & 3));
+      if (left > 0) continue;
+      // The entry's last tile here: both sets' sums and O^T, brought to the larger of their references;
+      // thread <-> latent column. (The other set is at most one tile ahead: the scores of its tile i + 3
+      // wait for this set to have read those of tile i + 2.)
+      if (!mbar_poll_warp(post_b + 8 * (i & 3), (i >> 2) & 1, abort_word, a.flag)) { ok = false; break; }
+      if (!first && !mbar_poll_warp(post_b + 8 * ((i - 1) & 3), ((i - 1) >> 2) & 1, abort_word, a.flag)) { ok = false; break; }
+      const long long unit = (long long)hg * (a.units + a.n_ent) + c + tile.w;
+      const int live = (int)min(16LL, a.flat ? a.rows_total - 16LL * tile.w : (long long)a.H - 16 * hg);
+      if (lane < 16) {
+        const float Ro = first ? -INFINITY : rp_s[((i - 1) & 3) * 16 + lane], Rc = fmaxf(R, Ro);
+        const float fa = R == -INFINITY ? 0.f : ex2_approx(R - Rc), fb = Ro == -INFINITY ? 0.f : ex2_approx(Ro - Rc);
+        ref_w[lane] = fa;
+        al_w[lane] = fb;
+        if (q == 0 && lane < live) {   // natural-log units; the weights carry the factor 2^8
+          const float* ra = rl + (i & 3) * 64 + lane;
+          const float* rb = rl + ((i - 1) & 3) * 64 + lane;
+          float sum = fa > 0.f ? fa * (ra[0] + ra[16] + ra[32] + ra[48]) : 0.f;
+          if (fb > 0.f) sum += fb * (rb[0] + rb[16] + rb[32] + rb[48]);
+          *reinterpret_cast<float2*>(a.part_ml + (unit * 16 + lane) * 2) = make_float2((Rc - 8.f) * 0.69314718055994531f, sum);
+        }
+      }
+      __syncwarp();
+      if (!mbar_poll_warp(p_free + 8 * set, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      if (!first && !mbar_poll_warp(p_free + 8 * (set ^ 1), ((i - 1) >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      tc_fence_after();
+      float* po = a.part_o + unit * 16 * 512 + row;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t o[16];
-          tmem_ld16(tmem + SM::TM_O + g * 2 * NH + 16 * wg + lane_base, o);
+      for (int g = 0; g < 4; ++g) {
+        uint32_t o[32];
+        float out[16];
+        tmem_ld16(tm_o + 128 * set + 32 * g, o);
+        tmem_ld16(tm_o + 128 * set + 32 * g + 16, o + 16);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 16; ++h)
+          out[h] = __uint_as_float(o[16 * (h >> 3) + (h & 7)]) + __uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]);
+        if (!first) {
+          tmem_ld16(tm_o + 128 * (set ^ 1) + 32 * g, o);
+          tmem_ld16(tm_o + 128 * (set ^ 1) + 32 * g + 16, o + 16);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < 8; ++h)
-            if (h < live) po[h * 512 + 128 * g] = __uint_as_float(o[h]) + __uint_as_float(o[8 + h]);
+          for (int h = 0; h < 16; ++h) {
+            const float fa = ref_w[h], fb = al_w[h];
+            const float ob = __uint_as_float(o[16 * (h >> 3) + (h & 7)]) + __uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]);
+            out[h] = (fa > 0.f ? fa * out[h] : 0.f) + (fb > 0.f ? fb * ob : 0.f);
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
-        if (!mbar_wait_warp(l_b, (kl++) & 1, abort_word, a.flag)) { ok = false; break; }
-        if (q == 0 && (lane >> 3) == wg) {
-          const int h = lane & 7;
-          if (h < live)   // natural-log units; w carries the factor 2^8
-            *reinterpret_cast<float2*>(a.part_ml + (unit * NH + 8 * wg + h) * 2) =
-                make_float2((R - 8.f) * 0.69314718055994531f, rl[h] + rl[8 + h] + rl[16 + h] + rl[24 + h]);
-        }
-        R = -INFINITY;
-        top = -INFINITY;
-        if (lane < 8) ref_w[lane] = 8.f;
-        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 16; ++h)
+          if (h < live) po[h * 512 + 128 * g] = out[h];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(o_free + 8 * set);
+        if (!first) mbar_arrive(o_free + 8 * (set ^ 1));
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -144,11 +144,12 @@ class Case:
         e_p: 16-bit: a probability in bf16, or in two E4M3 parts (2^-4 of 2^-4), 2^-8 either way.
           fp32 act: exponentials and sums, 64 2^-24.
         The two-part weights w_j = 2^8 p_j s_j / 2^R have an absolute floor besides: the second part's
-        smallest step is 2^-9, so w_j is off by up to 2^-10 however light the key; the reference 2^R is
-        at most 2^9 of the largest p_i s_i among the tile's 128 keys (or 2^-40 of the largest of all), so
-        p_j s_j is off by up to 2^-9 of the tile's largest. What it multiplies is the code, so o is off
-        by up to the sum over tiles of 2^-9 max_i(p_i s_i) sum_j |code_j|; the sums that normalise take
-        the weights unrounded. o is then rounded once to its type.
+        smallest step is 2^-9, so w_j is off by up to 2^-10 however light the key, p_j s_j by 2^-18 2^R.
+        2^R is at most 2^6 of the largest of late, which forgets an octave every second tile:
+        rec_t = max(largest p_i s_i of tile t, 2^-1/2 rec_(t-1)) over a pass's tiles of 128 keys (or
+        2^-40 of the largest of all), so p_j s_j is off by up to 2^-12 rec_t. What it multiplies is the
+        code, so o is off by up to the sum over tiles of 2^-12 rec_t sum_j |code_j|; the sums that
+        normalise take the weights unrounded. o is then rounded once to its type.
     """
         s = self.shape
         r = s.kv_lora_rank
@@ -174,9 +175,11 @@ class Case:
                     code, ps = np.abs(c) / sc[:, None], p * sc
                     floor = 2.0 ** -50 * ps.max(1)[:, None] * code.sum(0)[None]
                     for a0, a1 in ((0, self.prefix_len), (self.prefix_len, len(k))):   # the passes' tiles
+                        rec = np.zeros(len(ps))
                         for j in range(a0, a1, 128):
                             m = min(j + 128, a1)
-                            floor = floor + 2.0 ** -9 * ps[:, j:m].max(1)[:, None] * code[j:m].sum(0)[None]
+                            rec = np.maximum(rec * 2.0 ** -0.5, ps[:, j:m].max(1))
+                            floor = floor + 2.0 ** -12 * rec[:, None] * code[j:m].sum(0)[None]
             else:
                 e = (e.max(1) if len(k) else np.zeros(len(p))) + 64 * 2.0 ** -24
                 step = 2.0 ** -24

@@ -145,6 +145,12 @@ ATTN = {
     "prefix_5_heads": (5, 64, [i % 3 for i in range(67)], 64),
     "prefix_long": (16, 64, [100, 7], 1500),
     "prefix_odd_block": (8, 7, [20, 0, 9], 33),
+    "128_heads_blocks_of_16": (128, 16, [33, 200], 50),
+    "128_heads_long": (128, 64, [1500, 64], 0),
+    "128_heads_many_tiles": (128, 64, [5000 - 61 * i for i in range(40)], 0),
+    "80_heads": (80, 128, [70, 333], 140),
+    "prefix_tiny": (8, 64, [3, 0], 700),
+    "prefix_many_tiles": (16, 64, [1] * 40, 9000),
 }
 
 
