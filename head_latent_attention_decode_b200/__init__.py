@@ -311,83 +311,95 @@ def mla_cache_block_bytes(handle) -> int:
     return int(lib().mla_cache_block_bytes(handle))
 
 
-def _check_tensors(where: str, need: dict, ints: dict) -> None:
-    """Contiguous tensors on one device; `ints` (name -> tensor) are int32."""
-    dev = None
-    for name, t in {**need, **ints}.items():
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{where}: {name} must be a contiguous device tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, not on {dev}")
-        dev = t.device
-    for name, t in ints.items():
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{where}: {name} must be int32")
+def _bad_tensor(where: str, name: str, t) -> ValueError:
+    return ValueError(f"{where}: {name} must be a contiguous tensor on one device with the others, int32 if it holds "
+                      f"slots, blocks or lengths; got {t.dtype} on {t.device}, strides {tuple(t.stride())}")
+
+
+def _check_tensors(where: str, need: tuple, ints: tuple) -> int:
+    """Contiguous tensors on one device, those of `ints` int32; (name, tensor or None) pairs. The device's index."""
+    dev = need[0][1].get_device()
+    for name, t in need:
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.get_device() == dev):
+            raise _bad_tensor(where, name, t)
+    for name, t in ints:
+        if t is not None and not (t.is_cuda and t.dtype is torch.int32 and t.is_contiguous() and t.get_device() == dev):
+            raise _bad_tensor(where, name, t)
+    return dev
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The given stream, or the device's current one (the raw lookup: these calls can be a few microseconds apart)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def mla_cache_write(handle, rows, kv_cache, slot_mapping, ws, stream=None) -> None:
     """rows [n, R] into the cache's flat rows slot_mapping [n] (negative: skipped),
     quantised if the handle's cache is 8-bit."""
-    _check_tensors("mla_cache_write", dict(rows=rows, kv_cache=kv_cache, ws=ws), dict(slot_mapping=slot_mapping))
-    if slot_mapping.numel() != rows.shape[0]:
+    dev = _check_tensors("mla_cache_write", (("rows", rows), ("kv_cache", kv_cache), ("ws", ws)),
+                         (("slot_mapping", slot_mapping),))
+    n = rows.shape[0]
+    if slot_mapping.numel() != n:
         raise ValueError("mla_cache_write: one slot per row")
-    _check(lib().mla_cache_write(handle, _ptr(rows), rows.shape[0], _ptr(kv_cache), kv_cache.shape[0],
-                                 _ptr(slot_mapping), _ptr(ws), _nbytes(ws), _stream(stream)), "mla_cache_write")
+    _check(lib().mla_cache_write(handle, rows.data_ptr(), n, kv_cache.data_ptr(), kv_cache.shape[0],
+                                 slot_mapping.data_ptr(), ws.data_ptr(), ws.nbytes, _stream_on(stream, dev)),
+           "mla_cache_write")
 
 
 def mla_cache_read(handle, kv_cache, slots, rows, ws, stream=None) -> None:
     """rows [n, R] = the values of the cache's flat rows slots [n] (negative: left as it was)."""
-    _check_tensors("mla_cache_read", dict(kv_cache=kv_cache, rows=rows, ws=ws), dict(slots=slots))
-    if slots.numel() != rows.shape[0]:
+    dev = _check_tensors("mla_cache_read", (("rows", rows), ("kv_cache", kv_cache), ("ws", ws)), (("slots", slots),))
+    n = rows.shape[0]
+    if slots.numel() != n:
         raise ValueError("mla_cache_read: one slot per row")
-    _check(lib().mla_cache_read(handle, _ptr(kv_cache), kv_cache.shape[0], _ptr(slots), rows.shape[0], _ptr(rows),
-                                _ptr(ws), _nbytes(ws), _stream(stream)), "mla_cache_read")
+    _check(lib().mla_cache_read(handle, kv_cache.data_ptr(), kv_cache.shape[0], slots.data_ptr(), n, rows.data_ptr(),
+                                ws.data_ptr(), ws.nbytes, _stream_on(stream, dev)), "mla_cache_read")
 
 
 def mla_prefix_workspace_bytes(handle, max_tokens: int, max_prefix_len: int, max_context_len: int) -> int:
     return int(lib().mla_prefix_workspace_bytes(handle, int(max_tokens), int(max_prefix_len), int(max_context_len)))
 
 
-def _check_latent(where, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens, more):
-    _check_tensors(where, dict(q_abs=q_abs, q_pe=q_pe, kv_cache=kv_cache, **more),
-                   dict(prefix_table=prefix_table, block_table=block_table, context_lens=context_lens))
-    n = q_abs.shape[0]
-    if q_abs.dim() != 3 or q_pe.shape[:2] != q_abs.shape[:2] or q_pe.dtype != q_abs.dtype:
+def _check_latent(where, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens, more) -> int:
+    dev = _check_tensors(where, (("q_abs", q_abs), ("q_pe", q_pe), ("kv_cache", kv_cache), *more),
+                         (("prefix_table", prefix_table), ("block_table", block_table), ("context_lens", context_lens)))
+    qs, ps, ts = q_abs.shape, q_pe.shape, block_table.shape
+    if len(qs) != 3 or len(ps) != 3 or ps[0] != qs[0] or ps[1] != qs[1] or q_pe.dtype is not q_abs.dtype:
         raise ValueError(f"{where}: q_abs [n, H, r_kv] and q_pe [n, H, d_r] of one dtype")
-    if block_table.dim() != 2 or block_table.shape[0] != n or context_lens.numel() != n:
+    if len(ts) != 2 or ts[0] != qs[0] or context_lens.numel() != qs[0]:
         raise ValueError(f"{where}: block_table [n, blocks] and context_lens [n]")
     if prefix_len and prefix_table is None:
         raise ValueError(f"{where}: prefix_len without a prefix_table")
+    return dev
 
 
 def mla_latent_attn(handle, q_abs, q_pe, kv_cache, block_table, context_lens, max_context_len, o_lat, ws,
                     lse=None, prefix_table=None, prefix_len: int = 0, stream=None) -> None:
     """o_lat [n, H, r_kv] (and lse [n, H] fp32) of the shared prefix's keys followed by each
     sequence's own (see include/mla.h). The prefix_table must cover prefix_len rows."""
-    _check_latent("mla_latent_attn", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
-                  dict(o_lat=o_lat, lse=lse, ws=ws))
-    if o_lat.shape != q_abs.shape or o_lat.dtype != q_abs.dtype:
+    dev = _check_latent("mla_latent_attn", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
+                        (("o_lat", o_lat), ("lse", lse), ("ws", ws)))
+    if o_lat.shape != q_abs.shape or o_lat.dtype is not q_abs.dtype:
         raise ValueError("mla_latent_attn: o_lat must have q_abs's shape and dtype")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q_abs.shape[:2]):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != q_abs.shape[:2]):
         raise ValueError("mla_latent_attn: lse must be fp32 [n, H]")
-    _check(lib().mla_latent_attn(handle, _ptr(q_abs), _ptr(q_pe), _ptr(kv_cache), kv_cache.shape[0],
-                                 _ptr(prefix_table) if prefix_len else None, int(prefix_len), _ptr(block_table),
-                                 block_table.shape[1], _ptr(context_lens), int(max_context_len), q_abs.shape[0],
-                                 _ptr(o_lat), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)), "mla_latent_attn")
+    _check(lib().mla_latent_attn(handle, q_abs.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
+                                 prefix_table.data_ptr() if prefix_len else None, prefix_len, block_table.data_ptr(),
+                                 block_table.shape[1], context_lens.data_ptr(), max_context_len, q_abs.shape[0],
+                                 o_lat.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                 _stream_on(stream, dev)), "mla_latent_attn")
 
 
 def mla_decode_attn_prefix(handle, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
                            max_context_len, out, ws, head_out=None, stream=None) -> None:
     """mla_decode_attn over a prefix shared by the batch followed by each sequence's own rows."""
-    _check_latent("mla_decode_attn_prefix", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table,
-                  context_lens, dict(out=out, head_out=head_out, ws=ws))
-    _check(lib().mla_decode_attn_prefix(handle, _ptr(q_abs), _ptr(q_pe), _ptr(kv_cache), kv_cache.shape[0],
-                                        _ptr(prefix_table) if prefix_len else None, int(prefix_len),
-                                        _ptr(block_table), block_table.shape[1], _ptr(context_lens),
-                                        int(max_context_len), q_abs.shape[0], _ptr(out), _ptr(head_out), _ptr(ws),
-                                        _nbytes(ws), _stream(stream)), "mla_decode_attn_prefix")
+    dev = _check_latent("mla_decode_attn_prefix", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table,
+                        context_lens, (("out", out), ("head_out", head_out), ("ws", ws)))
+    _check(lib().mla_decode_attn_prefix(handle, q_abs.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(),
+                                        kv_cache.shape[0], prefix_table.data_ptr() if prefix_len else None, prefix_len,
+                                        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+                                        max_context_len, q_abs.shape[0], out.data_ptr(), _ptr(head_out), ws.data_ptr(),
+                                        ws.nbytes, _stream_on(stream, dev)), "mla_decode_attn_prefix")
 
 
 def mla_kernel_launch_count() -> int:

@@ -31,7 +31,8 @@ struct MergeSrc {
   long long group_units;   // units of one group of `rows` heads (flat = 0)
   int half;             // columns c >= half use the second (m, l) copy (0: one copy)
   int splits, rows;
-  int flat;             // entry = (t H + h) / rows; otherwise entry = t, and head group h / rows
+  int flat;             // entry = (t H + h) / rows; otherwise entry = e0 + t, and head group h / rows
+  int e0;
 };
 struct MergeArgs {
   MergeSrc src[2];
@@ -53,7 +54,7 @@ __device__ __forceinline__ long long merge_units(const MergeSrc& s, int H, int t
     e = q / s.rows;
     *row = (int)(q % s.rows);
   } else {
-    e = t;
+    e = s.e0 + t;
     g = h / s.rows;
     *row = h % s.rows;
   }
@@ -71,39 +72,54 @@ __device__ __forceinline__ long long merge_units(const MergeSrc& s, int H, int t
 // token's 150 partials of 2 KB are a latency chain for a single group).
 template <typename T>
 __global__ void __launch_bounds__(1024) latent_merge_kernel(MergeArgs p) {
-  griddep_wait();
-  griddep_launch_dependents();
   __shared__ float wsh[2][MERGE_MAX];
   __shared__ float inv_sh[2];
   extern __shared__ float4 accs[];   // [G][128]
   const int t = blockIdx.x, h = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the lengths and the sink are older than the kernels that this one waits for
   const int L = p.ctx[t];
+  const float z = p.sink ? p.sink[h] : -INFINITY;
+  griddep_wait();
+  griddep_launch_dependents();
   const bool live = L >= p.min_ctx && L <= p.max_ctx && (long long)L <= p.cap;
-  int cnt[2] = {0, 0}, row[2] = {0, 0};
-  long long unit[2] = {0, 0};
-  for (int k = 0; k < p.n_src; ++k) unit[k] = merge_units(p.src[k], p.H, t, h, &cnt[k], &row[k]);
-  if (!live) cnt[0] = cnt[1] = 0;
-  cnt[0] = min(cnt[0], MERGE_MAX);
-  const int total = min(cnt[0] + cnt[1], MERGE_MAX);
+  int cnt0 = 0, cnt1 = 0, row0 = 0, row1 = 0;
+  long long unit0 = merge_units(p.src[0], p.H, t, h, &cnt0, &row0), unit1 = 0;
+  if (p.n_src > 1) unit1 = merge_units(p.src[1], p.H, t, h, &cnt1, &row1);
+  if (!live) cnt0 = cnt1 = 0;
+  cnt0 = min(cnt0, MERGE_MAX);
+  const int total = min(cnt0 + cnt1, MERGE_MAX);
+  // query row of partial i in its source's [units, rows] (source 1 from i = cnt0 on)
+  auto at = [&](int i) {
+    return i < cnt0 ? (unit0 + i) * p.src[0].rows + row0 : (unit1 + i - cnt0) * p.src[1].rows + row1;
+  };
+  const int c = (threadIdx.x & 127) * 4, grp = threadIdx.x >> 7, G = blockDim.x >> 7;
+  auto part = [&](int i) {
+    return *reinterpret_cast<const float4*>((i < cnt0 ? p.src[0].o : p.src[1].o) + at(i) * (long long)p.r_kv + c);
+  };
+  // the first partials are on their way while the weights are made
+  constexpr int PRE = 4;
+  float4 pre[PRE];
+#pragma unroll
+  for (int k = 0; k < PRE; ++k) {
+    const int i = grp + k * G;
+    pre[k] = c < p.r_kv && i < total ? part(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   if (warp < 2) {   // warp w: the weights from (m, l) copy w
     auto stats = [&](int i) {
-      const int k = i >= cnt[0];
-      const MergeSrc& s = p.src[k];
-      const long long at = (unit[k] + i - (k ? cnt[0] : 0)) * s.rows + row[k];
-      return *reinterpret_cast<const float2*>(s.ml + (warp && s.half ? s.ml_r : 0) + at * 2);
+      const MergeSrc& s = p.src[i < cnt0 ? 0 : 1];
+      return *reinterpret_cast<const float2*>(s.ml + (warp && s.half ? s.ml_r : 0) + at(i) * 2);
     };
-    float M = -INFINITY;
-    for (int i = lane; i < total; i += 32) {
+    float2 v0 = lane < total ? stats(lane) : make_float2(-INFINITY, 0.f);
+    float M = v0.y > 0.f ? v0.x : -INFINITY;
+    for (int i = lane + 32; i < total; i += 32) {
       const float2 v = stats(i);
       if (v.y > 0.f) M = fmaxf(M, v.x);
     }
-    M = warp_max(M);
-    const float z = p.sink ? p.sink[h] : -INFINITY;
-    M = fmaxf(M, z);
+    M = fmaxf(warp_max(M), z);
     float den = 0.f;
     for (int i = lane; i < total; i += 32) {
-      const float2 v = stats(i);
+      const float2 v = i == lane ? v0 : stats(i);
       const float w = v.y > 0.f ? __expf(v.x - M) : (v.y != v.y ? v.y : 0.f);   // a NaN sum stays NaN
       wsh[warp][i] = w;
       den += w == 0.f ? 0.f : w * v.y;
@@ -115,20 +131,20 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(MergeArgs p) {
     }
   }
   __syncthreads();
-  const int c = (threadIdx.x & 127) * 4, grp = threadIdx.x >> 7, G = blockDim.x >> 7;
+  // a source with one (m, l) copy is weighed by it for every column: both warps read the same one
+  const int copy = (p.src[0].half && c >= p.src[0].half) || (p.n_src > 1 && p.src[1].half && c >= p.src[1].half);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, const float4& v) {
+    if (w == 0.f) return;   // also where nothing was written
+    acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
+  };
   if (c < p.r_kv) {
+#pragma unroll
+    for (int k = 0; k < PRE; ++k)
+      if (grp + k * G < total) add(wsh[copy][grp + k * G], pre[k]);
 #pragma unroll 4
-    for (int i = grp; i < total; i += G) {
-      const int k = i >= cnt[0];
-      const MergeSrc& s = p.src[k];
-      const float w = wsh[s.half && c >= s.half ? 1 : 0][i];
-      if (w == 0.f) continue;
-      const float4 v = *reinterpret_cast<const float4*>(
-          s.o + ((unit[k] + i - (k ? cnt[0] : 0)) * s.rows + row[k]) * (long long)p.r_kv + c);
-      acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
-    }
+    for (int i = grp + PRE * G; i < total; i += G) add(wsh[copy][i], part(i));
   }
   if (G > 1) {
     accs[threadIdx.x] = acc;
@@ -140,11 +156,15 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(MergeArgs p) {
       }
   }
   if (grp > 0 || c >= p.r_kv) return;
-  // the two copies differ only where a source has two; both cover every source
-  const float inv = inv_sh[(p.src[0].half && c >= p.src[0].half) || (p.n_src > 1 && p.src[1].half && c >= p.src[1].half)];
-  T* o = (T*)p.o + ((long long)t * p.H + h) * p.r_kv + c;
-  o[0] = from_f32<T>(acc.x * inv); o[1] = from_f32<T>(acc.y * inv);
-  o[2] = from_f32<T>(acc.z * inv); o[3] = from_f32<T>(acc.w * inv);
+  const float inv = inv_sh[copy];
+  T o[4] = {from_f32<T>(acc.x * inv), from_f32<T>(acc.y * inv), from_f32<T>(acc.z * inv), from_f32<T>(acc.w * inv)};
+  T* dst = (T*)p.o + ((long long)t * p.H + h) * p.r_kv + c;   // a multiple of four elements from an output
+  if (((uintptr_t)p.o & (4 * sizeof(T) - 1)) == 0) {           // that may lie anywhere
+    if (sizeof(T) == 4) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(o);
+    else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(o);
+  } else {
+    for (int k = 0; k < 4; ++k) dst[k] = o[k];
+  }
 }
 
 }  // namespace mla
@@ -164,15 +184,17 @@ struct LatentCall {
 };
 
 // Which kernels a call takes, how many tokens at a time, and where their partials lie.
-enum LatentOwn { OWN_SIMT, OWN_TC16, OWN_FEW8, OWN_HEADS8 };     // the own rows
-enum LatentPre { PRE_NONE, PRE_HEADS16, PRE_FEW8, PRE_HEADS8 };  // the prefix
 struct LatentPlan {
-  int own, pre, chunk;     // chunk: tokens per pass
-  int splits;              // OWN_SIMT, OWN_TC16: splits of the keys
-  int units, units_p;      // slices of the tile list
-  int rows, rows_p;        // query rows per partial (own: per head group; prefix: per entry)
-  int groups, ents_p;      // OWN_FEW8: head groups; prefix entries
-  size_t o, ml, seg, o_p, ml_p, seg_p, total;
+  // The head-major launch takes the prefix, the own rows, or both; what it does not take runs on the
+  // few-head 8-bit kernel, on mla_decode_attn's 16-bit kernels (own rows), or, all of it, on CUDA cores.
+  bool heads_pre, heads_own, few_pre, few_own, own16, simt;
+  int chunk;               // tokens per pass
+  int splits;              // own16, simt: splits of the keys
+  int units, groups;       // few_own: slices of the tile list, head groups
+  int units_p, ents_p;     // few_pre: slices, entries
+  int units_h, pre_h;      // head-major: SM pairs, prefix entries
+  size_t o, ml, seg, o_h, ml_h, seg_h, total;   // own rows (or few_pre) apart; the head-major launch
+  size_t o_p, ml_p, seg_p;
 };
 
 static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned) {
@@ -184,59 +206,70 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   auto put = [&](size_t b) { size_t o = off; off = align_up(off + b, 256); return o; };
   // the tensor-core kernels: the DeepSeek latent, TMA boxes of whole parts of a block
   const bool tc = h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64;
-  const bool b64 = c.block_size % 64 == 0;
+  const bool b64 = c.block_size % 64 == 0, pre = prefix_len > 0;
+  const long long tiles = cdiv(max_ctx, 64);
+  // The own rows may ride in the prefix's head-major launch. With few heads that wastes most of its 128
+  // rows (2 us per 64 rows and SM pair whatever the heads), but saves a launch with its start-up and tail
+  // (about 17 us): worth it up to eight of such tiles per pair.
+  const bool ride = H <= 128 && n * tiles <= 8LL * pairs;
   if (tc && h->cache8 && c.block_size % 16 == 0) {
     // Per 128 keys the few-head kernel takes about 5 k cycles of one SM for every 16 heads, the
-    // head-major one about 5.6 k of two SMs whatever the number of heads up to 128 (blocks of 64 rows only)
-    w.own = b64 && H > 32 && H <= 128 ? OWN_HEADS8 : OWN_FEW8;
-    w.pre = prefix_len <= 0 ? PRE_NONE : (b64 && n * H > 32 ? PRE_HEADS8 : PRE_FEW8);
+    // head-major one about 9 k of two SMs whatever the heads up to 128.
+    w.heads_pre = pre && b64 && n * H > 32;
+    w.few_pre = pre && !w.heads_pre;
+    w.heads_own = b64 && H <= 128 && (H > 48 || (w.heads_pre && ride));
+    w.few_own = !w.heads_own;
   } else if (tc && !h->cache8 && b64 && H <= 128) {
-    w.own = OWN_TC16;
-    w.pre = prefix_len > 0 ? PRE_HEADS16 : PRE_NONE;
+    w.heads_pre = pre;
+    w.heads_own = pre && (H > 32 || ride);
+    w.own16 = !w.heads_own;
+  } else {
+    w.simt = true;
   }
   // tokens per pass: the kernels' entries (sequences; blocks of query rows) and tile lists
   long long most = n;
-  if (w.own == OWN_FEW8) most = A8_MAX_ENT;
-  if (w.own == OWN_HEADS8 || (w.own == OWN_TC16 && H > 32)) most = ATT_MAX_SEQ;
-  if ((w.pre == PRE_HEADS16 || w.pre == PRE_HEADS8) && most * H > ATT_MAX_SEQ * 128LL) most = ATT_MAX_SEQ * 128LL / H;
-  if (w.own != OWN_SIMT) {   // tiles are counted in int
-    const long long tiles = cdiv(max_ctx, 64), tiles_p = cdiv(prefix_len, 64) * cdiv(H, 16);
-    const long long fit = (1 << 30) / (tiles > tiles_p ? tiles : tiles_p);
-    if (most > fit) most = fit > 0 ? fit : 1;
+  auto limit = [&](long long m) { if (most > m) most = m > 0 ? m : 1; };
+  if (w.few_own) limit(A8_MAX_ENT);
+  if (w.own16 && H > 32) limit(ATT_MAX_SEQ);
+  if (w.heads_pre || w.heads_own) {   // chunk + ceil(chunk H / 128) entries
+    const long long per = (w.heads_own ? 128 : 0) + (w.heads_pre ? H : 0);
+    limit((ATT_MAX_SEQ - 1) * 128LL / per);
   }
-  w.chunk = (int)(n < most ? n : most);
-  if (w.own == OWN_FEW8) {
-    w.rows = 16;
+  if (!w.simt) {   // tiles are counted in int
+    const long long p = cdiv(prefix_len, 64) * cdiv(H, 16);
+    limit((1 << 29) / (tiles > p ? tiles : p));
+  }
+  w.chunk = (int)most;
+  if (w.few_own) {
     w.groups = (int)cdiv(H, 16);
     w.units = sms / w.groups > 0 ? sms / w.groups : 1;
     const size_t rows = (size_t)w.groups * (w.units + w.chunk) * 16;
     w.o = put(rows * 512 * 4);
     w.ml = put(rows * 2 * 4);
     w.seg = put((size_t)w.chunk * 8);
-  } else if (w.own == OWN_HEADS8) {
-    w.rows = H;
-    w.units = pairs;
-    const size_t rows = (size_t)(pairs + w.chunk) * H;
-    w.o = put(rows * 512 * 4);
-    w.ml = put(rows * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
-    w.seg = put((size_t)w.chunk * 8);
-  } else {
-    const long long s = cdiv((long long)(w.own == OWN_SIMT ? prefix_len : 0) + max_ctx, 256);
-    w.rows = H;
+  } else if (!w.heads_own) {
+    const long long s = cdiv((long long)(w.simt ? prefix_len : 0) + max_ctx, 256);
     w.splits = s < 2 ? 2 : (s > 16 ? 16 : (int)s);
     const size_t rows = (size_t)w.chunk * w.splits * H;
     w.o = put(rows * c.kv_lora_rank * 4);
-    w.ml = put(rows * 2 * 4 * 2);
+    w.ml = put(rows * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
     w.seg = put((size_t)w.chunk * 4);
   }
-  if (w.pre != PRE_NONE) {
-    w.rows_p = w.pre == PRE_FEW8 ? 16 : 128;
-    w.ents_p = (int)cdiv((long long)w.chunk * H, w.rows_p);
-    w.units_p = w.pre == PRE_FEW8 ? sms : pairs;
-    const size_t rows = (size_t)(w.units_p + w.ents_p) * w.rows_p;
+  if (w.few_pre) {
+    w.ents_p = (int)cdiv((long long)w.chunk * H, 16);
+    w.units_p = sms;
+    const size_t rows = (size_t)(w.units_p + w.ents_p) * 16;
     w.o_p = put(rows * 512 * 4);
-    w.ml_p = put(rows * 2 * 4 * 2);
+    w.ml_p = put(rows * 2 * 4);
     w.seg_p = put((size_t)w.ents_p * 8);
+  }
+  if (w.heads_pre || w.heads_own) {
+    w.units_h = pairs;
+    w.pre_h = w.heads_pre ? (int)cdiv((long long)w.chunk * H, 128) : 0;
+    const size_t ents = (size_t)w.pre_h + (w.heads_own ? w.chunk : 0), rows = (pairs + ents) * 128;
+    w.o_h = put(rows * 512 * 4);
+    w.ml_h = put(rows * 2 * 4 * 2);
+    w.seg_h = put(ents * 8);
   }
   w.total = off;
   return w;
@@ -327,20 +360,22 @@ static int pass_few8(const mla_handle* h, const LatentPlan& w, const LatentCall&
   return MLA_OK;
 }
 
-template <bool FLAT, bool C8>
-static void launch_heads(const CUtensorMap& m0, const CUtensorMap& m1, const TcAttnArgs& k, cudaStream_t s) {
+template <bool C8>
+static void launch_heads(const CUtensorMap& m0, const CUtensorMap& m1, const TcAttnArgs& k, const char* timer,
+                         cudaStream_t s) {
   static std::atomic<bool> attr[64];
-  set_smem_once(attr, tc_attn_decode_kernel<FLAT, C8>, AttnSmemT<C8>::SIZE);
-  mla_timer_begin(FLAT ? "attn_prefix" : "attn", s);
-  launch_pdl(tc_attn_decode_kernel<FLAT, C8>, 2 * k.units, ATT_THREADS, AttnSmemT<C8>::SIZE, s, m0, m1, k);
-  mla_timer_end(FLAT ? "attn_prefix" : "attn", s);
+  set_smem_once(attr, tc_attn_decode_kernel<true, C8>, AttnSmemT<C8>::SIZE);
+  mla_timer_begin(timer, s);
+  launch_pdl(tc_attn_decode_kernel<true, C8>, 2 * k.units, C8 ? ATT_THREADS8 : ATT_THREADS, AttnSmemT<C8>::SIZE, s, m0, m1,
+             k);
+  mla_timer_end(timer, s);
   mla_count_launch(1);
 }
 
-// A pass on the head-major kernel with packed partials: over the prefix, where its 128 MMA rows take
-// 128 query rows of any sequences, or (8-bit cache) over each sequence's own rows.
-static int pass_heads(const mla_handle* h, const LatentPlan& w, const LatentCall& a, bool pre, MergeArgs* m, char* scratch,
-                      int* flag, cudaStream_t s) {
+// The head-major launch: the prefix (its 128 MMA rows take 128 query rows of any sequences), the own
+// rows, or both, in one tile list.
+static int pass_heads(const mla_handle* h, const LatentPlan& w, const LatentCall& a, MergeArgs* m, char* scratch, int* flag,
+                      cudaStream_t s) {
   const mla_config& c = h->cfg;
   const int R = c.kv_lora_rank + c.qk_rope;
   const long long blocks = a.n_blocks > 0 ? a.n_blocks : 1;
@@ -357,30 +392,32 @@ static int pass_heads(const mla_handle* h, const LatentPlan& w, const LatentCall
     k.lat_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? 0 : c.qk_rope;
     k.rope_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? c.kv_lora_rank : 0;
   }
+  k.H = c.n_heads; k.rows_total = (long long)a.n * c.n_heads;
+  k.n_pre = w.heads_pre ? (int)cdiv(k.rows_total, 128) : 0;
+  k.n = k.n_pre + (w.heads_own ? a.n : 0);
+  k.fixed_len = a.prefix_len; k.pre_table = a.prefix_table;
+  k.block_table = a.table; k.mbps = a.mbps; k.ctx = a.ctx; k.max_ctx = a.max_ctx;
+  k.allow_empty = m->min_ctx == 0;
   k.bs = c.block_size; k.n_blocks = a.n_blocks;
   k.q_abs = (const bf16*)a.q_abs; k.q_pe = (const bf16*)a.q_pe;
   k.scale_log2 = h->scale * 1.4426950408889634f;
-  k.flag = flag; k.min_per = 1;
-  MergeSrc& q = m->src[m->n_src++];
-  if (pre) {
-    k.rows_total = (long long)a.n * c.n_heads;
-    k.n = (int)cdiv(k.rows_total, 128); k.H = 128;
-    k.fixed_len = a.prefix_len; k.block_table = a.prefix_table;
-    k.units = w.units_p;
-    k.part_o = (float*)(scratch + w.o_p); k.part_ml = (float*)(scratch + w.ml_p); k.seg = (int2*)(scratch + w.seg_p);
+  k.flag = flag; k.min_per = 1; k.units = w.units_h;
+  k.part_o = (float*)(scratch + w.o_h); k.part_ml = (float*)(scratch + w.ml_h); k.seg = (int2*)(scratch + w.seg_h);
+  k.ml_r = (long long)(k.units + k.n) * 128 * 2;
+  MergeSrc q{};
+  q.o = k.part_o; q.ml = k.part_ml; q.ml_r = k.ml_r; q.half = 256; q.seg = k.seg; q.rows = 128;
+  if (w.heads_pre) {
     q.flat = 1;
-  } else {
-    k.n = a.n; k.H = c.n_heads;
-    k.block_table = a.table; k.mbps = a.mbps; k.ctx = a.ctx; k.max_ctx = a.max_ctx;
-    k.allow_empty = m->min_ctx == 0;
-    k.units = w.units;
-    k.part_o = (float*)(scratch + w.o); k.part_ml = (float*)(scratch + w.ml); k.seg = (int2*)(scratch + w.seg);
+    m->src[m->n_src++] = q;
   }
-  k.ml_r = (long long)(k.units + k.n) * k.H * 2;
-  q.o = k.part_o; q.ml = k.part_ml; q.ml_r = k.ml_r; q.half = 256; q.seg = k.seg; q.rows = k.H;
-  if (!h->cache8) launch_heads<true, false>(mc, ml, k, s);
-  else if (pre) launch_heads<true, true>(mc, ml, k, s);
-  else launch_heads<false, true>(mc, ml, k, s);
+  if (w.heads_own) {
+    q.flat = 0;
+    q.e0 = k.n_pre;
+    m->src[m->n_src++] = q;
+  }
+  const char* timer = w.heads_pre ? "attn_prefix" : "attn";
+  if (h->cache8) launch_heads<true>(mc, ml, k, timer, s);
+  else launch_heads<false>(mc, ml, k, timer, s);
   return MLA_OK;
 }
 
@@ -453,19 +490,25 @@ static inline int latent_core(const mla_handle* h, const LatentCall& call, void*
     m.ctx = a.ctx; m.min_ctx = a.prefix_len > 0 ? 0 : 1; m.max_ctx = a.max_ctx;
     m.cap = (long long)a.mbps * c.block_size;
     int st = MLA_OK;
-    if (w.pre == PRE_FEW8) st = pass_few8(h, w, a, true, &m, scratch, flag, s);
-    else if (w.pre != PRE_NONE) st = pass_heads(h, w, a, true, &m, scratch, flag, s);
+    if (w.heads_pre || w.heads_own) st = pass_heads(h, w, a, &m, scratch, flag, s);
+    if (st == MLA_OK && w.few_pre) st = pass_few8(h, w, a, true, &m, scratch, flag, s);
+    if (st == MLA_OK && w.few_own) st = pass_few8(h, w, a, false, &m, scratch, flag, s);
+    if (st == MLA_OK && w.own16) st = pass_own16(h, w, a, &m, scratch, flag, s);
+    if (st == MLA_OK && w.simt) st = pass_simt(h, w, a, &m, scratch, flag, s);
     if (st != MLA_OK) return st;
-    if (w.own == OWN_FEW8) st = pass_few8(h, w, a, false, &m, scratch, flag, s);
-    else if (w.own == OWN_HEADS8) st = pass_heads(h, w, a, false, &m, scratch, flag, s);
-    else if (w.own == OWN_TC16) st = pass_own16(h, w, a, &m, scratch, flag, s);
-    else st = pass_simt(h, w, a, &m, scratch, flag, s);
-    if (st != MLA_OK) return st;
-    // split partials of one query row, about
-    const long long own = w.splits ? w.splits : cdiv(w.units, a.n) + 1, pre = w.pre ? cdiv(w.units_p, w.ents_p) + 1 : 0;
+    // split partials of one query row, about: each part's slices per entry, at most one per tile
+    auto parts = [](long long slices, long long ents, long long tiles) {
+      const long long k = cdiv(slices, ents > 0 ? ents : 1) + 1;
+      return k < tiles ? k : tiles;
+    };
     const long long t_own = cdiv(a.max_ctx, 64), t_pre = cdiv(a.prefix_len, 64);
-    const int most = (int)((own < t_own ? own : t_own) + (pre < t_pre ? pre : t_pre));
-    launch_merge(m, a.n, most, o_dt, s);
+    const long long ents_h = w.pre_h + (w.heads_own ? a.n : 0);
+    long long most = w.splits;
+    if (w.few_own) most += parts(w.units, a.n, t_own);
+    if (w.few_pre) most += parts(w.units_p, w.ents_p, t_pre);
+    if (w.heads_own) most += parts(w.units_h, ents_h, t_own);
+    if (w.heads_pre) most += parts(w.units_h, w.heads_own && t_pre > 4 * t_own ? w.pre_h : ents_h, t_pre);
+    launch_merge(m, a.n, (int)most, o_dt, s);
   }
   return MLA_OK;
 }

@@ -624,7 +624,8 @@ static int cache_rows(mla_handle* h, const void* rows, int n, const void* kv_cac
   p.c = cache8_of(h);
   p.rows = const_cast<void*>(rows); p.cache = (uint8_t*)const_cast<void*>(kv_cache); p.slots = slots;
   p.n = n; p.n_rows = (long long)n_blocks * c->block_size; p.layout = c->row_layout; p.flag = (int*)ws;
-  const long long want = cdiv(n, 8), most = 8LL * (h->tc.num_sms > 0 ? h->tc.num_sms : 148);   // 8 CTAs of 256 per SM
+  // warps of four rows, eight to a CTA; as many CTAs as fit the SMs at a time, or enough for every row
+  const long long want = cdiv(n, 8 * CR_ROWS), most = 8LL * (h->tc.num_sms > 0 ? h->tc.num_sms : 148);
   const unsigned grid = (unsigned)(want < most ? want : most);
   cudaStream_t s = (cudaStream_t)stream;
   if (c->act_dtype == MLA_F32) {

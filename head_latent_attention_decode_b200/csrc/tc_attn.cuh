@@ -36,16 +36,32 @@
 // so a P.V never waits behind the issue of a later S), and warps 10-13 send
 // each tile's partial scores to the peer as soon as S lands.
 //
-// FLAT: the entries of the schedule are not sequences but blocks of 128 query
-// rows of any sequences, all against one block table (a shared prefix).
+// FLAT: the schedule begins with n_pre entries that are not sequences but blocks
+// of 128 query rows of any sequences, all against one block table (a shared
+// prefix); the sequences' own rows follow in the same list, so that one launch
+// with one start-up and one tail takes both. The partials are packed.
 // C8: the cache is 8-bit (cache8.cuh). TMA brings the CTA's 256 codes of each
-// row (16 KB a tile, two raw buffers) and the row scales; the sender warps, idle
-// for most of a tile, turn them into the bf16 latent stage (scale * code is
-// exact there), two tiles ahead and after each tile's send, so that everything
-// behind the stage is the 16-bit kernel. The latent ring is three deep then, in
-// the same shared memory. (Feeding the codes to kind::f8f6f4 MMAs instead would
-// take as many MMAs, the query and the weights being split in two there, and
-// put their splitting into the softmax, which bounds this kernel.)
+// row (16 KB a tile, two raw buffers) and the row scales 2^k_j; four more warps
+// widen them to f16, one conversion for two codes, into the latent stage. Codes
+// and scales together do not fit f16's exponents, but a tile's rows relative to
+// its largest do: with kt the tile's largest k_j plus 9 the stage holds
+//   V'_j = 2^(k_j - kt) code_j, at most 1,
+// exact for rows down to 2^-6 of the largest and off by 2^-25 of it below (a row
+// under 2^-15 of its tile's largest is taken as zeros), and the rotary rows take
+// 2^-kt as well. Partial scores leave the MMA as S 2^-kt and are brought back to
+// real units as they are read; with the reference R of y = score log2(e) + kt the
+// weights 2^(y - R) bring V' back to the rows' own size in O, and the row sums take
+// them times 2^-kt: one number a tile, so the softmax is the 16-bit cache's. The
+// weights are f16 too: kept below 2^15, they hold their 11 bits down to 2^-29 of
+// the largest and are off by 2^-40 of it below. So is the query (one beyond 65504
+// ends as NaN, one below 2^-14 is off by 2^-25).
+// (Widening to bf16, scale and all, took three times the instructions, and scales
+// kept out of V' two products a weight in the softmax: 340 and 424 us for 64
+// sequences of 1024 to 16384 rows and 128 heads where this form took 331, before
+// the code was made smaller, which took it to 262: see mbar_poll_long. Feeding the
+// codes to kind::f8f6f4 MMAs would take as many MMAs, query and weights being split
+// in two there, and put their splitting into the softmax, which bounds this kernel.)
+// The latent ring is three deep, in the same shared memory.
 #pragma once
 
 #include "cache8.cuh"
@@ -76,12 +92,14 @@ struct TcAttnArgs {
   int units, min_per;
   int* nseg;
   int allow_empty;   // a context length of 0 is valid (the sequence has keys elsewhere)
-  // FLAT: entry b is the 128 query rows 128 b .. of rows_total, all against the
-  // same fixed_len rows of one block table; H is 128 and the partials are units
-  // c + b of [units + n] with seg[b] = {first cluster, clusters}. C8: the partials
-  // lie so too, with H rows per unit
+  // FLAT: n entries, of which entry b < n_pre is the 128 query rows 128 b .. of
+  // rows_total against the fixed_len rows of `pre_table`, and entry n_pre + t is
+  // sequence t. Cluster c's partial of entry b is unit c + b of [units + n] units of
+  // 128 query rows; seg[b] = {first cluster, clusters}
+  int n_pre;
   long long rows_total;
   int fixed_len;
+  const int* pre_table;
   int2* seg;
   // C8: the cache, its blocks' size and where their scales begin
   const uint8_t* c8;
@@ -90,6 +108,7 @@ struct TcAttnArgs {
 
 constexpr int ATT_NRP = 3;                      // rotary slots (the tiles of this CTA's parity)
 constexpr int ATT_THREADS = 480;                // 8 softmax, 1 TMA, 1 S-MMA, 4 sender, 1 P.V-MMA warps
+constexpr int ATT_THREADS8 = 608;               // C8: and 4 that widen the codes
 constexpr int ATT_MAX_SEQ = 256;                // sequences per call (the prefix table in shared memory)
 template <bool C8>
 struct AttnSmemT {
@@ -104,7 +123,7 @@ struct AttnSmemT {
   static constexpr int RED_OFF = STG_OFF + 16384; // [2 tiles][2 halves][128] fp32 half-row maxima, then [128] l
   static constexpr int PREF_OFF = RED_OFF + 2 * 2 * 128 * 4 + 128 * 4;   // [ATT_MAX_SEQ + 1] tile prefix sums
   static constexpr int SC_OFF = PREF_OFF + (ATT_MAX_SEQ + 4) * 4;        // C8: row scales [2][64]
-  static constexpr int BAR_OFF = SC_OFF + (C8 ? 512 : 0);
+  static constexpr int BAR_OFF = SC_OFF + (C8 ? 512 + 16 : 0);
   static constexpr int SIZE = 1024 + BAR_OFF + 512;
   static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
   static_assert(SC_OFF % 16 == 0, "bulk copies");
@@ -113,33 +132,77 @@ using AttnSmem = AttnSmemT<false>;
 // TMEM columns: Q latent [0,128) (bf16 pairs), S buffers [128,192) [192,256), O [256,512)
 constexpr uint32_t ATT_TM_Q = 0, ATT_TM_S = 128, ATT_TM_O = 256;
 
+// FLAT: an entry counts as this many tiles more than it has when the list is cut, about what a
+// segment's start and end cost (query in, O out), or a cluster with many short sequences finishes last
+// (32 sequences of up to 1024 rows behind a prefix of 16384, 128 heads: 308 us at 2, 260 at 4, 217 at 7,
+// 219 at 11; 64 sequences of up to 512 rows behind 8192, 16 heads: 67, 64, 68, 74).
+constexpr int ATT_PAD = 6;
+
 // Walks a cluster's slice of the batch's tile list: sequence b, its tile lt.
-struct TileWalk {
-  const int* pref;   // pref[b] = tiles of sequences 0..b-1 (shared memory)
+template <int PAD>
+struct TileWalkT {
+  const int* pref;   // pref[b] = tiles of sequences 0..b-1, each padded by PAD (shared memory)
   int n, b, lt;
-  __device__ void start(int g) {
-    b = 0;
-    while (b < n && pref[b + 1] <= g) ++b;
-    lt = g - pref[b];
-  }
-  __device__ bool seg_last() const { return pref[b] + lt + 1 == pref[b + 1]; }
-  __device__ void next() {
-    if (seg_last()) {
-      ++b;
-      while (b < n && pref[b + 1] == pref[b]) ++b;
-      lt = 0;
-    } else {
-      ++lt;
+  __device__ int tiles() const { return pref[b + 1] - pref[b] - PAD; }
+  // the last entry that begins at or before list position g
+  __device__ int find(int g) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pref[mid] <= g) lo = mid;
+      else hi = mid - 1;
     }
+    return lo;
+  }
+  __device__ void start(int g) {
+    b = find(g);
+    lt = g - pref[b];
+    if (PAD > 0 && lt >= tiles()) enter(b + 1);
+  }
+  __device__ void enter(int e) {
+    b = e;
+    lt = 0;
+    while (b < n && tiles() == 0) ++b;
+  }
+  __device__ bool seg_last() const { return lt + 1 == tiles(); }
+  __device__ void next() {
+    if (seg_last()) enter(b + 1);
+    else ++lt;
+  }
+  // real tiles before list position g
+  __device__ int before(int g) const {
+    if (PAD == 0) return g;
+    if (g >= pref[n]) return pref[n] - PAD * n;
+    const int e = find(g);
+    return pref[e] - PAD * e + min(g - pref[e], pref[e + 1] - pref[e] - PAD);
   }
 };
 
-// Context length of sequence b as the schedule counts it (0 when invalid).
+// Context length of entry b as the schedule counts it (0 when invalid).
 template <bool FLAT = false>
 __device__ __forceinline__ int attn_seq_len(const TcAttnArgs& a, int b) {
-  if (FLAT) return a.fixed_len;
+  if (FLAT) {
+    if (b < a.n_pre) return a.fixed_len;
+    const int L = a.ctx[b - a.n_pre];
+    return (L < 1 || L > a.max_ctx || (long long)L > (long long)a.mbps * a.bs) ? 0 : L;
+  }
   const int L = a.ctx[b];
   return (L < 1 || L > a.max_ctx || L > a.mbps * a.bs) ? 0 : L;
+}
+// Its row of block ids.
+template <bool FLAT>
+__device__ __forceinline__ const int* attn_table(const TcAttnArgs& a, int b) {
+  if (!FLAT) return a.block_table + (long long)b * a.mbps;
+  return b < a.n_pre ? a.pre_table : a.block_table + (long long)(b - a.n_pre) * a.mbps;
+}
+// Its first query row, and how many it has (at most 128).
+template <bool FLAT>
+__device__ __forceinline__ long long attn_row0(const TcAttnArgs& a, int b) {
+  return FLAT && b < a.n_pre ? b * 128LL : (long long)(FLAT ? b - a.n_pre : b) * a.H;
+}
+template <bool FLAT>
+__device__ __forceinline__ int attn_rows(const TcAttnArgs& a, int b) {
+  return FLAT && b < a.n_pre ? (int)min(128LL, a.rows_total - b * 128LL) : a.H;
 }
 
 // The balanced schedule of a persistent attention kernel: the prefix sum of
@@ -148,7 +211,7 @@ __device__ __forceinline__ int attn_seq_len(const TcAttnArgs& a, int b) {
 // flattened tile list that cluster c takes (slices of `per` tiles, at least
 // a.min_per). Block 0 of the grid writes each sequence's segment count to
 // a.nseg. Every thread of the CTA calls it; it ends with a __syncthreads.
-template <bool FLAT = false, bool C8 = false>
+template <bool FLAT = false>
 __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows, int* pref, int c, uint32_t r,
                                               int warp, int lane, int* per_out, int* g0_out, int* g1_out) {
   if (warp == 0) {
@@ -159,8 +222,8 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
       int T = 0;
       if (b < a.n) {
         const int L = attn_seq_len<FLAT>(a, b);
-        if (L == 0 && c == 0 && r == 0 && !(a.allow_empty && a.ctx[b] == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
-        T = (L + tile_rows - 1) / tile_rows;
+        if (L == 0 && c == 0 && r == 0 && !(a.allow_empty && a.ctx[FLAT ? b - a.n_pre : b] == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
+        T = (L + tile_rows - 1) / tile_rows + (FLAT ? ATT_PAD : 0);
       }
       cnt[k] = T;
       sum += T;
@@ -186,8 +249,8 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   if (per < a.min_per) per = a.min_per;
   if (blockIdx.x == 0) {   // segments of each sequence, for the merge
     for (int b = threadIdx.x; b < a.n; b += blockDim.x) {
-      const int T = pref[b + 1] - pref[b];
-      if (FLAT || C8) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
+      const int T = pref[b + 1] - pref[b] - (FLAT ? ATT_PAD : 0);
+      if (FLAT) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
       else a.nseg[b] = T > 0 ? (pref[b] + T - 1) / per - pref[b] / per + 1 : 0;
     }
   }
@@ -196,8 +259,43 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   *g1_out = min(total, c * per + per);
 }
 
+// Two bf16 in f16 (infinite beyond 65504, off by 2^-25 below 2^-14).
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  const __half2 v = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The MMA warps' steps, by one lane or (W) by the whole warp with one lane elected (mma_bf16_w). With the
+// 15 warps of the 16-bit kernel one lane does better (V3 decode step 0.385 against 0.401 ms: the other
+// lanes' polling costs more than the operands' moves), with the 19 of the 8-bit one the whole warp (324
+// against 339 us for 128 x 16 query rows over 32767 rows).
+template <bool W>
+__device__ __forceinline__ bool issue_wait(uint32_t bar, uint32_t parity, volatile int* abort_word, int* flag) {
+  return W ? mbar_poll_warp(bar, parity, abort_word, flag) : mbar_wait(bar, parity, abort_word, flag);
+}
+template <bool W>
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (W) mma_bf16_ts_w(d, a, b, idesc, acc);
+  else mma_bf16_ts(d, a, b, idesc, acc);
+}
+template <bool W>
+__device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (W) mma_bf16_w(d, a, b, idesc, acc);
+  else mma_bf16(d, a, b, idesc, acc);
+}
+template <bool W>
+__device__ __forceinline__ void issue_commit(uint32_t bar) {
+  if (W) mma_commit_w(bar);
+  else mma_commit(bar);
+}
+template <bool W>
+__device__ __forceinline__ void issue_commit_mask(uint32_t bar, uint16_t mask) {
+  if (W) mma_commit_cta_mask_w(bar, mask);
+  else mma_commit_cta_mask(bar, mask);
+}
+
 template <bool FLAT, bool C8 = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : ATT_THREADS, 1)
     tc_attn_decode_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_lat,
                           TcAttnArgs a) {
   using SM = AttnSmemT<C8>;
@@ -230,7 +328,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
   const uint32_t rope_full = rope_empty + 8 * ATT_NRP;   // C8: [ATT_NRP] rotary block landed
   const uint32_t raw_full = rope_full + 8 * ATT_NRP;     // C8: [2] codes and scales landed
   const uint32_t raw_empty = raw_full + 16;              // C8: [2] codes converted
-  volatile int* raw_rows = (volatile int*)(smem + SM::BAR_OFF + 456);   // C8: [2] rows that count
+  // of the tile in each stage: rows that count + 128 for a segment's last, its entry; C8: kt too, and
+  // the first two also of the tile in each raw buffer
+  int2* tile_of = (int2*)(smem + SM::BAR_OFF + 464);
+  int* tile_kt = (int*)(smem + SM::BAR_OFF + 496);
+  int2* raw_of = (int2*)(smem + SM::SC_OFF + 512);
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 448);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 452);
 
@@ -240,10 +342,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
 
   // ---- the schedule: tile prefix over the batch, then this cluster's slice ----
   int per, g0, g1;
-  attn_schedule<FLAT, C8>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
+  attn_schedule<FLAT>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
+  using TileWalk = TileWalkT<FLAT ? ATT_PAD : 0>;
   if (g0 >= g1) return;   // both CTAs of the cluster take this branch together
-  const int N = g1 - g0;
-  const long long tab = FLAT ? 0 : a.mbps;   // block-table row of sequence b: b * tab
+  const TileWalk wl{pref, a.n, 0, 0};
+  const int N = wl.before(g1) - wl.before(g0);
+  if (N <= 0) return;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ATT_NST; ++i) { mbar_init(full_b + 8 * i, C8 ? 4 : 1); mbar_init(empty_b + 8 * i, 1); }
@@ -251,7 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       for (int i = 0; i < ATT_NRP; ++i) mbar_init(rope_full + 8 * i, 1);
       for (int i = 0; i < 2; ++i) { mbar_init(raw_full + 8 * i, 1); mbar_init(raw_empty + 8 * i, 4); }
     }
-    for (int i = 0; i < 2; ++i) { mbar_init(s_full + 8 * i, 1); mbar_init(s_free + 8 * i, 12); }
+    // C8: the issuing thread arrives too: it has seen the converters' arrivals, and with them kt
+    for (int i = 0; i < 2; ++i) { mbar_init(s_full + 8 * i, C8 ? 2 : 1); mbar_init(s_free + 8 * i, 12); }
     for (int i = 0; i < ATT_NRP; ++i) mbar_init(rope_empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(p_full_b + 8 * i, 8);
@@ -285,27 +390,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     TileWalk w{pref, a.n, 0, 0};
     w.start(g0);
     int i = 0, blkv = 0;
+    int2 ofv = make_int2(0, 0);
     for (; i < N; ++i, w.next()) {
       if ((i & 31) == 0) {   // the block ids of the next 32 tiles, loaded in parallel
         TileWalk wk = w;
         for (int k = 0; k < lane && i + k + 1 < N; ++k) wk.next();
-        blkv = (i + lane < N) ? a.block_table[wk.b * tab + (64 * wk.lt) / a.bs] : 0;
+        if (i + lane < N) {
+          blkv = attn_table<FLAT>(a, wk.b)[(64 * wk.lt) / a.bs];
+          const bool good = blkv >= 0 && blkv < a.n_blocks;
+          ofv.x = (good ? min(64, attn_seq_len<FLAT>(a, wk.b) - 64 * wk.lt) : 0) + (i + lane == N - 1 || wk.seg_last() ? 128 : 0);
+          ofv.y = wk.b;
+        }
       }
       const int blk = __shfl_sync(0xffffffffu, blkv, i & 31);
+      const int2 of = make_int2(__shfl_sync(0xffffffffu, ofv.x, i & 31), __shfl_sync(0xffffffffu, ofv.y, i & 31));
+      if (FLAT && w.lt == 0 && i > 0) {   // another entry: its query into L2 ahead of the softmax warps
+        const long long q0 = attn_row0<FLAT>(a, w.b);
+        for (int x = lane; x < attn_rows<FLAT>(a, w.b); x += 32) {
+          const char* qa = (const char*)(a.q_abs + (q0 + x) * 512 + 256 * r);
+          for (int k = 0; k < 4; ++k) prefetch_l2(qa + 128 * k);
+          prefetch_l2(a.q_pe + (q0 + x) * 64);
+        }
+      }
       const int st = i % ATT_NST;
       const bool rope = (i & 1) == (int)r;
       const int ri = (i >> 1) % ATT_NRP;
-      if (C8 ? !mbar_wait_warp(raw_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)
-             : !mbar_wait_warp(empty_b + 8 * st, ((i / ATT_NST) & 1) ^ 1, abort_word, a.flag))
+      if (C8 ? !mbar_poll_warp(raw_empty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)
+             : !mbar_poll_warp(empty_b + 8 * st, ((i / ATT_NST) & 1) ^ 1, abort_word, a.flag))
         break;
-      if (rope && !mbar_wait_warp(rope_empty + 8 * ri, (((i >> 1) / ATT_NRP) & 1) ^ 1, abort_word, a.flag)) break;
+      if (rope && !mbar_poll_warp(rope_empty + 8 * ri, (((i >> 1) / ATT_NRP) & 1) ^ 1, abort_word, a.flag)) break;
       if (C8) {
         if (lane == 0) {
           const int j0 = 64 * w.lt, off = j0 % a.bs, rb = i & 1;
           const bool good = blk >= 0 && blk < a.n_blocks;
           if (!good && r == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
           const int cur = good ? blk : max(a.n_blocks, 1);   // a block beyond the map: the load fills zeros
-          raw_rows[rb] = good ? min(64, attn_seq_len<FLAT>(a, w.b) - j0) : 0;
+          raw_of[rb] = of;
           mbar_arrive_expect_tx(raw_full + 8 * rb, 16384 + (good ? 256 : 0));
           tma_load_5d(sbase + SM::RAW_OFF + rb * 16384, &tm_lat, raw_full + 8 * rb, 0, 0, 2 * (int)r, good ? off / 8 : 0, cur);
           if (good) bulk_load(sbase + SM::SC_OFF + rb * 256, a.c8 + cur * a.c8_block + a.c8_scales + off * 4, 256, raw_full + 8 * rb);
@@ -321,6 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
         long long row = -64;
         if (blk >= 0 && blk < a.n_blocks) row = (long long)blk * a.bs + (j0 % a.bs);
         else if (r == 0) set_flag(a.flag, MLA_FLAG_BAD_BLOCK);
+        tile_of[st] = of;
         mbar_arrive_expect_tx(full_b + 8 * st, rope ? 5 * 8192 : 4 * 8192);
         const uint32_t dst = tile_s + st * SM::STAGE;
         // the 4 latent k-blocks of the 64 rows in one box: [8 row octets][4 k-blocks][8 rows][128 B]
@@ -351,8 +472,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     }
   } else if (warp == 9) {
     // ---------------- S issuer: S(t) into buffer t & 1 once its tile has landed ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(128, 64);
+    if (C8 || lane == 0) {   // C8: the whole warp runs the loop
+      constexpr uint32_t idesc_s = C8 ? idesc_f16(128, 64) : idesc_bf16(128, 64), idesc_pe = idesc_bf16(128, 64);
       // descriptors built once; stages and k-steps add their byte offset >> 4
       const uint64_t d_t = sdesc_sw128_sbo(tile_s, 4096), d_rope = sdesc_sw128(sbase + SM::ROPE_OFF);
       const uint64_t d_qpe = sdesc_sw128(sbase + SM::QPE_OFF);
@@ -362,9 +483,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       for (int t = 0; t < N; ++t, ws.next()) {
         const int st = t % ATT_NST;
         const bool first = (t == 0 || ws.lt == 0), last = (t == N - 1 || ws.seg_last());
-        if (!mbar_wait(full_b + 8 * st, (t / ATT_NST) & 1, abort_word, a.flag) ||
-            !mbar_wait(s_free + 8 * (t & 1), ((t >> 1) & 1) ^ 1, abort_word, a.flag) ||
-            (first && !mbar_wait(q_ready, ks & 1, abort_word, a.flag)))
+        if (!issue_wait<C8>(full_b + 8 * st, (t / ATT_NST) & 1, abort_word, a.flag) ||
+            !issue_wait<C8>(s_free + 8 * (t & 1), ((t >> 1) & 1) ^ 1, abort_word, a.flag) ||
+            (first && !issue_wait<C8>(q_ready, ks & 1, abort_word, a.flag)))
           break;
         tc_fence_after();
         const uint64_t dt = d_t + (uint64_t)(st * (SM::STAGE / 16));
@@ -373,29 +494,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16_ts(d, tmem + ATT_TM_Q + 32 * j + 8 * k, dt + (j * 1024 + 32 * k) / 16, idesc_s,
+            issue_ts<C8>(d, tmem + ATT_TM_Q + 32 * j + 8 * k, dt + (j * 1024 + 32 * k) / 16, idesc_s,
                         (j > 0 || k > 0) ? 1u : 0u);
         if ((t & 1) == (int)r) {
           const int ri = (t >> 1) % ATT_NRP;
-          if (C8 && !mbar_wait(rope_full + 8 * ri, ((t >> 1) / ATT_NRP) & 1, abort_word, a.flag)) break;
-          if (C8) tc_fence_after();
           const uint64_t dr = d_rope + (uint64_t)(ri * (8192 / 16));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_bf16(d, d_qpe + 2 * k, dr + 2 * k, idesc_s, 1u);
-          mma_commit(rope_empty + 8 * ri);
+          for (int k = 0; k < 4; ++k) issue_ss<C8>(d, d_qpe + 2 * k, dr + 2 * k, idesc_pe, 1u);
+          issue_commit<C8>(rope_empty + 8 * ri);
         }
-        mma_commit(s_full + 8 * (t & 1));
+        issue_commit<C8>(s_full + 8 * (t & 1));
+        if (C8 && lane == 0) mbar_arrive(s_full + 8 * (t & 1));
         if (last) ++ks;
       }
-      mma_commit(fin);
+      issue_commit<C8>(fin);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(fin, 0))
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
     }
   } else if (warp == 14) {
     // ---------------- P.V issuer: O += P(u) . V(u) as soon as P(u) is written ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_o = idesc_bf16(128, 256, 1);
+    if (C8 || lane == 0) {
+      constexpr uint32_t idesc_o = C8 ? idesc_f16(128, 256, 1) : idesc_bf16(128, 256, 1);
       const uint64_t d_v = sdesc_sw128_mn_sbo(tile_s, 1024, 4096), d_p = sdesc_sw128(x_s);
       TileWalk wo{pref, a.n, 0, 0};
       wo.start(g0);
@@ -403,24 +523,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       for (int u = 0; u < N; ++u, wo.next()) {
         const int st = u % ATT_NST, xb = u & 1;
         const bool first = (u == 0 || wo.lt == 0), last = (u == N - 1 || wo.seg_last());
-        if (!mbar_wait(p_full_b + 8 * xb, (u >> 1) & 1, abort_word, a.flag) ||
-            (first && ko > 0 && !mbar_wait(o_free, (ko - 1) & 1, abort_word, a.flag)))
+        if (!issue_wait<C8>(p_full_b + 8 * xb, (u >> 1) & 1, abort_word, a.flag) ||
+            (first && ko > 0 && !issue_wait<C8>(o_free, (ko - 1) & 1, abort_word, a.flag)))
           break;
         tc_fence_after();
         const uint64_t dv = d_v + (uint64_t)(st * (SM::STAGE / 16));
         const uint64_t dp = d_p + (uint64_t)(xb * (16384 / 16));
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_bf16(tmem + ATT_TM_O, dp + 2 * k, dv + 8192 * k / 16, idesc_o, (!first || k > 0) ? 1u : 0u);
-        mma_commit(o_done);
-        mma_commit(empty_b + 8 * st);
-        mma_commit_cta_mask(x_free_b + 8 * xb, (uint16_t)(1u << peer));   // our buffer xb is the peer's to fill
-        if (last) { mma_commit(o_seg); ++ko; }
+          issue_ss<C8>(tmem + ATT_TM_O, dp + 2 * k, dv + 8192 * k / 16, idesc_o, (!first || k > 0) ? 1u : 0u);
+        issue_commit<C8>(o_done);
+        issue_commit<C8>(empty_b + 8 * st);
+        issue_commit_mask<C8>(x_free_b + 8 * xb, (uint16_t)(1u << peer));   // our buffer xb is the peer's to fill
+        if (last) { issue_commit<C8>(o_seg); ++ko; }
       }
-      mma_commit(fin);
+      issue_commit<C8>(fin);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(fin, 0))
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
+    }
+  } else if (C8 && warp > 14) {   // warps 15-18
+    // ---------------- C8: tile t's codes -> its f16 stage. This warp takes chunks [4 (cw & 1), +4) of
+    // 16 codes of k-block cw >> 1 of every row: lane = row of an octet + 8 x chunk, so that the 128-byte
+    // swizzle spreads loads and stores over all banks. Rows that do not count become zeros.
+    const int cw = warp - 15, ro = lane & 7, cc = 4 * (cw & 1) + (lane >> 3);
+    const int o0 = ((2 * (cc & 3)) ^ ro) << 4, o1 = ((2 * (cc & 3) + 1) ^ ro) << 4;
+    for (int t = 0; t < N; ++t) {
+      const int rb = t & 1, st = t % ATT_NST;
+      if (!mbar_poll_warp(raw_full + 8 * rb, (t >> 1) & 1, abort_word, a.flag)) break;
+      const int2 of = raw_of[rb];
+      const int rows = of.x & 127;
+      const float* sc = reinterpret_cast<const float*>(smem + SM::SC_OFF + rb * 256);
+      // the exponents of rows lane and lane + 32 (none: far below every scale), kt, the rows' factors 2^(k - kt)
+      auto exponent = [&](int row) {
+        const float v = row < rows ? sc[row] : 0.f;
+        return v > 0.f ? (int)(__float_as_uint(v) >> 23) - 127 : -1000;
+      };
+      const int k0 = exponent(lane), k1 = exponent(lane + 32);
+      const int km = __reduce_max_sync(0xffffffffu, max(k0, k1)), kt = km > -1000 ? km + 9 : 0;
+      auto factor = [&](int k) -> uint32_t {
+        const int d = k - kt;
+        return d >= -14 ? (uint32_t)(d + 15) << 10 : (d >= -24 ? 1u << (d + 24) : 0u);
+      };
+      const uint32_t f01 = factor(k0) | factor(k1) << 16;
+      if (!mbar_poll_warp(empty_b + 8 * st, ((t / ATT_NST) & 1) ^ 1, abort_word, a.flag)) break;
+      if (cw == 0 && lane == 0) { tile_of[st] = of; tile_kt[st] = kt; }
+      const uint8_t* src = smem + SM::RAW_OFF + rb * 16384 + (cw >> 1) * 1024 + ro * 128 + ((cc ^ ro) << 4);
+      uint8_t* dst = smem + SM::TILE_OFF + st * SM::STAGE + (2 * (cw >> 1) + (cc >> 2)) * 1024 + ro * 128;
+#pragma unroll 2
+      for (int oct = 0; oct < 8; ++oct) {
+        uint4 cv = *reinterpret_cast<const uint4*>(src + oct * 2048);
+        if (8 * oct + ro >= rows) cv = make_uint4(0, 0, 0, 0);
+        const uint32_t fb = __byte_perm(__shfl_sync(0xffffffffu, f01, (8 * oct + ro) & 31), 0, oct < 4 ? 0x1010 : 0x3232);
+        const __half2 f = *reinterpret_cast<const __half2*>(&fb);
+        const uint32_t w[4] = {cv.x, cv.y, cv.z, cv.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t c2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c2) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
+          const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&c2), f);
+          o[k] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(dst + oct * 4096 + o0) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + oct * 4096 + o1) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      if ((t & 1) == (int)r) {   // the rotary block times 2^-kt, in place
+        const int ri = (t >> 1) % ATT_NRP;
+        if (!mbar_poll_warp(rope_full + 8 * ri, ((t >> 1) / ATT_NRP) & 1, abort_word, a.flag)) break;
+        const __nv_bfloat162 f = __float2bfloat162_rn(exp2_int(-kt));
+        uint4* pe = reinterpret_cast<uint4*>(smem + SM::ROPE_OFF + ri * 8192) + 128 * cw + lane;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint4 v = pe[32 * k];
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), f);
+            w[j] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          pe[32 * k] = v;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(full_b + 8 * st); mbar_arrive(raw_empty + 8 * rb); }
     }
   } else if (warp >= 10) {   // warps 10-13
     // ---------------- senders: S_r(i) -> staging -> per warp, one bulk copy of its 32 rows into the
@@ -431,67 +618,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     const uint32_t peer_x = mapa_shared(x_s, peer), peer_x_full = mapa_shared(x_full_b, peer);
     const uint32_t stg_s = sbase + SM::STG_OFF + 4096 * qs;   // this warp's rows, 4 KB
     uint4* stg_row = (uint4*)(smem + SM::STG_OFF + h * 128);
-    // C8: tile t's codes -> its bf16 stage. This warp takes chunks [4 (cw & 1), +4) of 16 codes of k-block
-    // cw >> 1 of every row: lane = row of an octet + 8 x chunk, so that the 128-byte swizzle spreads loads
-    // and stores over all banks. Rows that do not count become zeros.
-    auto convert = [&](int t) -> bool {
-      const int rb = t & 1, st = t % ATT_NST, cw = warp - 10;
-      if (!mbar_wait_warp(raw_full + 8 * rb, (t >> 1) & 1, abort_word, a.flag) ||
-          !mbar_wait_warp(empty_b + 8 * st, ((t / ATT_NST) & 1) ^ 1, abort_word, a.flag))
-        return false;
-      const int rows = raw_rows[rb], ro = lane & 7, cc = 4 * (cw & 1) + (lane >> 3);
-      const uint8_t* src = smem + SM::RAW_OFF + rb * 16384 + (cw >> 1) * 1024 + ro * 128 + ((cc ^ ro) << 4);
-      uint8_t* dst = smem + SM::TILE_OFF + st * SM::STAGE + (2 * (cw >> 1) + (cc >> 2)) * 1024 + ro * 128;
-      const int o0 = ((2 * (cc & 3)) ^ ro) << 4, o1 = ((2 * (cc & 3) + 1) ^ ro) << 4;
-      const float* sc = reinterpret_cast<const float*>(smem + SM::SC_OFF + rb * 256);
-#pragma unroll 4
-      for (int oct = 0; oct < 8; ++oct) {
-        const uint4 cv = *reinterpret_cast<const uint4*>(src + oct * 2048);
-        const bool live = 8 * oct + ro < rows;
-        const float s = sc[8 * oct + ro];
-        const uint32_t w[4] = {cv.x, cv.y, cv.z, cv.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 f = e4m3x2_f32((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
-          o[k] = live ? pack_bf16x2(f.x * s, f.y * s) : 0u;
-        }
-        *reinterpret_cast<uint4*>(dst + oct * 4096 + o0) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(dst + oct * 4096 + o1) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) { mbar_arrive(full_b + 8 * st); mbar_arrive(raw_empty + 8 * rb); }
-      return true;
-    };
-    bool live_s = true;
-    if (C8) live_s = convert(0) && (N < 2 || convert(1));
-    for (int i = 0; i < N && live_s; ++i) {
-      if (!mbar_wait_warp(s_full + 8 * (i & 1), (i >> 1) & 1, abort_word, a.flag)) break;
+    for (int i = 0; i < N; ++i) {
+      if (!mbar_poll_warp(s_full + 8 * (i & 1), (i >> 1) & 1, abort_word, a.flag)) break;
       tc_fence_after();
-      float v[64];
+      const float un = C8 ? exp2_int(tile_kt[i % ATT_NST]) : 1.f;
       const uint32_t sa = tmem + ATT_TM_S + 64 * (i & 1) + lane_base;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tmem_ld16(sa + 16 * k, (uint32_t*)&v[16 * k]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_free + 8 * (i & 1));
       if (lane == 0) bulk_wait_read_all();               // this warp's previous copy has left its rows
       __syncwarp();
       // the partial goes out in f16 (half the distributed-shared-memory bytes of fp32; the
       // partial scores stay far inside f16's range and its 11-bit significand costs the
       // scores ~1e-3 relative, well inside the output tolerance)
+#pragma unroll 1
+      for (int k0 = 0; k0 < 8; k0 += 2) {
+        float v[16];
+        tmem_ld16(sa + 8 * k0, (uint32_t*)v);
+        tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // chunk k (8 values) of row h at slot k ^ (h & 7): no bank conflicts
-        uint32_t w[4];
+        for (int k = 0; k < 2; ++k) {  // chunk k0 + k (8 values) of row h at slot (k0 + k) ^ (h & 7): no bank conflicts
+          uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          __half2 hv = __floats2half2_rn(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
-          w[j] = *reinterpret_cast<uint32_t*>(&hv);
+          for (int j = 0; j < 4; ++j) {
+            __half2 hv = C8 ? __floats2half2_rn(v[8 * k + 2 * j] * un, v[8 * k + 2 * j + 1] * un)
+                            : __floats2half2_rn(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
+            w[j] = *reinterpret_cast<uint32_t*>(&hv);
+          }
+          stg_row[(k0 + k) ^ (h & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        stg_row[k ^ (h & 7)] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free + 8 * (i & 1));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -501,10 +657,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           bulk_copy_to_peer(peer_x + xb * 16384 + 4096 * qs, stg_s, 4096, peer_x_full + 8 * (4 * xb + qs));
           bulk_commit_group();
         }
-      }
-      if (C8 && i + 2 < N) {
-        __syncwarp();
-        live_s = convert(i + 2);
       }
     }
     if (lane == 0) bulk_wait_read_all();
@@ -516,15 +668,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     // this half's share of sequence b's query: 128 latent values of CTA r's half
     // -> TMEM columns [64 g, 64 g + 64), 32 rotary values -> [128 + 16 g, 128 + 16 g + 16)
     auto load_q = [&](int b) {
-      const bool live = FLAT ? b * 128LL + h < a.rows_total : h < a.H;
-      const long long qh = (long long)b * a.H + (live ? h : 0);
+      const bool live = h < attn_rows<FLAT>(a, b);
+      const long long qh = attn_row0<FLAT>(a, b) + (live ? h : 0);
       const uint4* src = (const uint4*)(a.q_abs + qh * 512 + r * 256 + 128 * g);
 #pragma unroll
       for (int k4 = 0; k4 < 4; ++k4) {
         uint32_t qv[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint4 v = live ? src[4 * k4 + k] : make_uint4(0, 0, 0, 0);
+          uint4 v = live ? src[4 * k4 + k] : make_uint4(0, 0, 0, 0);
+          if (C8) v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
           qv[4 * k] = v.x; qv[4 * k + 1] = v.y; qv[4 * k + 2] = v.z; qv[4 * k + 3] = v.w;
         }
         tmem_st16(tmem + ATT_TM_Q + lane_base + 64 * g + 16 * k4, qv);
@@ -543,25 +696,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
     TileWalk w{pref, a.n, 0, 0};
     w.start(g0);
     load_q(w.b);
-    // block of tile i + 1, loaded one tile ahead (only its validity is needed here)
-    auto tile_block = [&](const TileWalk& t) { return a.block_table[t.b * tab + (64 * t.lt) / a.bs]; };
-    int blk_next = tile_block(w);
-    int seq_len = attn_seq_len<FLAT>(a, w.b);
+    constexpr float above = C8 ? 15.f : 8.f, below = C8 ? 7.f : 0.f;
     float m_ref = -INFINITY, l = 0.f;
     int tseg = 0, kseg = 0;   // tile within the segment, segments done
     bool ok = true;
-    for (int i = 0; i < N && ok; ++i, w.next()) {
-      const int b = w.b, lt = w.lt, st = i % ATT_NST, xb = i & 1;
-      const bool last = (i == N - 1 || w.seg_last());
-      const int blk = blk_next;
-      if (i + 1 < N) {
-        TileWalk wn = w;
-        wn.next();
-        blk_next = tile_block(wn);
-      }
-      const int valid = (blk >= 0 && blk < a.n_blocks) ? min(64, seq_len - 64 * lt) : 0;
+    for (int i = 0; i < N && ok; ++i) {
+      const int st = i % ATT_NST, xb = i & 1;
       if (g == 0 && lane == 0) mbar_arrive_expect_tx(x_full_b + 8 * (4 * xb + q), 4096);   // this quarter's rows
-      if (!mbar_wait_warp(s_full + 8 * xb, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      // the tile landed before its S: this only makes what came with it visible
+      if (!mbar_poll_warp(full_b + 8 * st, (i / ATT_NST) & 1, abort_word, a.flag)) { ok = false; break; }
+      const int2 of = tile_of[st];
+      const int valid = of.x & 127, b = of.y;
+      const bool last = of.x & 128;
+      const int kt = C8 ? tile_kt[st] : 0;
+      const float un = C8 ? exp2_int(kt) : 1.f;
+      if (!mbar_poll_warp(s_full + 8 * xb, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       tc_fence_after();
       float v[32];
       const uint32_t sp_addr = tmem + ATT_TM_S + 64 * xb + 32 * g + lane_base;
@@ -571,7 +720,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free + 8 * xb);   // S(i + 2) may overwrite the buffer
-      if (!mbar_wait_warp(x_full_b + 8 * (4 * xb + q), (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      if (!mbar_poll_warp(x_full_b + 8 * (4 * xb + q), (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       // row h, chunks 4 g .. 4 g + 3 of the peer's partial; P(i) later goes to exactly these bytes
       uint4* xrow = (uint4*)(smem + SM::X_OFF + xb * 16384 + h * 128);
 #pragma unroll
@@ -581,8 +730,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&wx[j]));
-          v[8 * k + 2 * j] += f.x;
-          v[8 * k + 2 * j + 1] += f.y;
+          const float2 s = make_float2(v[8 * k + 2 * j], v[8 * k + 2 * j + 1]);
+          const float2 s2 = C8 ? fma2(s, make_float2(un, un), f) : add2(s, f);
+          v[8 * k + 2 * j] = s2.x;
+          v[8 * k + 2 * j + 1] = s2.y;
         }
       }
       if (valid < 64) {
@@ -590,39 +741,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = (j < vc) ? v[j] : -INFINITY;   // also drops NaN past the context
       }
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float m4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
-      const float mloc = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      for (int j = 4; j < 28; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], v[j + k], v[j + 4 + k]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], v[28 + k]);
+      const float mloc = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
       // the two halves of head h meet: both then take the same decisions
       red[(xb * 2 + g) * 128 + h] = mloc;
       __syncwarp();
       if (lane == 0) mbar_arrive(xch_b + 8 * (2 * q + xb));
-      if (!mbar_wait_warp(xch_b + 8 * (2 * q + xb), (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
-      const float mt = fmaxf(mloc, red[(xb * 2 + (g ^ 1)) * 128 + h]) * a.scale_log2;
+      if (!mbar_poll_warp(xch_b + 8 * (2 * q + xb), (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
+      float mt = fmaxf(mloc, red[(xb * 2 + (g ^ 1)) * 128 + h]) * a.scale_log2;
+      if (C8) mt += (float)kt;
       // online softmax in log2 units with a lazily moved reference max
       float alpha = 1.f;
       bool rescale = false;
-      if (mt > m_ref + 8.f) {
-        if (m_ref != -INFINITY) { alpha = ex2_approx(m_ref - mt); rescale = true; }
-        m_ref = mt;
+      if (mt > m_ref + above) {
+        if (m_ref != -INFINITY) { alpha = ex2_approx(m_ref + below - mt); rescale = true; }
+        m_ref = mt - below;
       }
-      const float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
-      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+      float nm = (m_ref == -INFINITY) ? 0.f : -m_ref;
+      if (C8) nm += (float)kt;
+      const float2 sl2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(nm, nm);
+      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       uint32_t pk[16];
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
-        const float e0 = ex2_approx(fmaf(v[j], a.scale_log2, nm)), e1 = ex2_approx(fmaf(v[j + 1], a.scale_log2, nm));
-        __nv_bfloat162 pb = __floats2bfloat162_rn(e0, e1);
-        ps[(j >> 1) & 3] += e0 + e1;
-        pk[j >> 1] = *reinterpret_cast<uint32_t*>(&pb);
+        float2 e = fma2(make_float2(v[j], v[j + 1]), sl2, nm2);
+        e = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+        ps[(j >> 1) & 1] = add2(ps[(j >> 1) & 1], e);
+        if (C8) {
+          const __half2 pb = __floats2half2_rn(e.x, e.y);
+          pk[j >> 1] = *reinterpret_cast<const uint32_t*>(&pb);
+        } else {
+          const __nv_bfloat162 pb = __floats2bfloat162_rn(e.x, e.y);
+          pk[j >> 1] = *reinterpret_cast<const uint32_t*>(&pb);
+        }
       }
-      const float psum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      const float2 pt = add2(ps[0], ps[1]);
+      float psum = pt.x + pt.y;
+      if (C8) psum *= exp2_int(-kt);
       if (__any_sync(0xffffffffu, rescale) && tseg >= 1) {
         // P.V(i - 2) is complete (its release let the peer fill this X buffer), so
         // waiting for the phase of P.V(i - 1) cannot pass early; O must not be
         // touched before it completes
-        if (!mbar_wait_warp(o_done, (i - 1) & 1, abort_word, a.flag)) { ok = false; break; }
+        if (!mbar_poll_warp(o_done, (i - 1) & 1, abort_word, a.flag)) { ok = false; break; }
         tc_fence_after();
         for (int k = 0; k < 8; ++k) {
           uint32_t o[16];
@@ -659,18 +825,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
         // the segment's S MMAs are all complete (the softmax read each S): the next
         // segment's query may replace this one while the last P.V runs
         if (i + 1 < N) {
-          TileWalk wn = w;
-          wn.next();
+          TileWalk wn{pref, a.n, b, 0};
+          wn.enter(b + 1);
           load_q(wn.b);
-          seq_len = attn_seq_len<FLAT>(a, wn.b);
         }
         const int j = c - pref[b] / per;               // this segment's split slot in sequence b
-        const long long unit = FLAT || C8 ? (long long)c + b : (long long)b * a.splits + j;
-        const bool store = FLAT ? b * 128LL + h < a.rows_total : h < a.H;
+        const long long unit = FLAT ? (long long)c + b : (long long)b * a.splits + j;
+        const int rows_u = FLAT ? 128 : a.H;
+        const bool store = h < attn_rows<FLAT>(a, b);
         float* const ml = a.part_ml + r * a.ml_r;      // this CTA's (m, l) copy
-        if (!mbar_wait_warp(o_seg, kseg & 1, abort_word, a.flag)) { ok = false; break; }
+        if (!mbar_poll_warp(o_seg, kseg & 1, abort_word, a.flag)) { ok = false; break; }
         tc_fence_after();
-        float* po = a.part_o + (unit * a.H + h) * 512 + r * 256 + 128 * g;
+        float* po = a.part_o + (unit * rows_u + h) * 512 + r * 256 + 128 * g;
         for (int k = 0; k < 8; ++k) {
           uint32_t o[16];
           tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 16 * k, o);
@@ -691,10 +857,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(ATT_THREADS, 1)
           red_l[h] = l;
           __syncwarp();
           if (lane == 0) mbar_arrive(l_done + 8 * q);
-        } else if (mbar_wait_warp(l_done + 8 * q, kseg & 1, abort_word, a.flag)) {
+        } else if (mbar_poll_warp(l_done + 8 * q, kseg & 1, abort_word, a.flag)) {
           if (store) {
-            ml[(unit * a.H + h) * 2] = m_ref * 0.69314718055994531f;   // natural-log units
-            ml[(unit * a.H + h) * 2 + 1] = l + red_l[h];
+            ml[(unit * rows_u + h) * 2] = m_ref * 0.69314718055994531f;   // natural-log units
+            ml[(unit * rows_u + h) * 2 + 1] = l + red_l[h];
           }
         } else {
           ok = false;

@@ -6,9 +6,10 @@
 // The other operand of each product would lose accuracy in E4M3, so it is split
 // in two E4M3 parts, x = hi + lo with hi = e4m3(x) and lo = e4m3(x - hi): two 4-bit
 // significands carry the 8 bits of a bf16 value, and both parts ride in one MMA
-// as extra columns (N = 32 for 16 heads). An MMA of M 128 costs 49 cycles for any
-// N up to 64 (62 for 128, 121 for 256; K- or MN-major and 8- or 16-bit alike), so
-// the second part is free.
+// as extra columns (N = 32 for 16 heads). An MMA of M 128 takes as long as its
+// operands' way out of shared memory, 40 cycles for N 32 and 39 for N 16 (48 for
+// 64, 63 for 128; K- or MN-major and 8- or 16-bit alike), so the second part is
+// nearly free.
 //   q_abs_h = 2^k_h (hi + lo): k_h brings the row's largest to at most 448; columns
 //     within 2^-10 of it are exact, smaller ones off by at most 2^-18 of it
 //   p: relative to a per-head reference R that follows the tiles' maxima both up
@@ -52,38 +53,9 @@
 namespace mla {
 namespace tc {
 
-// D(tmem) (+)= A * B^T, E4M3 in, fp32 accumulation, K 32.
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // kind::f8f6f4: fp32 accumulator, A and B E4M3 (format 0).
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major = 0) {
   return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// mbar_wait without a look at the clock before the first polls fail: the softmax warps wait often
-// and briefly.
-__device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity, volatile int* abort_word, int* flag) {
-  bool ok = true;
-  uint64_t t0 = 0;
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if ((it & 63) == 0) {
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
-      if (*abort_word || t - t0 > WAIT_LIMIT_NS) {
-        if (!*abort_word) set_flag(flag, MLA_FLAG_WAIT_TIMEOUT);
-        *abort_word = 1;
-        ok = false;
-        break;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
 }
 
 struct TcAttn8Args {
@@ -354,64 +326,64 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
       while (global_timer_ns() - t0 < 1000000ull) {}
     }
   } else if (warp == 8 + 1) {
-    // ---------------- score MMAs ----------------
-    if (lane == 0) {
+    // ---------------- score MMAs (the whole warp runs the loop; see mma_f8_w) ----------------
+    {
       constexpr uint32_t id_u = idesc_e4m3(128, 32), id_r = idesc_bf16(128, 16);
       const uint64_t d_ring = sdesc_sw128_sbo(ring_s, 2048), d_rope = sdesc_sw128(rope_s);
       const uint64_t d_q = sdesc_sw128(q_s), d_qpe = sdesc_sw128(qpe_s);
       int ks = 0;
       for (int i = 0; i < N; ++i) {
         const int b = i & 1;
-        if (!mbar_wait(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag) ||
-            !mbar_wait(s_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag))
+        if (!mbar_poll_warp(rfull + 8 * b, (i >> 1) & 1, abort_word, a.flag) ||
+            !mbar_poll_warp(s_free + 8 * b, ((i >> 1) & 1) ^ 1, abort_word, a.flag))
           break;
         if (tile_s[b].z & TILE_FIRST) {
-          if (!mbar_wait(q_ready, ks & 1, abort_word, a.flag)) break;
+          if (!mbar_poll_warp(q_ready, ks & 1, abort_word, a.flag)) break;
           ++ks;
         }
         tc_fence_after();
         const uint32_t d = tmem + SM::TM_S + 64 * b;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_bf16(d + 32, d_rope + (b * 16384 + 32 * k) / 16, d_qpe + 2 * k, id_r, k > 0 ? 1u : 0u);
-        mma_commit(rempty + 8 * b);
+          mma_bf16_w(d + 32, d_rope + (b * 16384 + 32 * k) / 16, d_qpe + 2 * k, id_r, k > 0 ? 1u : 0u);
+        mma_commit_w(rempty + 8 * b);
         bool ok = true;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int e = 2 * i + g, slot = e % NPR;
-          if (!mbar_wait(full_b + 8 * slot, (e / NPR) & 1, abort_word, a.flag)) { ok = false; break; }
+          if (!mbar_poll_warp(full_b + 8 * slot, (e / NPR) & 1, abort_word, a.flag)) { ok = false; break; }
           tc_fence_after();
           const uint64_t da = d_ring + (uint64_t)(slot * (32768 / 16));
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8(d, da + (kk * 1024 + 32 * k) / 16, d_q + ((2 * g + kk) * SM::QB + 32 * k) / 16, id_u,
+              mma_f8_w(d, da + (kk * 1024 + 32 * k) / 16, d_q + ((2 * g + kk) * SM::QB + 32 * k) / 16, id_u,
                      (g > 0 || kk > 0 || k > 0) ? 1u : 0u);
         }
         if (!ok) break;
-        mma_commit(s_full + 8 * b);
-        mbar_arrive(s_full + 8 * b);
+        mma_commit_w(s_full + 8 * b);
+        if (lane == 0) mbar_arrive(s_full + 8 * b);
       }
-      mma_commit(fin_s);
+      mma_commit_w(fin_s);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(fin_s, 0))
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }
     }
   } else if (warp == 8 + 2) {
     // ---------------- value MMAs ----------------
-    if (lane == 0) {
+    {
       constexpr uint32_t id_o = idesc_e4m3(128, 32, 1);
       // codes^T: one 128-column group along M, 8-key octets 2048 B apart along K
       const uint64_t d_v = sdesc_sw128_mn_sbo(ring_s, 1024, 2048), d_p = sdesc_sw128(p_s);
       int ko[2] = {0, 0};   // entries whose O^T the set has begun
       for (int i = 0; i < N; ++i) {
         const int b = i & 1;
-        if (!mbar_wait(p_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) break;
+        if (!mbar_poll_warp(p_full + 8 * b, (i >> 1) & 1, abort_word, a.flag)) break;
         const bool fresh = pv_fresh[b] != 0;
         if (fresh) {
           const int k = b ? ko[1]++ : ko[0]++;
-          if (k > 0 && !mbar_wait(o_free + 8 * b, (k - 1) & 1, abort_word, a.flag)) break;
+          if (k > 0 && !mbar_poll_warp(o_free + 8 * b, (k - 1) & 1, abort_word, a.flag)) break;
         }
         tc_fence_after();
         const uint64_t dp = d_p + (uint64_t)(b * (SM::PB / 16));
@@ -423,13 +395,13 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f8(tmem + SM::TM_O + 128 * b + (2 * g + kk) * 32, dv + (kk * 1024 + 8192 * k) / 16, dp + 2 * k, id_o,
+              mma_f8_w(tmem + SM::TM_O + 128 * b + (2 * g + kk) * 32, dv + (kk * 1024 + 8192 * k) / 16, dp + 2 * k, id_o,
                      (!fresh || k > 0) ? 1u : 0u);
-          mma_commit(empty_b + 8 * slot);
+          mma_commit_w(empty_b + 8 * slot);
         }
-        mma_commit(p_free + 8 * b);
+        mma_commit_w(p_free + 8 * b);
       }
-      mma_commit(fin_o);
+      mma_commit_w(fin_o);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(fin_o, 0))
         if (global_timer_ns() - t0 > WAIT_LIMIT_NS) { set_flag(a.flag, MLA_FLAG_WAIT_TIMEOUT); break; }

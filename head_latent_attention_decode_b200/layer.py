@@ -59,7 +59,10 @@ class MlaLayer:
         del src
         if cache_dtype == "fp8":
             mla_set_cache_dtype(self.handle, MLA_FP8_E4M3_ROW)
+        self.block_bytes = mla_cache_block_bytes(self.handle)
+        self._cache_torch = torch.uint8 if cache_dtype == "fp8" else self.act
         self.ws = None
+        self._ws_for = None   # the sizes the workspace was last asked for
 
     def close(self) -> None:
         """Release the library handle (the weight blob is torch memory)."""
@@ -82,6 +85,9 @@ class MlaLayer:
 
     def prefix_workspace(self, max_tokens: int, max_prefix_len: int, max_context_len: int) -> torch.Tensor:
         """A workspace for latent_attn and decode_attn_prefix (and every other call)."""
+        sizes = (max_tokens, max_prefix_len, max_context_len)
+        if sizes == self._ws_for:
+            return self.ws
         need = mla_prefix_workspace_bytes(self.handle, max(1, max_tokens), max(0, max_prefix_len),
                                           max(1, max_context_len))
         if need == 0:
@@ -89,20 +95,20 @@ class MlaLayer:
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             mla_workspace_init(self.ws)
+        self._ws_for = sizes   # it only ever grows, so it stays large enough
         return self.ws
 
     def new_cache(self, n_blocks: int) -> torch.Tensor:
         """A zeroed paged cache: [n_blocks, 1, block_size, R], or [n_blocks, block bytes] uint8 if 8-bit."""
         if self.cache_dtype == "fp8":
-            return torch.zeros((n_blocks, mla_cache_block_bytes(self.handle)), dtype=torch.uint8, device=self.device)
+            return torch.zeros((n_blocks, self.block_bytes), dtype=torch.uint8, device=self.device)
         return torch.zeros((n_blocks, 1, self.shape.block_size, self.shape.kv_row_dim), dtype=self.act,
                            device=self.device)
 
     def _check_cache(self, kv_cache):
-        want = torch.uint8 if self.cache_dtype == "fp8" else self.act
-        if kv_cache.dtype != want or kv_cache[:1].numel() * kv_cache.element_size() != mla_cache_block_bytes(self.handle):
-            raise ValueError(f"kv_cache does not hold blocks of this layer's cache ({want}, "
-                             f"{mla_cache_block_bytes(self.handle)} bytes a block)")
+        if kv_cache.dtype is not self._cache_torch or kv_cache.nbytes != kv_cache.shape[0] * self.block_bytes:
+            raise ValueError(f"kv_cache does not hold blocks of this layer's cache ({self._cache_torch}, "
+                             f"{self.block_bytes} bytes a block)")
 
     def _check_rows(self, rows):
         if rows.dtype != self.act or rows.dim() != 2 or rows.shape[1] != self.shape.kv_row_dim:
