@@ -132,18 +132,23 @@ using AttnSmem = AttnSmemT<false>;
 // TMEM columns: Q latent [0,128) (bf16 pairs), S buffers [128,192) [192,256), O [256,512)
 constexpr uint32_t ATT_TM_Q = 0, ATT_TM_S = 128, ATT_TM_O = 256;
 
-// FLAT: an entry counts as this many tiles more than it has when the list is cut, about what a
-// segment's start and end cost (query in, O out), or a cluster with many short sequences finishes last
-// (32 sequences of up to 1024 rows behind a prefix of 16384, 128 heads: 308 us at 2, 260 at 4, 217 at 7,
-// 219 at 11; 64 sequences of up to 512 rows behind 8192, 16 heads: 67, 64, 68, 74).
-constexpr int ATT_PAD = 6;
+// FLAT: an entry of `rows` query rows counts as this many tiles more than it has when the list is cut,
+// about what a segment's start and end cost (query in, O out), or a cluster with many short sequences
+// finishes last (32 sequences of up to 1024 rows behind a prefix of 16384, 128 heads: 308 us at 2 for
+// every entry, 260 at 4, 217 at 7, 219 at 11; 16 heads, whose own rows start and end sooner, 64 of up to
+// 512 behind 8192: 67, 64, 68, 74 us, and 55 with 6 for a prefix block and 3 for them).
+__host__ __device__ constexpr int att_pad(int rows) { return 3 + 3 * rows / 128; }
 
 // Walks a cluster's slice of the batch's tile list: sequence b, its tile lt.
-template <int PAD>
+template <bool FLAT>
 struct TileWalkT {
-  const int* pref;   // pref[b] = tiles of sequences 0..b-1, each padded by PAD (shared memory)
-  int n, b, lt;
-  __device__ int tiles() const { return pref[b + 1] - pref[b] - PAD; }
+  const int* pref;   // pref[b] = tiles of entries 0..b-1, each with its padding (shared memory)
+  int n, n_pre, pad_own, b, lt;
+  __device__ int pad(int e) const { return !FLAT ? 0 : (e < n_pre ? att_pad(128) : pad_own); }
+  __device__ int pads(int e) const {   // of the entries before e
+    return !FLAT ? 0 : min(e, n_pre) * att_pad(128) + max(e - n_pre, 0) * pad_own;
+  }
+  __device__ int tiles() const { return pref[b + 1] - pref[b] - pad(b); }
   // the last entry that begins at or before list position g
   __device__ int find(int g) const {
     int lo = 0, hi = n - 1;
@@ -157,7 +162,7 @@ struct TileWalkT {
   __device__ void start(int g) {
     b = find(g);
     lt = g - pref[b];
-    if (PAD > 0 && lt >= tiles()) enter(b + 1);
+    if (FLAT && lt >= tiles()) enter(b + 1);
   }
   __device__ void enter(int e) {
     b = e;
@@ -171,10 +176,10 @@ struct TileWalkT {
   }
   // real tiles before list position g
   __device__ int before(int g) const {
-    if (PAD == 0) return g;
-    if (g >= pref[n]) return pref[n] - PAD * n;
+    if (!FLAT) return g;
+    if (g >= pref[n]) return pref[n] - pads(n);
     const int e = find(g);
-    return pref[e] - PAD * e + min(g - pref[e], pref[e + 1] - pref[e] - PAD);
+    return pref[e] - pads(e) + min(g - pref[e], pref[e + 1] - pref[e] - pad(e));
   }
 };
 
@@ -215,15 +220,17 @@ template <bool FLAT = false>
 __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows, int* pref, int c, uint32_t r,
                                               int warp, int lane, int* per_out, int* g0_out, int* g1_out) {
   if (warp == 0) {
-    int cnt[8], sum = 0;
+    int cnt[8], len[8], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) len[k] = 8 * lane + k < a.n ? attn_seq_len<FLAT>(a, 8 * lane + k) : 0;   // loads in flight
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int b = 8 * lane + k;
       int T = 0;
       if (b < a.n) {
-        const int L = attn_seq_len<FLAT>(a, b);
+        const int L = len[k];
         if (L == 0 && c == 0 && r == 0 && !(a.allow_empty && a.ctx[FLAT ? b - a.n_pre : b] == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
-        T = (L + tile_rows - 1) / tile_rows + (FLAT ? ATT_PAD : 0);
+        T = (L + tile_rows - 1) / tile_rows + (FLAT ? (b < a.n_pre ? att_pad(128) : att_pad(a.H)) : 0);
       }
       cnt[k] = T;
       sum += T;
@@ -249,7 +256,7 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
   if (per < a.min_per) per = a.min_per;
   if (blockIdx.x == 0) {   // segments of each sequence, for the merge
     for (int b = threadIdx.x; b < a.n; b += blockDim.x) {
-      const int T = pref[b + 1] - pref[b] - (FLAT ? ATT_PAD : 0);
+      const int T = pref[b + 1] - pref[b] - (FLAT ? (b < a.n_pre ? att_pad(128) : att_pad(a.H)) : 0);
       if (FLAT) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
       else a.nseg[b] = T > 0 ? (pref[b] + T - 1) / per - pref[b] / per + 1 : 0;
     }
@@ -300,7 +307,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
                           TcAttnArgs a) {
   using SM = AttnSmemT<C8>;
   constexpr int ATT_NST = SM::NST;
-  griddep_wait();   // the inputs all come from the stream's earlier kernels
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -340,15 +346,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
   const int c = blockIdx.x >> 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- the schedule: tile prefix over the batch, then this cluster's slice ----
-  int per, g0, g1;
-  attn_schedule<FLAT>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
-  using TileWalk = TileWalkT<FLAT ? ATT_PAD : 0>;
-  if (g0 >= g1) return;   // both CTAs of the cluster take this branch together
-  const TileWalk wl{pref, a.n, 0, 0};
-  const int N = wl.before(g1) - wl.before(g0);
-  if (N <= 0) return;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < ATT_NST; ++i) { mbar_init(full_b + 8 * i, C8 ? 4 : 1); mbar_init(empty_b + 8 * i, 1); }
     if (C8) {
@@ -373,21 +370,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
     *abort_word = 0;
     fence_mbar_init();
   }
-  if (warp == 0) { tmem_alloc(smem_u32(tmem_slot), 512); tmem_relinquish(); }
-  tc_fence_before();
+  if (threadIdx.x == 256) {
+    prefetch_tmap(&tm_cache);
+    prefetch_tmap(&tm_lat);
+  }
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers exist before any remote arrive
+  griddep_wait();       // the inputs all come from the stream's earlier kernels, and those may still need their TMEM
+  if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), 512); tmem_relinquish(); }
+  tc_fence_before();
+
+  // ---- the schedule: tile prefix over the batch, then this cluster's slice ----
+  int per, g0, g1;
+  attn_schedule<FLAT>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  using TileWalk = TileWalkT<FLAT>;
+  const TileWalk wl{pref, a.n, a.n_pre, att_pad(a.H), 0, 0};
+  const int N = g0 < g1 ? wl.before(g1) - wl.before(g0) : 0;
+  if (N <= 0) {   // both CTAs of the cluster take this branch together
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
   if (threadIdx.x == 0) griddep_launch_dependents();
 
   if (warp == 8) {
     // ---------------- TMA producer (lane 0 issues; lane k holds the block id of tile i + k) ----------------
-    if (lane == 0) {
-      prefetch_tmap(&tm_cache);
-      prefetch_tmap(&tm_lat);
-    }
-    TileWalk w{pref, a.n, 0, 0};
+    TileWalk w = wl;
     w.start(g0);
     int i = 0, blkv = 0;
     int2 ofv = make_int2(0, 0);
@@ -477,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       // descriptors built once; stages and k-steps add their byte offset >> 4
       const uint64_t d_t = sdesc_sw128_sbo(tile_s, 4096), d_rope = sdesc_sw128(sbase + SM::ROPE_OFF);
       const uint64_t d_qpe = sdesc_sw128(sbase + SM::QPE_OFF);
-      TileWalk ws{pref, a.n, 0, 0};
+      TileWalk ws = wl;
       ws.start(g0);
       int ks = 0;
       for (int t = 0; t < N; ++t, ws.next()) {
@@ -517,7 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
     if (C8 || lane == 0) {
       constexpr uint32_t idesc_o = C8 ? idesc_f16(128, 256, 1) : idesc_bf16(128, 256, 1);
       const uint64_t d_v = sdesc_sw128_mn_sbo(tile_s, 1024, 4096), d_p = sdesc_sw128(x_s);
-      TileWalk wo{pref, a.n, 0, 0};
+      TileWalk wo = wl;
       wo.start(g0);
       int ko = 0;
       for (int u = 0; u < N; ++u, wo.next()) {
@@ -632,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       for (int k0 = 0; k0 < 8; k0 += 2) {
         float v[16];
         tmem_ld16(sa + 8 * k0, (uint32_t*)v);
-        tmem_ld_wait();
+        tmem_ld_wait<16>((uint32_t*)v);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // chunk k0 + k (8 values) of row h at slot (k0 + k) ^ (h & 7): no bank conflicts
           uint32_t w[4];
@@ -671,29 +680,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       const bool live = h < attn_rows<FLAT>(a, b);
       const long long qh = attn_row0<FLAT>(a, b) + (live ? h : 0);
       const uint4* src = (const uint4*)(a.q_abs + qh * 512 + r * 256 + 128 * g);
+      const uint4* pe = (const uint4*)(a.q_pe + qh * 64 + 32 * g);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 pv[4];
 #pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4) {
-        uint32_t qv[16];
+      for (int k = 0; k < 4; ++k) pv[k] = live ? pe[k] : zero;
+      constexpr int NL = 8;   // loads in flight: their latency is what this costs (all 16: 2 us slower at 16 heads)
+#pragma unroll 1
+      for (int k0 = 0; k0 < 16; k0 += NL) {
+        uint4 v[NL];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint4 v = live ? src[4 * k4 + k] : make_uint4(0, 0, 0, 0);
-          if (C8) v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-          qv[4 * k] = v.x; qv[4 * k + 1] = v.y; qv[4 * k + 2] = v.z; qv[4 * k + 3] = v.w;
+        for (int k = 0; k < NL; ++k) v[k] = live ? src[k0 + k] : zero;
+#pragma unroll
+        for (int k = 0; k < NL; k += 4) {
+          uint32_t qv[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint4 x = v[k + j];
+            if (C8) x = make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+            qv[4 * j] = x.x; qv[4 * j + 1] = x.y; qv[4 * j + 2] = x.z; qv[4 * j + 3] = x.w;
+          }
+          tmem_st16(tmem + ATT_TM_Q + lane_base + 64 * g + 4 * (k0 + k), qv);
         }
-        tmem_st16(tmem + ATT_TM_Q + lane_base + 64 * g + 16 * k4, qv);
       }
       // q_pe row h, chunks 4 g .. 4 g + 3, in the 128-byte-swizzled K-major operand layout
-      const uint4* pe = (const uint4*)(a.q_pe + qh * 64 + 32 * g);
       uint4* qrow = (uint4*)(smem + SM::QPE_OFF + h * 128);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) qrow[(4 * g + k) ^ (h & 7)] = live ? pe[k] : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < 4; ++k) qrow[(4 * g + k) ^ (h & 7)] = pv[k];
       fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     };
-    TileWalk w{pref, a.n, 0, 0};
+    TileWalk w = wl;
     w.start(g0);
     load_q(w.b);
     constexpr float above = C8 ? 15.f : 8.f, below = C8 ? 7.f : 0.f;
@@ -716,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       const uint32_t sp_addr = tmem + ATT_TM_S + 64 * xb + 32 * g + lane_base;
       tmem_ld16(sp_addr, (uint32_t*)&v[0]);
       tmem_ld16(sp_addr + 16, (uint32_t*)&v[16]);
-      tmem_ld_wait();
+      tmem_ld_wait<32>((uint32_t*)v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free + 8 * xb);   // S(i + 2) may overwrite the buffer
@@ -794,7 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
           uint32_t o[16];
           const uint32_t oa = tmem + ATT_TM_O + lane_base + 128 * g + 16 * k;
           tmem_ld16(oa, o);
-          tmem_ld_wait();
+          tmem_ld_wait<16>(o);
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
           tmem_st16(oa, o);
@@ -825,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
         // the segment's S MMAs are all complete (the softmax read each S): the next
         // segment's query may replace this one while the last P.V runs
         if (i + 1 < N) {
-          TileWalk wn{pref, a.n, b, 0};
+          TileWalk wn = wl;
           wn.enter(b + 1);
           load_q(wn.b);
         }
@@ -837,16 +857,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
         if (!mbar_poll_warp(o_seg, kseg & 1, abort_word, a.flag)) { ok = false; break; }
         tc_fence_after();
         float* po = a.part_o + (unit * rows_u + h) * 512 + r * 256 + 128 * g;
-        for (int k = 0; k < 8; ++k) {
-          uint32_t o[16];
-          tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 16 * k, o);
-          tmem_ld_wait();
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {   // whole sectors: 32 bytes of a row per store
+          uint32_t o[32];
+          tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 32 * k, o);
+          tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 32 * k + 16, o + 16);
+          tmem_ld_wait<32>(o);
           if (store) {
 #pragma unroll
-            for (int jj = 0; jj < 16; jj += 4)
-              *reinterpret_cast<float4*>(po + 16 * k + jj) =
-                  make_float4(__uint_as_float(o[jj]), __uint_as_float(o[jj + 1]), __uint_as_float(o[jj + 2]),
-                              __uint_as_float(o[jj + 3]));
+            for (int jj = 0; jj < 32; jj += 8) st_global_8(po + 32 * k + jj, o + jj);
           }
         }
         tc_fence_before();
@@ -875,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

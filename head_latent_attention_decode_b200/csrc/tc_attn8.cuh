@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
     tc_attn8_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
                     TcAttn8Args a) {
   using SM = Attn8Smem;
-  griddep_wait();   // the inputs all come from the stream's earlier kernels
   constexpr int NPR = SM::NPR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -199,6 +198,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
     *abort_word = 0;
     fence_mbar_init();
   }
+  griddep_wait();   // the inputs all come from the stream's earlier kernels, and those may still need their TMEM
   if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), 512); tmem_relinquish(); }
   // ---- the schedule ----
   const int T_flat = a.flat ? (a.len + 127) / 128 : 0;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
         fetch_box(w);
       }
       const uint32_t rb = rfull + 8 * (i & 1);
-      if (!mbar_wait_warp(rempty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
+      if (!mbar_poll_warp(rempty + 8 * (i & 1), ((i >> 1) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
       if (lane == 0) {
         tile_s[i & 1] = tile;
         mbar_arrive_expect_tx(rb, 16384 + __popc(boxes) * a.box * 4);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int e = 2 * i + g, slot = e % NPR;
-        if (!mbar_wait_warp(empty_b + 8 * slot, ((e / NPR) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
+        if (!mbar_poll_warp(empty_b + 8 * slot, ((e / NPR) & 1) ^ 1, abort_word, a.flag)) { ok = false; break; }
         if (lane == 0) mbar_arrive_expect_tx(full_b + 8 * slot, 32768);
         __syncwarp();
         if (lane < nb)
@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
         tmem_ld16(sa, u);
         tmem_ld16(sa + 16, u + 16);
         tmem_ld16(sa + 32, rp);
-        tmem_ld_wait();
+        tmem_ld_wait<32>(u);
+        tmem_ld_pin<16>(rp);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float4 s4 = *reinterpret_cast<const float4*>(sq + 4 * k);
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
               uint32_t v[64];
 #pragma unroll
               for (int g = 0; g < 4; ++g) tmem_ld16(tm_o + 128 * set + 32 * g + 16 * o, v + 16 * g);
-              tmem_ld_wait();
+              tmem_ld_wait<64>(v);
 #pragma unroll
               for (int h = 0; h < 64; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h & 7]);
 #pragma unroll
@@ -674,20 +675,20 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
       if (!first && !mbar_poll_warp(p_free + 8 * (set ^ 1), ((i - 1) >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       tc_fence_after();
       float* po = a.part_o + unit * 16 * 512 + row;
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         uint32_t o[32];
         float out[16];
         tmem_ld16(tm_o + 128 * set + 32 * g, o);
         tmem_ld16(tm_o + 128 * set + 32 * g + 16, o + 16);
-        tmem_ld_wait();
+        tmem_ld_wait<32>(o);
 #pragma unroll
         for (int h = 0; h < 16; ++h)
           out[h] = __uint_as_float(o[16 * (h >> 3) + (h & 7)]) + __uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]);
         if (!first) {
           tmem_ld16(tm_o + 128 * (set ^ 1) + 32 * g, o);
           tmem_ld16(tm_o + 128 * (set ^ 1) + 32 * g + 16, o + 16);
-          tmem_ld_wait();
+          tmem_ld_wait<32>(o);
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
             const float fa = ref_w[h], fb = al_w[h];

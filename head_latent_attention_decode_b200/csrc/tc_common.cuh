@@ -140,6 +140,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same for a caller whose N values (a multiple of 16) are in flight: nothing that uses them moves up
+// past the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_pin(uint32_t* r) {
+#pragma unroll
+  for (int k = 0; k < N; k += 16)
+    asm volatile(""
+                 : "+r"(r[k]), "+r"(r[k + 1]), "+r"(r[k + 2]), "+r"(r[k + 3]), "+r"(r[k + 4]), "+r"(r[k + 5]),
+                   "+r"(r[k + 6]), "+r"(r[k + 7]), "+r"(r[k + 8]), "+r"(r[k + 9]), "+r"(r[k + 10]), "+r"(r[k + 11]),
+                   "+r"(r[k + 12]), "+r"(r[k + 13]), "+r"(r[k + 14]), "+r"(r[k + 15]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t* r) {
+  tmem_ld_wait();
+  tmem_ld_pin<N>(r);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
@@ -448,6 +464,13 @@ __device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity, vo
       break;
     }
   return __all_sync(0xffffffffu, ok);
+}
+
+// 32 bytes, 32-byte aligned, in one store.
+__device__ __forceinline__ void st_global_8(float* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Two fp32 operations in one instruction.
