@@ -145,41 +145,24 @@ struct TileWalkT {
   const int* pref;   // pref[b] = tiles of entries 0..b-1, each with its padding (shared memory)
   int n, n_pre, pad_own, b, lt;
   __device__ int pad(int e) const { return !FLAT ? 0 : (e < n_pre ? att_pad(128) : pad_own); }
-  __device__ int pads(int e) const {   // of the entries before e
-    return !FLAT ? 0 : min(e, n_pre) * att_pad(128) + max(e - n_pre, 0) * pad_own;
-  }
   __device__ int tiles() const { return pref[b + 1] - pref[b] - pad(b); }
-  // the last entry that begins at or before list position g
-  __device__ int find(int g) const {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pref[mid] <= g) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  }
-  __device__ void start(int g) {
-    b = find(g);
-    lt = g - pref[b];
-    if (FLAT && lt >= tiles()) enter(b + 1);
-  }
   __device__ void enter(int e) {
     b = e;
     lt = 0;
     while (b < n && tiles() == 0) ++b;
   }
+  // `k` tiles on (the list is long enough), entry by entry
+  __device__ void skip(int k) {
+    for (int left = tiles() - lt; k >= left; left = tiles()) {
+      k -= left;
+      enter(b + 1);
+    }
+    lt += k;
+  }
   __device__ bool seg_last() const { return lt + 1 == tiles(); }
   __device__ void next() {
     if (seg_last()) enter(b + 1);
     else ++lt;
-  }
-  // real tiles before list position g
-  __device__ int before(int g) const {
-    if (!FLAT) return g;
-    if (g >= pref[n]) return pref[n] - pads(n);
-    const int e = find(g);
-    return pref[e] - pads(e) + min(g - pref[e], pref[e + 1] - pref[e] - pad(e));
   }
 };
 
@@ -210,30 +193,30 @@ __device__ __forceinline__ int attn_rows(const TcAttnArgs& a, int b) {
   return FLAT && b < a.n_pre ? (int)min(128LL, a.rows_total - b * 128LL) : a.H;
 }
 
-// The balanced schedule of a persistent attention kernel: the prefix sum of
-// the batch's tiles of `tile_rows` rows, in shared memory (pref[b] = tiles of
-// sequences 0..b-1, n + 1 entries, n <= 256), and the slice [g0, g1) of the
-// flattened tile list that cluster c takes (slices of `per` tiles, at least
-// a.min_per). Block 0 of the grid writes each sequence's segment count to
-// a.nseg. Every thread of the CTA calls it; it ends with a __syncthreads.
-template <bool FLAT = false>
-__device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows, int* pref, int c, uint32_t r,
-                                              int warp, int lane, int* per_out, int* g0_out, int* g1_out) {
+// The balanced schedule: the prefix sum of the batch's tiles of 64 rows, in shared
+// memory (pref[b] = tiles of entries 0..b-1 with their padding, n + 1 entries, n <=
+// 256), and the slice of the flattened tile list that cluster c takes (slices of
+// `per`, at least a.min_per): its tiles N, and the first one's entry b0 and place
+// lt0 in it, which one warp finds while it has the list in registers. Block 0 of the
+// grid writes each entry's segments to a.nseg or a.seg. Every thread of the CTA
+// calls it; there is a __syncthreads in it.
+struct AttnSlice { int per, N, b0, lt0; };
+template <bool FLAT>
+__device__ __forceinline__ AttnSlice attn_schedule(const TcAttnArgs& a, int* pref, int c, uint32_t r, int warp, int lane) {
+  int* out = pref + ATT_MAX_SEQ + 1;   // N, b0, lt0
+  auto pad = [&](int b) { return !FLAT ? 0 : (b < a.n_pre ? att_pad(128) : att_pad(a.H)); };
   if (warp == 0) {
-    int cnt[8], len[8], sum = 0;
+    int cnt[8], sum = 0;   // tiles of entries 8 lane + k
 #pragma unroll
-    for (int k = 0; k < 8; ++k) len[k] = 8 * lane + k < a.n ? attn_seq_len<FLAT>(a, 8 * lane + k) : 0;   // loads in flight
+    for (int k = 0; k < 8; ++k) cnt[k] = 8 * lane + k < a.n ? attn_seq_len<FLAT>(a, 8 * lane + k) : 0;   // loads in flight
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int b = 8 * lane + k;
-      int T = 0;
       if (b < a.n) {
-        const int L = len[k];
-        if (L == 0 && c == 0 && r == 0 && !(a.allow_empty && a.ctx[FLAT ? b - a.n_pre : b] == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
-        T = (L + tile_rows - 1) / tile_rows + (FLAT ? (b < a.n_pre ? att_pad(128) : att_pad(a.H)) : 0);
+        if (cnt[k] == 0 && c == 0 && r == 0 && !(a.allow_empty && a.ctx[FLAT ? b - a.n_pre : b] == 0)) set_flag(a.flag, MLA_FLAG_BAD_CONTEXT);
+        cnt[k] = (cnt[k] + 63) / 64;
+        sum += cnt[k] + pad(b);
       }
-      cnt[k] = T;
-      sum += T;
     }
     int incl = sum;
 #pragma unroll
@@ -241,29 +224,39 @@ __device__ __forceinline__ void attn_schedule(const TcAttnArgs& a, int tile_rows
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    int run = incl - sum;
+    const int total = __shfl_sync(0xffffffffu, incl, 31);   // the batch's tile count
+    const int per = max((total + a.units - 1) / a.units, a.min_per), g0 = c * per, g1 = min(total, g0 + per);
+    int run = incl - sum, N = 0, b0 = -1, lt0 = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int b = 8 * lane + k;
-      if (b < a.n) pref[b] = run;
-      run += cnt[k];
+      if (b < a.n) {
+        pref[b] = run;
+        const int lo = max(g0, run), n_here = min(g1, run + cnt[k]) - lo;   // its tiles within [g0, g1)
+        if (n_here > 0) {
+          if (b0 < 0) { b0 = b; lt0 = lo - run; }
+          N += n_here;
+        }
+        run += cnt[k] + pad(b);
+      }
     }
-    if (lane == 31) pref[a.n] = incl;   // the batch's tile count
+    const uint32_t has = __ballot_sync(0xffffffffu, b0 >= 0);
+    if (has && lane == __ffs(has) - 1) { out[1] = b0; out[2] = lt0; }
+    N = __reduce_add_sync(0xffffffffu, N);
+    if (lane == 0) out[0] = N;
+    if (lane == 31) pref[a.n] = total;
   }
   __syncthreads();
-  const int total = pref[a.n];
-  int per = (total + a.units - 1) / a.units;
-  if (per < a.min_per) per = a.min_per;
-  if (blockIdx.x == 0) {   // segments of each sequence, for the merge
+  const int total = pref[a.n], per = max((total + a.units - 1) / a.units, a.min_per);
+  if (blockIdx.x == 0) {   // segments of each entry, for the merge
     for (int b = threadIdx.x; b < a.n; b += blockDim.x) {
-      const int T = pref[b + 1] - pref[b] - (FLAT ? (b < a.n_pre ? att_pad(128) : att_pad(a.H)) : 0);
-      if (FLAT) a.seg[b] = T > 0 ? make_int2(pref[b] / per, (pref[b] + T - 1) / per - pref[b] / per + 1) : make_int2(0, 0);
-      else a.nseg[b] = T > 0 ? (pref[b] + T - 1) / per - pref[b] / per + 1 : 0;
+      const int T = pref[b + 1] - pref[b] - pad(b);
+      const int first = pref[b] / per, last = (pref[b] + T - 1) / per;
+      if (FLAT) a.seg[b] = T > 0 ? make_int2(first, last - first + 1) : make_int2(0, 0);
+      else a.nseg[b] = T > 0 ? last - first + 1 : 0;
     }
   }
-  *per_out = per;
-  *g0_out = c * per;
-  *g1_out = min(total, c * per + per);
+  return {per, out[0], out[1], out[2]};
 }
 
 // Two bf16 in f16 (infinite beyond 65504, off by 2^-25 below 2^-14).
@@ -381,13 +374,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
   tc_fence_before();
 
   // ---- the schedule: tile prefix over the batch, then this cluster's slice ----
-  int per, g0, g1;
-  attn_schedule<FLAT>(a, 64, pref, c, r, warp, lane, &per, &g0, &g1);
+  const AttnSlice slice = attn_schedule<FLAT>(a, pref, c, r, warp, lane);
+  const int per = slice.per, N = slice.N;
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   using TileWalk = TileWalkT<FLAT>;
-  const TileWalk wl{pref, a.n, a.n_pre, att_pad(a.H), 0, 0};
-  const int N = g0 < g1 ? wl.before(g1) - wl.before(g0) : 0;
+  const TileWalk wl{pref, a.n, a.n_pre, att_pad(a.H), slice.b0, slice.lt0};   // at the first tile
   if (N <= 0) {   // both CTAs of the cluster take this branch together
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
@@ -397,14 +389,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
   if (warp == 8) {
     // ---------------- TMA producer (lane 0 issues; lane k holds the block id of tile i + k) ----------------
     TileWalk w = wl;
-    w.start(g0);
     int i = 0, blkv = 0;
     int2 ofv = make_int2(0, 0);
     for (; i < N; ++i, w.next()) {
       if ((i & 31) == 0) {   // the block ids of the next 32 tiles, loaded in parallel
         TileWalk wk = w;
-        for (int k = 0; k < lane && i + k + 1 < N; ++k) wk.next();
         if (i + lane < N) {
+          wk.skip(lane);
           blkv = attn_table<FLAT>(a, wk.b)[(64 * wk.lt) / a.bs];
           const bool good = blkv >= 0 && blkv < a.n_blocks;
           ofv.x = (good ? min(64, attn_seq_len<FLAT>(a, wk.b) - 64 * wk.lt) : 0) + (i + lane == N - 1 || wk.seg_last() ? 128 : 0);
@@ -487,7 +478,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       const uint64_t d_t = sdesc_sw128_sbo(tile_s, 4096), d_rope = sdesc_sw128(sbase + SM::ROPE_OFF);
       const uint64_t d_qpe = sdesc_sw128(sbase + SM::QPE_OFF);
       TileWalk ws = wl;
-      ws.start(g0);
       int ks = 0;
       for (int t = 0; t < N; ++t, ws.next()) {
         const int st = t % ATT_NST;
@@ -527,7 +517,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       constexpr uint32_t idesc_o = C8 ? idesc_f16(128, 256, 1) : idesc_bf16(128, 256, 1);
       const uint64_t d_v = sdesc_sw128_mn_sbo(tile_s, 1024, 4096), d_p = sdesc_sw128(x_s);
       TileWalk wo = wl;
-      wo.start(g0);
       int ko = 0;
       for (int u = 0; u < N; ++u, wo.next()) {
         const int st = u % ATT_NST, xb = u & 1;
@@ -713,9 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       __syncwarp();
       if (lane == 0) mbar_arrive(q_ready);
     };
-    TileWalk w = wl;
-    w.start(g0);
-    load_q(w.b);
+    load_q(wl.b);
     constexpr float above = C8 ? 15.f : 8.f, below = C8 ? 7.f : 0.f;
     float m_ref = -INFINITY, l = 0.f;
     int tseg = 0, kseg = 0;   // tile within the segment, segments done

@@ -117,21 +117,6 @@ struct Walk8 {
   const int* pref;   // tiles before entry e (shared memory), or NULL: e * T
   int T, n, e, lt, len, tiles;
   __device__ __forceinline__ int at(int i) const { return pref ? pref[i] : i * T; }
-  __device__ __forceinline__ void start(const TcAttn8Args& a, int g) {
-    if (pref) {
-      int lo = 0, hi = n - 1;   // the last entry that begins at or before g: it is not empty
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pref[mid] <= g) lo = mid;
-        else hi = mid - 1;
-      }
-      e = lo;
-    } else {
-      e = g / T;
-    }
-    lt = g - at(e);
-    enter(a);
-  }
   __device__ __forceinline__ void enter(const TcAttn8Args& a) {
     len = a8_len(a, e);
     tiles = (len + 127) / 128;
@@ -174,6 +159,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
   const uint32_t post_b = red_b + 32;                             // [4 tiles] a tile's warps are done
   int4* tile_s = (int4*)(smem + SM::BAR_OFF + 384);   // [2]: {keys in the tile, boxes loaded, TILE_ bits, entry}
   volatile int* pv_fresh = (volatile int*)(smem + SM::BAR_OFF + 416);   // [2]: the set's first tile of an entry
+  int4* start_s = (int4*)(smem + SM::BAR_OFF + 432);   // the first tile: {entry, its tile, its length}
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 480);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 484);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,16 +205,26 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    for (int k = 0; k < each; ++k)
-      if (each * lane + k < a.n_ent) pref[each * lane + k] += incl - sum;
-    if (lane == 31) pref[a.n_ent] = incl;
+    // and the tile that this CTA begins with: one lane's entry holds it
+    const int all = __shfl_sync(0xffffffffu, incl, 31), g = c * max(1, (all + a.units - 1) / a.units);
+    for (int k = 0; k < each; ++k) {
+      const int e = each * lane + k;
+      if (e >= a.n_ent) break;
+      const int b0 = pref[e] + incl - sum;
+      pref[e] = b0;
+      if (b0 <= g) {
+        const int L = a8_len(a, e);
+        if (g < b0 + (L + 127) / 128) *start_s = make_int4(e, g - b0, L, 0);
+      }
+    }
+    if (lane == 31) pref[a.n_ent] = all;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const Walk8 w0{a.flat ? nullptr : pref, T_flat, a.n_ent, 0, 0, 0, 0};
+  Walk8 w0{a.flat ? nullptr : pref, T_flat, a.n_ent, 0, 0, 0, 0};
   const int total = w0.at(a.n_ent);
   const int per = max(1, (total + a.units - 1) / a.units);
   if (blockIdx.x == 0)
@@ -242,6 +238,15 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
     return;
   }
   const int g0 = (int)g0l, N = min(total - g0, per);
+  if (a.flat) {
+    w0.e = g0 / T_flat;
+    w0.lt = g0 - w0.e * T_flat;
+    w0.len = a.len;
+  } else {
+    const int4 at = *start_s;
+    w0.e = at.x; w0.lt = at.y; w0.len = at.z;
+  }
+  w0.tiles = (w0.len + 127) / 128;
 
   if (warp == 8) {
     // ---------------- TMA: lane k < 128 / box brings rows [box k, box k + box) of each tile ----------------
@@ -251,7 +256,6 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
     }
     const int nb = 128 / a.box, none = max(a.n_blocks, 1);   // a block id beyond the map
     Walk8 w = w0;
-    w.start(a, g0);
     // this lane's box of the walk's tile, one tile ahead of its use: the block id as loaded (so that
     // nothing waits for it) and the first row within the block
     int raw = 0, off = 0;
@@ -484,11 +488,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 #pragma unroll
     for (int h = 0; h < 16; ++h) l[h] = 0.f;
     bool ok = true;
-    if (set == 0) {   // while the first tile is on its way
-      Walk8 w = w0;
-      w.start(a, g0);
-      load_q(w.e, 0);
-    }
+    if (set == 0) load_q(w0.e, 0);   // while the first tile is on its way
     for (int i = set; i < N && ok; i += 2) {
       if (!mbar_poll_warp(rfull + 8 * set, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       const int4 tile = tile_s[set];
