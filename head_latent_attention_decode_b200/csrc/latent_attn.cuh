@@ -213,11 +213,13 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   // (about 17 us): worth it up to eight of such tiles per pair.
   const bool ride = H <= 128 && n * tiles <= 8LL * pairs;
   if (tc && h->cache8 && c.block_size % 16 == 0) {
-    // Per 128 keys the few-head kernel takes about 5 k cycles of one SM for every 16 heads, the
-    // head-major one about 9 k of two SMs whatever the heads up to 128.
+    // Per 128 keys the few-head kernel takes 1.7 us of one SM for every 16 heads (or 16 query rows), the
+    // head-major one 2.9 us of two SMs whatever the rows up to 128. Own rows, 32 sequences of 8192:
+    // 64 heads 111 against 126 us, 80 heads 139 against 128. A prefix of 16384: 48 rows 36 against 29 us,
+    // since the head-major launch takes the own rows along.
     w.heads_pre = pre && b64 && n * H > 32;
     w.few_pre = pre && !w.heads_pre;
-    w.heads_own = b64 && H <= 128 && (H > 48 || (w.heads_pre && ride));
+    w.heads_own = b64 && H <= 128 && (H > 64 || (w.heads_pre && ride));
     w.few_own = !w.heads_own;
   } else if (tc && !h->cache8 && b64 && H <= 128) {
     w.heads_pre = pre;

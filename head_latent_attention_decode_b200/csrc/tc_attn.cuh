@@ -345,8 +345,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       for (int i = 0; i < ATT_NRP; ++i) mbar_init(rope_full + 8 * i, 1);
       for (int i = 0; i < 2; ++i) { mbar_init(raw_full + 8 * i, 1); mbar_init(raw_empty + 8 * i, 4); }
     }
-    // C8: the issuing thread arrives too: it has seen the converters' arrivals, and with them kt
-    for (int i = 0; i < 2; ++i) { mbar_init(s_full + 8 * i, C8 ? 2 : 1); mbar_init(s_free + 8 * i, 12); }
+    // S: its MMAs and the issuing thread, which has seen the tile land and with it what the tile is
+    for (int i = 0; i < 2; ++i) { mbar_init(s_full + 8 * i, 2); mbar_init(s_free + 8 * i, 12); }
     for (int i = 0; i < ATT_NRP; ++i) mbar_init(rope_empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(p_full_b + 8 * i, 8);
@@ -503,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
           issue_commit<C8>(rope_empty + 8 * ri);
         }
         issue_commit<C8>(s_full + 8 * (t & 1));
-        if (C8 && lane == 0) mbar_arrive(s_full + 8 * (t & 1));
+        if (lane == 0) mbar_arrive(s_full + 8 * (t & 1));
         if (last) ++ks;
       }
       issue_commit<C8>(fin);
@@ -710,19 +710,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
     for (int i = 0; i < N && ok; ++i) {
       const int st = i % ATT_NST, xb = i & 1;
       if (g == 0 && lane == 0) mbar_arrive_expect_tx(x_full_b + 8 * (4 * xb + q), 4096);   // this quarter's rows
-      // the tile landed before its S: this only makes what came with it visible
-      if (!mbar_poll_warp(full_b + 8 * st, (i / ATT_NST) & 1, abort_word, a.flag)) { ok = false; break; }
-      const int2 of = tile_of[st];
-      const int valid = of.x & 127, b = of.y;
-      const bool last = of.x & 128;
-      const int kt = C8 ? tile_kt[st] : 0;
-      const float un = C8 ? exp2_int(kt) : 1.f;
       if (!mbar_poll_warp(s_full + 8 * xb, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       tc_fence_after();
       float v[32];
       const uint32_t sp_addr = tmem + ATT_TM_S + 64 * xb + 32 * g + lane_base;
       tmem_ld16(sp_addr, (uint32_t*)&v[0]);
       tmem_ld16(sp_addr + 16, (uint32_t*)&v[16]);
+      const int2 of = tile_of[st];
+      const int valid = of.x & 127, b = of.y;
+      const bool last = of.x & 128;
+      const int kt = C8 ? tile_kt[st] : 0;
+      const float un = C8 ? exp2_int(kt) : 1.f;
       tmem_ld_wait<32>((uint32_t*)v);
       tc_fence_before();
       __syncwarp();
