@@ -55,12 +55,14 @@
 // weights are f16 too: kept below 2^15, they hold their 11 bits down to 2^-29 of
 // the largest and are off by 2^-40 of it below. So is the query (one beyond 65504
 // ends as NaN, one below 2^-14 is off by 2^-25).
-// (Widening to bf16, scale and all, took three times the instructions, and scales
-// kept out of V' two products a weight in the softmax: 340 and 424 us for 64
-// sequences of 1024 to 16384 rows and 128 heads where this form took 331, before
-// the code was made smaller, which took it to 262: see mbar_poll_long. Feeding the
-// codes to kind::f8f6f4 MMAs would take as many MMAs, query and weights being split
-// in two there, and put their splitting into the softmax, which bounds this kernel.)
+// For 64 sequences of 1024 to 16384 rows and 128 heads: 242 us (the 16-bit cache's
+// tiles 2400 cycles, these 2700: the three stages, each held from its conversion
+// through S, the exchange and the softmax to its P.V, bound it). Widening to bf16,
+// scale and all, took three times the instructions and 340 us; scales kept out of V'
+// cost the softmax two products a weight and took 424, when this form took 331; smaller
+// code then gave 262 (mbar_poll_long), shorter starts, ends and waits the rest.
+// Feeding the codes to kind::f8f6f4 MMAs would take as many MMAs, query and weights
+// being split in two there, and put their splitting into the softmax.
 // The latent ring is three deep, in the same shared memory.
 #pragma once
 
@@ -568,7 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       if (cw == 0 && lane == 0) { tile_of[st] = of; tile_kt[st] = kt; }
       const uint8_t* src = smem + SM::RAW_OFF + rb * 16384 + (cw >> 1) * 1024 + ro * 128 + ((cc ^ ro) << 4);
       uint8_t* dst = smem + SM::TILE_OFF + st * SM::STAGE + (2 * (cw >> 1) + (cc >> 2)) * 1024 + ro * 128;
-#pragma unroll 2
+#pragma unroll
       for (int oct = 0; oct < 8; ++oct) {
         uint4 cv = *reinterpret_cast<const uint4*>(src + oct * 2048);
         if (8 * oct + ro >= rows) cv = make_uint4(0, 0, 0, 0);

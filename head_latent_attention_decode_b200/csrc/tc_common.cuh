@@ -225,8 +225,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn_major =
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// kind::f16 with f16 A and B, fp32 accumulator; K-major operands but for b_mn_major.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major = 0) {
+// kind::f16 with f16 A and B, fp32 accumulator, A K-major, B MN-major if told so.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
