@@ -197,7 +197,10 @@ struct LatentPlan {
   size_t o_p, ml_p, seg_p;
 };
 
-static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned) {
+// `force` < 0: by the rules; else bit 0 says whether a prefix goes to the head-major kernel and bit 1
+// whether the own rows ride along, as a smaller call may have it (latent_ws_bytes).
+static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned,
+                                     int force = -1) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads;
   const int sms = h->tc.num_sms > 0 ? h->tc.num_sms : 148, pairs = sms / 2 > 0 ? sms / 2 : 1;
@@ -211,13 +214,13 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   // The own rows may ride in the prefix's head-major launch. With few heads that wastes most of its 128
   // rows (2 us per 64 rows and SM pair whatever the heads), but saves a launch with its start-up and tail
   // (about 17 us): worth it up to eight of such tiles per pair.
-  const bool ride = H <= 128 && n * tiles <= 8LL * pairs;
+  const bool ride = H <= 128 && (force < 0 ? n * tiles <= 8LL * pairs : (force & 2) != 0);
   if (tc && h->cache8 && c.block_size % 16 == 0) {
     // Per 128 keys the few-head kernel takes 1.7 us of one SM for every 16 heads (or 16 query rows), the
     // head-major one 2.9 us of two SMs whatever the rows up to 128. Own rows, 32 sequences of 8192:
     // 64 heads 111 against 126 us, 80 heads 139 against 128. A prefix of 16384: 48 rows 36 against 29 us,
     // since the head-major launch takes the own rows along.
-    w.heads_pre = pre && b64 && n * H > 32;
+    w.heads_pre = pre && b64 && (force < 0 ? n * H > 32 : (force & 1) != 0);
     w.few_pre = pre && !w.heads_pre;
     w.heads_own = b64 && H <= 128 && (H > 64 || (w.heads_pre && ride));
     w.few_own = !w.heads_own;
@@ -237,7 +240,7 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
     const long long per = (w.heads_own ? 128 : 0) + (w.heads_pre ? H : 0);
     limit((ATT_MAX_SEQ - 1) * 128LL / per);
   }
-  if (!w.simt) {   // tiles are counted in int
+  if (!w.simt && force < 0) {   // tiles are counted in int
     const long long p = cdiv(prefix_len, 64) * cdiv(H, 16);
     limit((1 << 29) / (tiles > p ? tiles : p));
   }
@@ -276,10 +279,17 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   w.total = off;
   return w;
 }
+// Enough for every call of up to these sizes: what a smaller one needs may be more where it takes other
+// kernels.
 static inline size_t latent_ws_bytes(const mla_handle* h, long long n, int prefix_len, int max_ctx) {
-  const size_t a = latent_plan(h, n, prefix_len, max_ctx, true).total;
-  const size_t b = latent_plan(h, n, prefix_len, max_ctx, false).total;
-  return a > b ? a : b;
+  size_t most = 0;
+  for (int p = 0; p < (prefix_len > 0 ? 2 : 1); ++p)
+    for (int force = 0; force < 4; ++force)
+      for (int aligned = 0; aligned < 2; ++aligned) {
+        const size_t t = latent_plan(h, n, p ? prefix_len : 0, max_ctx, aligned != 0, force).total;
+        if (t > most) most = t;
+      }
+  return most;
 }
 
 static inline void launch_merge(const MergeArgs& m, int n, int most, int o_dt, cudaStream_t s) {

@@ -44,19 +44,18 @@
 // row (16 KB a tile, two raw buffers) and the row scales 2^k_j; four more warps
 // widen them to f16, one conversion for two codes, into the latent stage. Codes
 // and scales together do not fit f16's exponents, but a tile's rows relative to
-// its largest do: with kt the tile's largest k_j plus 9 the stage holds
-//   V'_j = 2^(k_j - kt) code_j, at most 1,
-// exact for rows down to 2^-6 of the largest and off by 2^-25 of it below (a row
-// under 2^-15 of its tile's largest is taken as zeros), and the rotary rows take
-// 2^-kt as well. Partial scores leave the MMA as S 2^-kt and are brought back to
+// its largest do: with kt the tile's largest k_j less 6 the stage holds
+//   V'_j = 2^(k_j - kt) code_j, at most 2^15,
+// exact for rows down to 2^-21 of the tile's largest scale (the values of smaller
+// ones are off by up to 2^-22 of it), and the rotary rows take 2^-kt as well. Partial scores leave the MMA as S 2^-kt and are brought back to
 // real units as they are read; with the reference R of y = score log2(e) + kt the
 // weights 2^(y - R) bring V' back to the rows' own size in O, and the row sums take
 // them times 2^-kt: one number a tile, so the softmax is the 16-bit cache's. The
 // weights are f16 too: kept below 2^15, they hold their 11 bits down to 2^-29 of
-// the largest and are off by 2^-40 of it below. So is the query (one beyond 65504
-// ends as NaN, one below 2^-14 is off by 2^-25).
-// For 64 sequences of 1024 to 16384 rows and 128 heads: 242 us (the 16-bit cache's
-// tiles 2400 cycles, these 2700: the three stages, each held from its conversion
+// the largest and are off by 2^-40 of it below. So is the query (within +-65504; an
+// entry below 2^-14 is off by 2^-25).
+// For 64 sequences of 1024 to 16384 rows and 128 heads: 236 us (the 16-bit cache's
+// tiles 2400 cycles, these 2650: the three stages, each held from its conversion
 // through S, the exchange and the softmax to its P.V, bound it). Widening to bf16,
 // scale and all, took three times the instructions and 340 us; scales kept out of V'
 // cost the softmax two products a weight and took 424, when this form took 331; smaller
@@ -329,10 +328,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
   const uint32_t rope_full = rope_empty + 8 * ATT_NRP;   // C8: [ATT_NRP] rotary block landed
   const uint32_t raw_full = rope_full + 8 * ATT_NRP;     // C8: [2] codes and scales landed
   const uint32_t raw_empty = raw_full + 16;              // C8: [2] codes converted
-  // of the tile in each stage: rows that count + 128 for a segment's last, its entry; C8: kt too, and
-  // the first two also of the tile in each raw buffer
+  // of the tile in each stage: rows that count + 128 for a segment's last, its entry; C8: the same of
+  // the tile in each raw buffer, and the tiles' kt. The senders read kt too, and no wait of this CTA
+  // holds a stage for them: tile t + 8 is converted after this CTA's P.V(t + 5), so after the peer's
+  // S(t + 5) and its P.V(t + 2), which took what the senders sent of t.
   int2* tile_of = (int2*)(smem + SM::BAR_OFF + 464);
-  int* tile_kt = (int*)(smem + SM::BAR_OFF + 496);
+  int* tile_kt = (int*)(smem + SM::BAR_OFF + 416);   // [8]
   int2* raw_of = (int2*)(smem + SM::SC_OFF + 512);
   uint32_t* tmem_slot = (uint32_t*)(smem + SM::BAR_OFF + 448);
   volatile int* abort_word = (volatile int*)(smem + SM::BAR_OFF + 452);
@@ -560,14 +561,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
         return v > 0.f ? (int)(__float_as_uint(v) >> 23) - 127 : -1000;
       };
       const int k0 = exponent(lane), k1 = exponent(lane + 32);
-      const int km = __reduce_max_sync(0xffffffffu, max(k0, k1)), kt = km > -1000 ? km + 9 : 0;
+      const int km = __reduce_max_sync(0xffffffffu, max(k0, k1)), kt = km > -1000 ? km - 6 : 0;
       auto factor = [&](int k) -> uint32_t {
         const int d = k - kt;
         return d >= -14 ? (uint32_t)(d + 15) << 10 : (d >= -24 ? 1u << (d + 24) : 0u);
       };
       const uint32_t f01 = factor(k0) | factor(k1) << 16;
       if (!mbar_poll_warp(empty_b + 8 * st, ((t / ATT_NST) & 1) ^ 1, abort_word, a.flag)) break;
-      if (cw == 0 && lane == 0) { tile_of[st] = of; tile_kt[st] = kt; }
+      if (cw == 0 && lane == 0) { tile_of[st] = of; tile_kt[t & 7] = kt; }
       const uint8_t* src = smem + SM::RAW_OFF + rb * 16384 + (cw >> 1) * 1024 + ro * 128 + ((cc ^ ro) << 4);
       uint8_t* dst = smem + SM::TILE_OFF + st * SM::STAGE + (2 * (cw >> 1) + (cc >> 2)) * 1024 + ro * 128;
 #pragma unroll
@@ -621,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
     for (int i = 0; i < N; ++i) {
       if (!mbar_poll_warp(s_full + 8 * (i & 1), (i >> 1) & 1, abort_word, a.flag)) break;
       tc_fence_after();
-      const float un = C8 ? exp2_int(tile_kt[i % ATT_NST]) : 1.f;
+      const float un = C8 ? exp2_int(tile_kt[i & 7]) : 1.f;
       const uint32_t sa = tmem + ATT_TM_S + 64 * (i & 1) + lane_base;
       if (lane == 0) bulk_wait_read_all();               // this warp's previous copy has left its rows
       __syncwarp();
@@ -721,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
       const int2 of = tile_of[st];
       const int valid = of.x & 127, b = of.y;
       const bool last = of.x & 128;
-      const int kt = C8 ? tile_kt[st] : 0;
+      const int kt = C8 ? tile_kt[i & 7] : 0;
       const float un = C8 ? exp2_int(kt) : 1.f;
       tmem_ld_wait<32>((uint32_t*)v);
       tc_fence_before();

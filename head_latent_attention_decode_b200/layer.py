@@ -110,6 +110,15 @@ class MlaLayer:
             raise ValueError(f"kv_cache does not hold blocks of this layer's cache ({self._cache_torch}, "
                              f"{self.block_bytes} bytes a block)")
 
+    def _check_cache_bytes(self, kv_cache):
+        """For the calls that took any tensor before: an 8-bit cache is checked, another only for its size."""
+        if kv_cache is None:
+            return
+        if self.cache_dtype == "fp8":
+            self._check_cache(kv_cache)
+        elif kv_cache.nbytes < kv_cache.shape[0] * self.block_bytes:
+            raise ValueError(f"kv_cache is smaller than its {kv_cache.shape[0]} blocks of {self.block_bytes} bytes")
+
     def _check_rows(self, rows):
         if rows.dtype != self.act or rows.dim() != 2 or rows.shape[1] != self.shape.kv_row_dim:
             raise ValueError(f"rows must be [n, {self.shape.kv_row_dim}] {self.act}")
@@ -131,7 +140,7 @@ class MlaLayer:
         return rows
 
     def _check_prefix(self, prefix_table, prefix_len):
-        if prefix_len and prefix_table.numel() * self.shape.block_size < prefix_len:
+        if prefix_len and (prefix_table is None or prefix_table.numel() * self.shape.block_size < prefix_len):
             raise ValueError("prefix_table does not cover prefix_len rows")
 
     def latent_attn(self, q_abs, q_pe, kv_cache, block_table, context_lens, max_context_len, prefix_table=None,
@@ -175,6 +184,7 @@ class MlaLayer:
     def decode_qkv(self, hidden, cos, sin, kv_cache, slot_mapping, q_abs=None, q_pe=None, input_norm_w=None):
         s = self.shape
         n = hidden.shape[0]
+        self._check_cache_bytes(kv_cache)
         if q_abs is None:
             q_abs = torch.empty((n, s.n_heads, s.kv_lora_rank), dtype=self.act, device=self.device)
         if q_pe is None:
@@ -189,6 +199,7 @@ class MlaLayer:
                     out=None, head_out=None):
         s = self.shape
         n = q_abs.shape[0]
+        self._check_cache_bytes(kv_cache)
         if out is None:
             out = torch.empty((n, s.hidden), dtype=self.act, device=self.device)
         ws = self.ws if self.ws is not None and self.ws.numel() >= mla_workspace_bytes(
@@ -213,6 +224,7 @@ class MlaLayer:
     def prefill(self, hidden, cos, sin, out=None, head_out=None, kv_cache=None, slot_mapping=None):
         s = self.shape
         S = hidden.shape[0]
+        self._check_cache_bytes(kv_cache)
         if out is None:
             out = torch.empty((S, s.hidden), dtype=self.act, device=self.device)
         ws = self.ws if self.ws is not None and self.ws.numel() >= mla_workspace_bytes(

@@ -199,7 +199,11 @@ int mla_clear_device_flag(void* ws, void* stream);
  * mla_decode_qkv, mla_decode_qkv_noalloc, mla_prefill and mla_decode_step_host
  * then quantise the rows they write, and mla_decode_attn reads them; kv_cache
  * must be 16-byte aligned. mla_workspace_bytes depends on it: ask again after a
- * change. Not to be called while calls on the same handle are in progress. */
+ * change. With more than 64 heads, or under a shared prefix, attention may take
+ * 64 consecutive rows of a block relative to the largest scale among them (rows
+ * down to 2^-21 of it are exact, the values of smaller ones off by up to 2^-22
+ * of it) and q_abs in f16, whose entries must then lie within +-65504.
+ * Not to be called while calls on the same handle are in progress. */
 int mla_set_cache_dtype(mla_handle* h, int cache_dtype);
 
 /* Bytes of one block of the cache as the handle's calls take it. */
@@ -459,7 +463,9 @@ uint64_t mla_kernel_launch_count(void);
  * `kernel` is bracketed by records of the two events (cudaEvent_t, created by
  * the caller with timing enabled) on the launch stream, so that
  * cudaEventElapsedTime(start, stop) is that kernel's device time. Names:
- * "attn" (decode attention), "prefill_attn", and the decode weight GEMMs
+ * "attn" (decode attention, one launch or more), "attn_prefix" (the launch that
+ * takes a shared prefix, and with it the sequences' own rows where they ride
+ * along), "prefill_attn", and the decode weight GEMMs
  * "gemm_w1" (down-projection), "gemm_qb" (wq_b), "gemm_uk" (absorption),
  * "gemm_uv" (V extraction), "gemm_o" (o_proj), each including the operand
  * conversion or weight dequantisation it launches, and "v4_qb" (the wq_b GEMM

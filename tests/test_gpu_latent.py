@@ -12,7 +12,7 @@ import head_latent_attention_decode_b200 as mla
 from head_latent_attention_decode_b200 import workloads as wl
 from oracle import latent_ref as lr
 
-from latent_common import ACT, ESZ, Case, check, layer_of, pack_cache, row_values, shape_of
+from latent_common import ACT, ESZ, Case, check, layer_of, pack_cache, row_scales, row_values, shape_of
 
 pytestmark = pytest.mark.gpu
 
@@ -196,6 +196,40 @@ def test_sharp_scores(fp8, prefix):
             case.rows[s[at], :64] = case.q_abs[t, at % 16, :64] * 3
     case.keys = row_values(case.shape, case.rows) if fp8 else case.rows.double().numpy()
     o, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("heads,lens,prefix", [(128, [200, 64, 1], 0), (16, [100, 3, 0], 300), (64, [130, 70], 0)])
+def test_rows_of_much_different_sizes_in_one_tile(heads, lens, prefix):
+    # neighbouring rows 2^-20 to 2^3 of the usual size; below 2^-21 of a tile's largest scale the
+    # values may be off by 2^-22 of it (weights add up to one, so o by no more)
+    case = Case(shape_of(heads, 64), lens, prefix, True, seed=heads)
+    size = np.random.default_rng(heads).integers(-20, 4, (len(case.rows), 1))
+    case.rows[:, :512] *= torch.from_numpy(2.0 ** size).bfloat16()
+    case.keys = row_values(case.shape, case.rows)
+    o, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    wo, wl_, bo, bl = case.oracle()
+    largest = row_scales(case.shape, case.rows[torch.from_numpy(case.used)]).max()
+    check(case, o, lse, want=(wo, wl_, bo + 2.0 ** -22 * largest, bl))
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads", [4, 16, 40, 128])
+def test_a_workspace_covers_every_smaller_call(heads, fp8):
+    layer = layer_of(shape_of(heads, 64), fp8)
+    sizes = [(n, p, c) for n in (1, 3, 40, 300) for p in (0, 1, 500) for c in (1, 100, 9000)]
+    need = {s: mla.mla_prefix_workspace_bytes(layer.handle, *s) for s in sizes}
+    for a in sizes:
+        for b in sizes:
+            if all(x <= y for x, y in zip(a, b)):
+                assert need[a] <= need[b], (a, b)
+    # and is accepted: short rows of a batch that was planned for long ones
+    case = Case(shape_of(heads, 64), [3, 0, 70], 100, fp8, seed=1)
+    x = case.device_inputs()
+    ws = torch.empty(mla.mla_prefix_workspace_bytes(layer.handle, 40, 200, 9000), dtype=torch.uint8, device="cuda")
+    mla.mla_workspace_init(ws)
+    o, lse = torch.empty_like(x["q_abs"]), torch.empty(x["q_abs"].shape[:2], device="cuda")
+    mla.mla_latent_attn(layer.handle, ws=ws, o_lat=o, lse=lse, **x)
     check(case, o, lse)
 
 
@@ -501,6 +535,27 @@ def test_refusals():
     mla.mla_cache_write(h, rows[:0], x["kv_cache"], slots[:0], ws)
     mla.mla_latent_attn(h, **dict(kw, q_abs=x["q_abs"][:0], q_pe=x["q_pe"][:0], block_table=x["block_table"][:0],
                                   context_lens=x["context_lens"][:0]), ws=ws, o_lat=o[:0])
+
+
+def test_a_cache_of_the_other_kind_is_refused():
+    shape = shape_of(16, 64)
+    eight, full = layer_of(shape, True), layer_of(shape, False)
+    c8, c16 = eight.new_cache(4), full.new_cache(4)
+    hidden = torch.zeros(1, shape.hidden, device="cuda").bfloat16()
+    cos, sin = full.rope(torch.zeros(1, dtype=torch.int32, device="cuda"))
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_abs, q_pe = full.decode_qkv(hidden, cos, sin, c16, slot)
+    table, one = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    for layer, cache in ((eight, c16), (full, c8)):
+        for call in (lambda: layer.decode_qkv(hidden, cos, sin, cache, slot),
+                     lambda: layer.decode_attn(q_abs, q_pe, cache, table, one, 1),
+                     lambda: layer.prefill(hidden, cos, sin, kv_cache=cache, slot_mapping=slot),
+                     lambda: layer.latent_attn(q_abs, q_pe, cache, table, one, 1),
+                     lambda: layer.decode_attn_prefix(q_abs, q_pe, cache, table[0], 1, table, one, 1)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        eight.latent_attn(q_abs, q_pe, c8, table, one, 1, prefix_len=1)   # without a table
 
 
 def test_block_bytes():
