@@ -33,6 +33,7 @@ struct MergeSrc {
   int splits, rows;
   int flat;             // entry = (t H + h) / rows; otherwise entry = e0 + t, and head group h / rows
   int e0;
+  const float* corr;   // [units, rows] or NULL: the relative error of copy 0's sums (TcAttnArgs::corr)
 };
 struct MergeArgs {
   MergeSrc src[2];
@@ -117,17 +118,21 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(MergeArgs p) {
       if (v.y > 0.f) M = fmaxf(M, v.x);
     }
     M = fmaxf(warp_max(M), z);
-    float den = 0.f;
+    float den = 0.f, den_l = 0.f;
     for (int i = lane; i < total; i += 32) {
       const float2 v = i == lane ? v0 : stats(i);
       const float w = v.y > 0.f ? __expf(v.x - M) : (v.y != v.y ? v.y : 0.f);   // a NaN sum stays NaN
       wsh[warp][i] = w;
       den += w == 0.f ? 0.f : w * v.y;
+      const float* cr = p.src[i < cnt0 ? 0 : 1].corr;   // the log-sum-exp's own sum: with the score errors taken out
+      if (warp == 0 && p.lse) den_l += w == 0.f ? 0.f : w * v.y * (cr ? 1.f - cr[at(i)] : 1.f);
     }
-    den = warp_sum(den) + (z > -INFINITY ? __expf(z - M) : 0.f);
+    const float sink = z > -INFINITY ? __expf(z - M) : 0.f;
+    den = warp_sum(den) + sink;
+    den_l = warp_sum(den_l) + sink;
     if (lane == 0) {
       inv_sh[warp] = den == 0.f ? 0.f : 1.f / den;
-      if (warp == 0 && p.lse) p.lse[(long long)t * p.H + h] = den == 0.f ? -INFINITY : M + logf(den);
+      if (warp == 0 && p.lse) p.lse[(long long)t * p.H + h] = den == 0.f ? -INFINITY : M + logf(den_l);
     }
   }
   __syncthreads();
@@ -194,7 +199,7 @@ struct LatentPlan {
   int units_p, ents_p;     // few_pre: slices, entries
   int units_h, pre_h;      // head-major: SM pairs, prefix entries
   size_t o, ml, seg, o_h, ml_h, seg_h, total;   // own rows (or few_pre) apart; the head-major launch
-  size_t o_p, ml_p, seg_p;
+  size_t o_p, ml_p, seg_p, corr_h;
 };
 
 // `force` < 0: by the rules; else bit 0 says whether a prefix goes to the head-major kernel and bit 1
@@ -275,6 +280,7 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
     w.o_h = put(rows * 512 * 4);
     w.ml_h = put(rows * 2 * 4 * 2);
     w.seg_h = put(ents * 8);
+    w.corr_h = put(rows * 4);
   }
   w.total = off;
   return w;
@@ -372,13 +378,13 @@ static int pass_few8(const mla_handle* h, const LatentPlan& w, const LatentCall&
   return MLA_OK;
 }
 
-template <bool C8>
+template <bool C8, bool LSE>
 static void launch_heads(const CUtensorMap& m0, const CUtensorMap& m1, const TcAttnArgs& k, const char* timer,
                          cudaStream_t s) {
   static std::atomic<bool> attr[64];
-  set_smem_once(attr, tc_attn_decode_kernel<true, C8>, AttnSmemT<C8>::SIZE);
+  set_smem_once(attr, tc_attn_decode_kernel<true, C8, LSE>, AttnSmemT<C8>::SIZE);
   mla_timer_begin(timer, s);
-  launch_pdl(tc_attn_decode_kernel<true, C8>, 2 * k.units, C8 ? ATT_THREADS8 : ATT_THREADS, AttnSmemT<C8>::SIZE, s, m0, m1,
+  launch_pdl(tc_attn_decode_kernel<true, C8, LSE>, 2 * k.units, C8 ? ATT_THREADS8 : ATT_THREADS, AttnSmemT<C8>::SIZE, s, m0, m1,
              k);
   mla_timer_end(timer, s);
   mla_count_launch(1);
@@ -416,7 +422,9 @@ static int pass_heads(const mla_handle* h, const LatentPlan& w, const LatentCall
   k.flag = flag; k.min_per = 1; k.units = w.units_h;
   k.part_o = (float*)(scratch + w.o_h); k.part_ml = (float*)(scratch + w.ml_h); k.seg = (int2*)(scratch + w.seg_h);
   k.ml_r = (long long)(k.units + k.n) * 128 * 2;
+  k.corr = m->lse ? (float*)(scratch + w.corr_h) : nullptr;
   MergeSrc q{};
+  q.corr = k.corr;
   q.o = k.part_o; q.ml = k.part_ml; q.ml_r = k.ml_r; q.half = 256; q.seg = k.seg; q.rows = 128;
   if (w.heads_pre) {
     q.flat = 1;
@@ -428,8 +436,13 @@ static int pass_heads(const mla_handle* h, const LatentPlan& w, const LatentCall
     m->src[m->n_src++] = q;
   }
   const char* timer = w.heads_pre ? "attn_prefix" : "attn";
-  if (h->cache8) launch_heads<true>(mc, ml, k, timer, s);
-  else launch_heads<false>(mc, ml, k, timer, s);
+  if (h->cache8) {
+    if (k.corr) launch_heads<true, true>(mc, ml, k, timer, s);
+    else launch_heads<true, false>(mc, ml, k, timer, s);
+  } else {
+    if (k.corr) launch_heads<false, true>(mc, ml, k, timer, s);
+    else launch_heads<false, false>(mc, ml, k, timer, s);
+  }
   return MLA_OK;
 }
 

@@ -62,6 +62,7 @@ class MlaLayer:
         self.block_bytes = mla_cache_block_bytes(self.handle)
         self._cache_torch = torch.uint8 if cache_dtype == "fp8" else self.act
         self.ws = None
+        self._graph_ws = []
         self._ws_for = None   # the sizes the workspace was last asked for
 
     def close(self) -> None:
@@ -76,6 +77,12 @@ class MlaLayer:
         if mla_destroy is not None:
             self.close()
 
+    def _held(self, ws: torch.Tensor) -> torch.Tensor:
+        """ws, kept alive with the layer if a graph is being captured (a later call may need a larger one)."""
+        if torch.cuda.is_current_stream_capturing() and all(w is not ws for w in self._graph_ws):
+            self._graph_ws.append(ws)
+        return ws
+
     def workspace(self, max_tokens: int, max_context_len: int = 1) -> torch.Tensor:
         need = mla_workspace_bytes(self.handle, max(1, max_tokens), max(1, max_context_len))
         if self.ws is None or self.ws.numel() < need:
@@ -87,7 +94,7 @@ class MlaLayer:
         """A workspace for latent_attn and decode_attn_prefix (and every other call)."""
         sizes = (max_tokens, max_prefix_len, max_context_len)
         if sizes == self._ws_for:
-            return self.ws
+            return self._held(self.ws)
         need = mla_prefix_workspace_bytes(self.handle, max(1, max_tokens), max(0, max_prefix_len),
                                           max(1, max_context_len))
         if need == 0:
@@ -96,7 +103,7 @@ class MlaLayer:
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             mla_workspace_init(self.ws)
         self._ws_for = sizes   # it only ever grows, so it stays large enough
-        return self.ws
+        return self._held(self.ws)
 
     def new_cache(self, n_blocks: int) -> torch.Tensor:
         """A zeroed paged cache: [n_blocks, 1, block_size, R], or [n_blocks, block bytes] uint8 if 8-bit."""
@@ -127,7 +134,8 @@ class MlaLayer:
         """rows [n, R] into the cache's flat rows slot_mapping (negative: skipped), quantised if it is 8-bit."""
         self._check_rows(rows)
         self._check_cache(kv_cache)
-        mla_cache_write(self.handle, rows, kv_cache, slot_mapping, self.ws if self.ws is not None else self.workspace(1))
+        ws = self._held(self.ws if self.ws is not None else self.workspace(1))
+        mla_cache_write(self.handle, rows, kv_cache, slot_mapping, ws)
         return kv_cache
 
     def cache_read(self, kv_cache, slots, rows=None):
@@ -136,7 +144,8 @@ class MlaLayer:
             rows = torch.zeros((slots.numel(), self.shape.kv_row_dim), dtype=self.act, device=self.device)
         self._check_rows(rows)
         self._check_cache(kv_cache)
-        mla_cache_read(self.handle, kv_cache, slots, rows, self.ws if self.ws is not None else self.workspace(1))
+        ws = self._held(self.ws if self.ws is not None else self.workspace(1))
+        mla_cache_read(self.handle, kv_cache, slots, rows, ws)
         return rows
 
     def _check_prefix(self, prefix_table, prefix_len):

@@ -213,6 +213,82 @@ def test_rows_of_much_different_sizes_in_one_tile(heads, lens, prefix):
     check(case, o, lse, want=(wo, wl_, bo + 2.0 ** -22 * largest, bl))
 
 
+@pytest.mark.parametrize("heads,lens,prefix,fp8", [(128, [700, 300, 64, 130], 0, True), (16, [100, 7, 0], 900, True),
+                                                   (128, [200, 30], 400, False), (16, [64, 1, 90], 900, False)])
+def test_the_lse_is_good_to_fp32(heads, lens, prefix, fp8):
+    # Half of each score crosses between two CTAs in f16, off by d <= 2^-12 |half| scale, about 2^-12 4 =
+    # 2^-10 here. The sums take that out to first order: d^2 / 2 = 2^-21 is left, and the weights'
+    # own rounding times d, 2^-18 a key with either sign, over a hundred keys and more below 2^-21.
+    # Together with the fp32 sums 2e-6 of an lse of about 6 at most; with the first order left in, 3e-5.
+    case = Case(shape_of(heads, 64), lens, prefix, fp8, seed=17)
+    size = 2.0 ** np.floor(np.log2(np.abs(case.rows[:, :512].float().numpy()).mean(1, keepdims=True) + 1e-30))
+    size[~np.isfinite(size)] = 1.0
+    case.rows[:, :512] /= torch.from_numpy(size).bfloat16()   # rows of one size, as a norm leaves them
+    case.keys = row_values(case.shape, case.rows) if fp8 else case.rows.double().numpy()
+    _, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    _, want, _, _ = case.oracle()
+    got, keep = lse.double().cpu().numpy(), np.isfinite(want)
+    assert (np.isfinite(got) == keep).all()
+    assert np.linalg.norm(got[keep] - want[keep]) <= 2e-6 * np.linalg.norm(want[keep])
+
+
+@pytest.mark.parametrize("heads,bs,lens,prefix,fp8", [
+    (16, 16, [1 + i % 3 for i in range(800)], 0, True), (128, 64, [1 + i % 2 for i in range(300)], 0, True),
+    (16, 64, [i % 3 for i in range(300)], 70, True), (16, 64, [i % 3 for i in range(300)], 70, False),
+    (130, 64, [70, 3], 0, True), (130, 64, [70, 0], 100, True), (130, 64, [70, 0], 100, False),
+], ids=["few_800", "heads_300", "prefix8_300", "prefix16_300", "130_heads", "prefix8_130_heads", "prefix16_130_heads"])
+def test_more_tokens_than_a_pass_takes_and_more_heads_than_a_tile(heads, bs, lens, prefix, fp8):
+    case = Case(shape_of(heads, bs), lens, prefix, fp8, seed=len(lens) + heads)
+    layer = case.layer()
+    o, lse = layer.latent_attn(want_lse=True, **case.device_inputs())
+    assert mla.mla_read_device_flag(layer.ws) == 0
+    check(case, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_blocks_beyond_four_gigabytes(heads, fp8):
+    case = Case(shape_of(heads, 64), [100, 64, 3], 130, fp8, seed=5)
+    layer = case.layer()
+    x = case.device_inputs()
+    want, wl_ = layer.latent_attn(want_lse=True, **x)
+    many = (1 << 32) // layer.block_bytes + 100
+    big = layer.new_cache(many)
+    at = many - case.n_blocks
+    big[at:] = x["kv_cache"]
+    move = lambda t: torch.where(t >= 0, t + at, t)  # noqa: E731
+    o, lse = layer.latent_attn(want_lse=True, **dict(x, kv_cache=big, block_table=move(x["block_table"]),
+                                                     prefix_table=move(x["prefix_table"])))
+    assert mla.mla_read_device_flag(layer.ws) == 0
+    assert same_bytes(o, want) and same_bytes(lse, wl_)
+    # its last rows, written and read
+    rows = case.rows[torch.from_numpy(case.used[:50])].cuda()
+    slots = torch.arange(many * 64 - 50, many * 64, dtype=torch.int32, device="cuda")
+    layer.cache_write(rows, big, slots)
+    small = layer.new_cache(1)
+    low = torch.arange(14, 64, dtype=torch.int32, device="cuda")
+    layer.cache_write(rows, small, low)
+    assert same_bytes(layer.cache_read(big, slots), layer.cache_read(small, low))
+
+
+def test_a_graph_keeps_its_workspace_when_the_layer_needs_a_larger_one():
+    case = Case(shape_of(16, 64), [30, 64], 40, True, seed=3)
+    layer = case.layer()
+    x = case.device_inputs()
+    want, _ = layer.latent_attn(**x)
+    o, g = torch.empty_like(want), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.latent_attn(o_lat=o, **x)
+    held = layer.ws.data_ptr()
+    layer.prefix_workspace(500, 4000, 4000)
+    assert layer.ws.data_ptr() != held
+    junk = [torch.full((layer.ws.numel() // 64,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert same_bytes(o, want) and all(bool((j == 255).all()) for j in junk)
+
+
 @pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
 @pytest.mark.parametrize("heads", [4, 16, 40, 128])
 def test_a_workspace_covers_every_smaller_call(heads, fp8):
