@@ -580,7 +580,7 @@ int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
   if (n == 0) return MLA_OK;
   if (!q_abs || !q_pe || !kv_cache || !block_table || !context_lens || !out || !ws) return MLA_ERR_INVALID_ARG;
   if (max_context_len < 1 || max_blocks_per_seq < 1) return MLA_ERR_INVALID_ARG;
-  if (h->cache8 && (uintptr_t)kv_cache % 16) return MLA_ERR_INVALID_ARG;
+  if (h->cache8 && ((uintptr_t)kv_cache % 16 || (uintptr_t)ws % 16)) return MLA_ERR_INVALID_ARG;
   const WsLayout W = make_ws(h, n, max_context_len);
   if (ws_bytes < W.dec_total) return MLA_ERR_WORKSPACE;
   const LatentCall call{q_abs, q_pe, kv_cache, n_blocks, nullptr, 0, block_table, max_blocks_per_seq,
@@ -616,7 +616,8 @@ static int cache_rows(mla_handle* h, const void* rows, int n, const void* kv_cac
                       const int32_t* slots, void* ws, size_t ws_bytes, void* stream, bool write) {
   if (!h || n < 0 || n_blocks < 0) return MLA_ERR_INVALID_ARG;
   if (n == 0) return MLA_OK;
-  if (!rows || !kv_cache || !slots || !ws || (uintptr_t)rows % 16 || (uintptr_t)kv_cache % 16) return MLA_ERR_INVALID_ARG;
+  if (!rows || !kv_cache || !slots || !ws || (uintptr_t)rows % 16 || (uintptr_t)kv_cache % 16 || (uintptr_t)ws % 4)
+    return MLA_ERR_INVALID_ARG;
   if (ws_bytes < 256) return MLA_ERR_WORKSPACE;
   if (!on_device(h)) return MLA_ERR_INVALID_ARG;
   const mla_config* c = &h->cfg;
@@ -664,7 +665,7 @@ static int latent_check(mla_handle* h, const LatentCall& a, const void* out, con
   if (a.max_ctx < 1 || a.mbps < 1 || a.prefix_len < 0 || (a.prefix_len > 0) != (a.prefix_table != nullptr))
     return MLA_ERR_INVALID_ARG;
   if ((long long)a.prefix_len + a.max_ctx > (1 << 30)) return MLA_ERR_UNSUPPORTED;
-  if ((uintptr_t)a.cache % 16 || !on_device(h)) return MLA_ERR_INVALID_ARG;
+  if ((uintptr_t)a.cache % 16 || (uintptr_t)ws % 16 || !on_device(h)) return MLA_ERR_INVALID_ARG;
   *W = make_ws(h, a.n, a.max_ctx);
   if (ws_bytes < W->total + latent_ws_bytes(h, a.n, a.prefix_len, a.max_ctx)) return MLA_ERR_WORKSPACE;
   return MLA_OK;

@@ -640,3 +640,52 @@ def test_block_bytes():
         _, _, size = lr.block_layout(shape.block_size, shape.kv_lora_rank, shape.qk_rope, ESZ[act])
         assert mla.mla_cache_block_bytes(layer_of(shape, True).handle) == size
         assert mla.mla_cache_block_bytes(layer_of(shape, False).handle) == shape.block_size * shape.kv_row_dim * ESZ[act]
+
+
+# ---------------------------------------------------------------------------
+# workspaces at any 16-byte boundary
+# ---------------------------------------------------------------------------
+
+def workspace_at(nbytes, offset):
+    """A zeroed workspace `offset` bytes past a 256-byte boundary."""
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device="cuda")[offset:offset + nbytes]
+    assert ws.data_ptr() % 256 == offset
+    mla.mla_workspace_init(ws)
+    return ws
+
+
+@pytest.mark.parametrize("offset", [16, 48])
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads,prefix", [(16, 0), (16, 100), (40, 0), (128, 0), (128, 100)])
+def test_a_workspace_at_a_16_byte_boundary(heads, prefix, fp8, offset):
+    case = Case(shape_of(heads, 64), [70, 3, 130], prefix, fp8, seed=heads)
+    layer = case.layer()
+    x = case.device_inputs()
+    want, wl_ = layer.latent_attn(want_lse=True, **x)
+    ws = workspace_at(mla.mla_prefix_workspace_bytes(layer.handle, 3, prefix, 130), offset)
+    o, lse = torch.empty_like(want), torch.empty_like(wl_)
+    mla.mla_latent_attn(layer.handle, ws=ws, o_lat=o, lse=lse, **x)
+    assert same_bytes(o, want) and same_bytes(lse, wl_)
+    if not prefix:   # the call that was there before
+        args = [x[k] for k in ("q_abs", "q_pe", "kv_cache", "block_table", "context_lens", "max_context_len")]
+        out = torch.empty(3, case.shape.hidden, dtype=torch.bfloat16, device="cuda")
+        ws = workspace_at(mla.mla_workspace_bytes(layer.handle, 3, 130), offset)
+        mla.mla_decode_attn(layer.handle, *args, out, ws)
+        assert same_bytes(out, layer.decode_attn(*args))
+
+
+def test_other_alignments_of_a_workspace_are_refused():
+    case = Case(shape_of(16, 64), [10, 20], 30, True, seed=0)
+    layer = case.layer()
+    x = case.device_inputs()
+    o = torch.empty_like(x["q_abs"])
+    need = mla.mla_prefix_workspace_bytes(layer.handle, 2, 30, 20)
+    ws = torch.zeros(need + 8, dtype=torch.uint8, device="cuda")[8:]
+    args = [x[k] for k in ("q_abs", "q_pe", "kv_cache", "block_table", "context_lens", "max_context_len")]
+    rows, slots = torch.zeros(1, 576, device="cuda").bfloat16(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in (lambda: mla.mla_latent_attn(layer.handle, ws=ws, o_lat=o, **x),
+                 lambda: mla.mla_decode_attn(layer.handle, *args, torch.empty(2, 256, device="cuda").bfloat16(), ws),
+                 lambda: mla.mla_cache_write(layer.handle, rows, x["kv_cache"], slots, ws[1:])):
+        with pytest.raises(mla.MlaError) as e:
+            call()
+        assert e.value.status == mla.MLA_ERR_INVALID_ARG
