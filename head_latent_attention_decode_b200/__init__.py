@@ -395,6 +395,11 @@ def mla_decode_attn_prefix(handle, q_abs, q_pe, kv_cache, prefix_table, prefix_l
     """mla_decode_attn over a prefix shared by the batch followed by each sequence's own rows."""
     dev = _check_latent("mla_decode_attn_prefix", q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table,
                         context_lens, (("out", out), ("head_out", head_out), ("ws", ws)))
+    n, dtype = q_abs.shape[0], q_abs.dtype
+    if out.dim() != 2 or out.shape[0] != n or out.dtype is not dtype:
+        raise ValueError("mla_decode_attn_prefix: out must be [n, D] of the query's dtype")
+    if head_out is not None and (head_out.dim() != 3 or head_out.shape[:2] != q_abs.shape[:2] or head_out.dtype is not dtype):
+        raise ValueError("mla_decode_attn_prefix: head_out must be [n, H, d_v] of the query's dtype")
     _check(lib().mla_decode_attn_prefix(handle, q_abs.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(),
                                         kv_cache.shape[0], prefix_table.data_ptr() if prefix_len else None, prefix_len,
                                         block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),

@@ -152,9 +152,23 @@ class MlaLayer:
         if prefix_len and (prefix_table is None or prefix_table.numel() * self.shape.block_size < prefix_len):
             raise ValueError("prefix_table does not cover prefix_len rows")
 
+    def _check_query(self, q_abs, q_pe):
+        s, n = self.shape, q_abs.shape[0]
+        if (q_abs.shape != (n, s.n_heads, s.kv_lora_rank) or q_pe.shape != (n, s.n_heads, s.qk_rope)
+                or q_abs.dtype is not self.act or q_pe.dtype is not self.act):
+            raise ValueError(f"q_abs must be [n, {s.n_heads}, {s.kv_lora_rank}] and q_pe [n, {s.n_heads}, {s.qk_rope}], {self.act}")
+
+    def _check_out(self, n, out, head_out):
+        s = self.shape
+        if out.shape != (n, s.hidden) or out.dtype is not self.act:
+            raise ValueError(f"out must be [{n}, {s.hidden}] {self.act}")
+        if head_out is not None and (head_out.shape != (n, s.n_heads, s.v_dim) or head_out.dtype is not self.act):
+            raise ValueError(f"head_out must be [{n}, {s.n_heads}, {s.v_dim}] {self.act}")
+
     def latent_attn(self, q_abs, q_pe, kv_cache, block_table, context_lens, max_context_len, prefix_table=None,
                     prefix_len: int = 0, o_lat=None, want_lse: bool = False):
         """(o_lat [n, H, r_kv], lse [n, H] fp32 or None) over the batch's shared prefix and each sequence's own rows."""
+        self._check_query(q_abs, q_pe)
         self._check_cache(kv_cache)
         self._check_prefix(prefix_table, prefix_len)
         if o_lat is None:
@@ -168,10 +182,12 @@ class MlaLayer:
     def decode_attn_prefix(self, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table, context_lens,
                            max_context_len, out=None, head_out=None):
         """decode_attn over a prefix shared by the batch (its blocks in prefix_table) and each sequence's own rows."""
+        self._check_query(q_abs, q_pe)
         self._check_cache(kv_cache)
         self._check_prefix(prefix_table, prefix_len)
         if out is None:
             out = torch.empty((q_abs.shape[0], self.shape.hidden), dtype=self.act, device=self.device)
+        self._check_out(q_abs.shape[0], out, head_out)
         ws = self.prefix_workspace(q_abs.shape[0], prefix_len, max_context_len)
         mla_decode_attn_prefix(self.handle, q_abs, q_pe, kv_cache, prefix_table, prefix_len, block_table,
                                context_lens, max_context_len, out, ws, head_out=head_out)

@@ -689,3 +689,39 @@ def test_other_alignments_of_a_workspace_are_refused():
         with pytest.raises(mla.MlaError) as e:
             call()
         assert e.value.status == mla.MLA_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------------------
+# queries and outputs of another layer's shape or type
+# ---------------------------------------------------------------------------
+
+def test_queries_and_outputs_of_another_shape_or_type_are_refused():
+    case = Case(shape_of(16, 64), [10, 20], 30, True, seed=0)
+    layer, x = case.layer(), case.device_inputs()
+    qa, qp = x["q_abs"], x["q_pe"]
+    prefix = (x.pop("prefix_table"), x.pop("prefix_len"))
+    rest = [x[k] for k in ("block_table", "context_lens", "max_context_len")]
+    queries = [(qa[:, :8], qp[:, :8]), (qa[..., :256], qp), (qa, qp[..., :32]), (qa.float(), qp.float()),
+               (qa.half(), qp.half()), (qa, qp.float()), (qa.flatten(1), qp.flatten(1)), (qa, qp[:1])]
+    for a, b in queries:
+        a, b = a.contiguous(), b.contiguous()
+        with pytest.raises(ValueError):
+            layer.latent_attn(a, b, x["kv_cache"], *rest, prefix_table=prefix[0], prefix_len=prefix[1])
+        with pytest.raises(ValueError):
+            layer.decode_attn_prefix(a, b, x["kv_cache"], *prefix, *rest)
+    bf = dict(device="cuda", dtype=torch.bfloat16)
+    hidden, heads, dv = case.shape.hidden, case.shape.n_heads, case.shape.v_dim
+    for bad in (dict(out=torch.empty(2, hidden // 2, **bf)), dict(out=torch.empty(1, hidden, **bf)),
+                dict(out=torch.empty(2, hidden, device="cuda")), dict(head_out=torch.empty(2, heads // 2, dv, **bf)),
+                dict(head_out=torch.empty(2, heads, dv // 2, **bf)), dict(head_out=torch.empty(1, heads, dv, **bf)),
+                dict(head_out=torch.empty(2, heads, dv, device="cuda"))):
+        with pytest.raises(ValueError):
+            layer.decode_attn_prefix(qa, qp, x["kv_cache"], *prefix, *rest, **bad)
+    # the binding, which does not know the layer, compares them with the query
+    ws, out = layer.prefix_workspace(2, 30, 20), torch.empty(2, hidden, **bf)
+    for bad in (dict(out=out[:1]), dict(out=out.float()), dict(head_out=torch.empty(2, 8, dv, **bf)),
+                dict(head_out=torch.empty(2, heads, dv, device="cuda"))):
+        kw = dict(out=out, head_out=None)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            mla.mla_decode_attn_prefix(layer.handle, qa, qp, x["kv_cache"], *prefix, *rest, kw["out"], ws, head_out=kw["head_out"])

@@ -115,3 +115,21 @@ def test_new_dtype_is_no_weight_or_activation_type(lib):
     c.act_dtype = mla.MLA_FP8_E4M3_ROW
     assert mla.mla_weights_bytes(c) == 0
     assert ctypes.sizeof(mla.mla_config) == 15 * 4
+
+
+def test_the_layer_refuses_queries_and_outputs_of_another_shape_or_type():
+    from types import SimpleNamespace
+    from head_latent_attention_decode_b200.layer import MlaLayer
+    layer = MlaLayer.__new__(MlaLayer)   # the checks read the shape and the type alone
+    layer.shape, layer.act = SimpleNamespace(n_heads=4, kv_lora_rank=64, qk_rope=16, hidden=32, v_dim=8), torch.bfloat16
+    q, p = torch.zeros(2, 4, 64).bfloat16(), torch.zeros(2, 4, 16).bfloat16()
+    layer._check_query(q, p)
+    for a, b in ((q[:, :2], p[:, :2]), (q[..., :32], p), (q, p[..., :8]), (q, p[:1]), (q.float(), p.float()), (q.flatten(1), p)):
+        with pytest.raises(ValueError):
+            layer._check_query(a, b)
+    out, head = torch.zeros(2, 32).bfloat16(), torch.zeros(2, 4, 8).bfloat16()
+    layer._check_out(2, out, None)
+    layer._check_out(2, out, head)
+    for a, b in ((out[:1], None), (out[:, :16], None), (out.float(), None), (out, head[:1]), (out, head[..., :4]), (out, head.float())):
+        with pytest.raises(ValueError):
+            layer._check_out(2, a, b)
