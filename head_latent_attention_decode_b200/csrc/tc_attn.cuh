@@ -879,18 +879,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(C8 ? ATT_THREADS8 : 
         tc_fence_after();
         float* po = a.part_o + (unit * rows_u + h) * 512 + r * 256 + 128 * g;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {   // whole sectors, 32 bytes of a row per store, where the caller's workspace is so aligned
+        for (int k = 0; k < 4; ++k) {   // whole sectors: 32 bytes of a row per store
           uint32_t o[32];
           tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 32 * k, o);
           tmem_ld16(tmem + ATT_TM_O + lane_base + 128 * g + 32 * k + 16, o + 16);
           tmem_ld_wait<32>(o);
-          if (store && ((uintptr_t)a.part_o & 31) == 0) {
+          if (store) {
 #pragma unroll
             for (int jj = 0; jj < 32; jj += 8) st_global_8(po + 32 * k + jj, o + jj);
-          } else if (store) {
-#pragma unroll
-            for (int jj = 0; jj < 32; jj += 4)
-              *reinterpret_cast<uint4*>(po + 32 * k + jj) = make_uint4(o[jj], o[jj + 1], o[jj + 2], o[jj + 3]);
           }
         }
         tc_fence_before();
