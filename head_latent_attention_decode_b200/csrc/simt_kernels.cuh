@@ -462,12 +462,12 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const float* part_o, 
     for (int s = threadIdx.x & 31; s < used; s += 32) {
       const long long base = ((long long)t * n_splits + s) * H + h;
       const float l = ml[base * 2 + 1];
-      const float w = (l > 0.f) ? __expf(ml[base * 2] - M) : 0.f;
+      const float w = (l > 0.f) ? __expf(ml[base * 2] - M) : (l != l ? l : 0.f);   // a NaN sum stays NaN
       if (s < 64) wsh[warp][s] = w;
-      den += w * l;
+      den += w == 0.f ? 0.f : w * l;
     }
     den = warp_sum(den);
-    if ((threadIdx.x & 31) == 0) inv_sh[warp] = den > 0.f ? 1.f / den : 0.f;
+    if ((threadIdx.x & 31) == 0) inv_sh[warp] = den == 0.f ? 0.f : 1.f / den;
   }
   __syncthreads();
   const int c = threadIdx.x * 4;

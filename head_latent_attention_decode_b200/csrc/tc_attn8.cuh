@@ -663,16 +663,16 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
       const int live = (int)min(16LL, a.flat ? a.rows_total - 16LL * tile.w : (long long)a.H - 16 * hg);
       if (lane < 16) {
         const float Ro = first ? -INFINITY : rp_s[((i - 1) & 3) * 16 + lane], Rc = fmaxf(R, Ro);
-        const float fa = R == -INFINITY ? 0.f : ex2_approx(R - Rc), fb = Ro == -INFINITY ? 0.f : ex2_approx(Ro - Rc);
+        const float* ra = rl + (i & 3) * 64 + lane;
+        const float* rb = rl + ((i - 1) & 3) * 64 + lane;
+        const float sa = ra[0] + ra[16] + ra[32] + ra[48], sb = first ? 0.f : rb[0] + rb[16] + rb[32] + rb[48];
+        // a set without a reference has no keys of any weight (a sum of zero), or NaN scores alone (a NaN sum)
+        const float fa = R == -INFINITY ? sa : ex2_approx(R - Rc), fb = Ro == -INFINITY ? sb : ex2_approx(Ro - Rc);
         ref_w[lane] = fa;
         al_w[lane] = fb;
-        if (q == 0 && lane < live) {   // natural-log units; the weights carry the factor 2^8
-          const float* ra = rl + (i & 3) * 64 + lane;
-          const float* rb = rl + ((i - 1) & 3) * 64 + lane;
-          float sum = fa > 0.f ? fa * (ra[0] + ra[16] + ra[32] + ra[48]) : 0.f;
-          if (fb > 0.f) sum += fb * (rb[0] + rb[16] + rb[32] + rb[48]);
-          *reinterpret_cast<float2*>(a.part_ml + (unit * 16 + lane) * 2) = make_float2((Rc - 8.f) * 0.69314718055994531f, sum);
-        }
+        if (q == 0 && lane < live)   // natural-log units; the weights carry the factor 2^8
+          *reinterpret_cast<float2*>(a.part_ml + (unit * 16 + lane) * 2) =
+              make_float2((Rc - 8.f) * 0.69314718055994531f, (fa != 0.f ? fa * sa : 0.f) + (fb != 0.f ? fb * sb : 0.f));
       }
       __syncwarp();
       if (!mbar_poll_warp(p_free + 8 * set, (i >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
           for (int h = 0; h < 16; ++h) {
             const float fa = ref_w[h], fb = al_w[h];
             const float ob = __uint_as_float(o[16 * (h >> 3) + (h & 7)]) + __uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]);
-            out[h] = (fa > 0.f ? fa * out[h] : 0.f) + (fb > 0.f ? fb * ob : 0.f);
+            out[h] = (fa != 0.f ? fa * out[h] : 0.f) + (fb != 0.f ? fb * ob : 0.f);
           }
         }
 #pragma unroll

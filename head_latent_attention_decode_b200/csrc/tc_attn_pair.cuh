@@ -389,7 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
       const int col = i & 63;
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        const float p = (valid && m_ref[h] != -INFINITY) ? ex2_approx(fmaf(cur[h], a.scale_log2, -m_ref[h])) : 0.f;
+        // no reference yet: scores of -inf, weight 0, or NaN, which stay visible
+        const float p = valid ? ex2_approx(fmaf(cur[h], a.scale_log2, m_ref[h] == -INFINITY ? 0.f : -m_ref[h])) : 0.f;
         const bf16 pb = __float2bfloat16_rn(p);
         l_part[h] = l_part[h] * alpha[h] + __bfloat162float(pb);
         *reinterpret_cast<bf16*>(pbuf + h * 128 + ((((col >> 3) ^ (h & 7))) << 4) + (col & 7) * 2) = pb;

@@ -326,6 +326,7 @@ size_t mla_prefix_workspace_bytes(const mla_handle* h, int max_tokens, int max_p
  *                  length is invalid attends to nothing: o_lat 0, lse -inf (the
  *                  sink's, if any), and MLA_FLAG_BAD_CONTEXT. A block id out of
  *                  range sets MLA_FLAG_BAD_BLOCK and its rows are left out
+ *                  A NaN or +infinite score makes its head's o_lat and lse NaN
  * o_lat            device [n, H, r_kv] act dtype
  * lse              device [n, H] fp32, or NULL
  * ws               device workspace of mla_prefix_workspace_bytes(h, n,

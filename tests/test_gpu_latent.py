@@ -725,3 +725,91 @@ def test_queries_and_outputs_of_another_shape_or_type_are_refused():
         kw.update(bad)
         with pytest.raises(ValueError):
             mla.mla_decode_attn_prefix(layer.handle, qa, qp, x["kv_cache"], *prefix, *rest, kw["out"], ws, head_out=kw["head_out"])
+
+
+# ---------------------------------------------------------------------------
+# NaN and infinite scores
+# ---------------------------------------------------------------------------
+
+def dead_and_alive(case, layer, x, want, dead, lse=True):
+    """The (sequence, head) pairs of `dead` give NaN, the others what they gave without it."""
+    o, s = layer.latent_attn(want_lse=lse, **x)
+    o, wo, wl_, bo, bl = o.double().cpu().numpy(), *want
+    assert np.isnan(o[dead]).all()
+    assert (np.abs(o - wo) <= bo)[~dead].all()
+    if lse:
+        s = s.double().cpu().numpy()
+        assert np.isnan(s[dead]).all() and (np.abs(s - wl_) <= bl)[~dead].all()
+    assert mla.mla_read_device_flag(layer.ws) == 0
+
+
+NAN_ROUTES = [(16, 64, 0, True), (16, 64, 0, False), (16, 16, 0, True), (40, 64, 0, True), (40, 64, 0, False),
+              (128, 64, 0, True), (128, 64, 0, False), (130, 64, 0, True), (16, 64, 70, True), (16, 64, 70, False),
+              (4, 24, 0, True), (4, 24, 0, False)]
+
+
+@pytest.mark.parametrize("last", [1, 65, 129, 257, 300])
+@pytest.mark.parametrize("heads,bs,prefix,fp8", NAN_ROUTES)
+def test_a_nan_in_the_newest_row_stays_visible(heads, bs, prefix, fp8, last):
+    # alone in its tile for most lengths, so that no finite score stands beside it
+    case = Case(shape_of(heads, bs), [last, 200, last], prefix, fp8, seed=last)
+    want = case.oracle()
+    case.rows[case.key_slots(0)[-1], 5] = float("nan")
+    dead = np.zeros((3, heads), bool)
+    dead[0] = True
+    dead_and_alive(case, case.layer(), case.device_inputs(), want, dead)
+
+
+@pytest.mark.parametrize("heads,n", [(4, 3), (16, 2), (16, 5), (128, 2)])
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+def test_a_nan_in_the_last_row_of_a_prefix_stays_visible(heads, n, fp8):
+    case = Case(shape_of(heads, 64), [3, 0, 70, 5, 0][:n], 129, fp8, seed=n)
+    want = case.oracle()
+    case.rows[case.key_slots(0)[128], 5] = float("nan")
+    dead_and_alive(case, case.layer(), case.device_inputs(), want, np.ones((n, heads), bool))
+
+
+@pytest.mark.parametrize("heads,bs,prefix,fp8", NAN_ROUTES)
+def test_a_nan_in_a_query_head_spoils_that_head_alone(heads, bs, prefix, fp8):
+    case = Case(shape_of(heads, bs), [1, 300, 129], prefix, fp8, seed=heads)
+    want = case.oracle()
+    x = case.device_inputs()
+    dead = np.zeros((3, heads), bool)
+    for t, h, c in ((0, heads - 1, 3), (1, 1, 300), (2, 0, 511)):
+        x["q_abs"][t, h, c] = float("nan")
+        dead[t, h] = True
+    dead_and_alive(case, case.layer(), x, want, dead)
+
+
+@pytest.mark.parametrize("heads,bs,prefix,fp8", NAN_ROUTES)
+def test_infinite_rotary_keys(heads, bs, prefix, fp8):
+    # score +inf where the query's entry is positive (NaN out), -inf where it is negative (the key has no weight)
+    case = Case(shape_of(heads, bs), [129, 40, 1], prefix, fp8, seed=heads + 1)
+    slots_of = [case.key_slots(t) for t in range(3)]
+    slots, at = case.key_slots, {0: prefix + 128, 1: prefix + 7}
+    case.lens, case.key_slots = [128, 39, 1], lambda t: np.delete(slots_of[t], at[t]) if t in at else slots_of[t]
+    want = case.oracle()   # without those keys
+    case.lens, case.key_slots = [129, 40, 1], slots
+    for t, j in at.items():
+        case.rows[slots_of[t][j], case.shape.kv_lora_rank + 2] = float("inf")
+    dead = case.q_pe[:, :, 2].double().numpy() > 0
+    dead[2] = False
+    dead_and_alive(case, case.layer(), case.device_inputs(), want, dead, lse=False)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "plain"])
+@pytest.mark.parametrize("heads", [16, 40])
+def test_decode_attn_shows_a_nan_too(heads, fp8, act):
+    small = dict(r_kv=64, d_r=16) if act == "f32" else {}
+    case = Case(shape_of(heads, 64, act=act, **small), [3000, 200, 2049], 0, fp8, seed=heads)
+    layer, x = case.layer(), case.device_inputs()
+    args = lambda x: [x[k] for k in ("q_abs", "q_pe", "kv_cache", "block_table", "context_lens", "max_context_len")]  # noqa: E731
+    head = torch.empty(3, heads, case.shape.v_dim, dtype=ACT[act], device="cuda")
+    want = layer.decode_attn(*args(x), head_out=head)
+    whole = head.clone()
+    for t in (0, 2):   # among 951 other rows of its split, and alone in its tile
+        case.rows[case.key_slots(t)[-1], 5] = float("nan")
+    out = layer.decode_attn(*args(case.device_inputs()), head_out=head)
+    assert torch.isnan(head[0::2]).all() and torch.isnan(out[0::2]).all()
+    assert same_bytes(head[1], whole[1]) and same_bytes(out[1], want[1])
