@@ -202,9 +202,9 @@ struct LatentPlan {
   size_t o_p, ml_p, seg_p, corr_h;
 };
 
-// `force` < 0: by the rules; else bit 0 says whether a prefix goes to the head-major kernel and bit 1
-// whether the own rows ride along, as a smaller call may have it (latent_ws_bytes).
-static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned,
+// `lse`: the log-sum-exp is wanted. `force` < 0: by the rules; else bit 0 says whether a prefix goes to the
+// head-major kernel and bit 1 whether the own rows ride along, as a smaller call may have it (latent_ws_bytes).
+static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned, bool lse,
                                      int force = -1) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads;
@@ -230,8 +230,10 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
     w.heads_own = b64 && H <= 128 && (H > 64 || (w.heads_pre && ride));
     w.few_own = !w.heads_own;
   } else if (tc && !h->cache8 && b64 && H <= 128) {
+    // Beyond 32 heads only the head-major form of this file has the log-sum-exp good to fp32
+    // (TcAttnArgs::corr); up to 32 the kernel of mla_decode_attn has a form for it.
     w.heads_pre = pre;
-    w.heads_own = pre && (H > 32 || ride);
+    w.heads_own = H > 32 ? pre || lse : pre && ride;
     w.own16 = !w.heads_own;
   } else {
     w.simt = true;
@@ -291,8 +293,8 @@ static inline size_t latent_ws_bytes(const mla_handle* h, long long n, int prefi
   size_t most = 0;
   for (int p = 0; p < (prefix_len > 0 ? 2 : 1); ++p)
     for (int force = 0; force < 4; ++force)
-      for (int aligned = 0; aligned < 2; ++aligned) {
-        const size_t t = latent_plan(h, n, p ? prefix_len : 0, max_ctx, aligned != 0, force).total;
+      for (int k = 0; k < 4; ++k) {
+        const size_t t = latent_plan(h, n, p ? prefix_len : 0, max_ctx, (k & 1) != 0, (k & 2) != 0, force).total;
         if (t > most) most = t;
       }
   return most;
@@ -453,7 +455,7 @@ static int pass_own16(const mla_handle* h, const LatentPlan& w, const LatentCall
   float* part_o = (float*)(scratch + w.o);
   float* part_ml = (float*)(scratch + w.ml);
   const int st = tc_attention_launch(h, a.q_abs, a.q_pe, a.cache, a.n_blocks, a.table, a.mbps, a.ctx, a.max_ctx, a.n,
-                                     part_o, part_ml, w.splits, flag, (int*)(scratch + w.seg), a.prefix_len > 0, &P, s);
+                                     part_o, part_ml, w.splits, flag, (int*)(scratch + w.seg), a.prefix_len > 0, m->lse != nullptr, &P, s);
   if (st != MLA_OK) return st;
   MergeSrc& q = m->src[m->n_src++];
   q.o = part_o; q.ml = part_ml; q.ml_r = P.ml_r; q.half = P.half_cols; q.nseg = P.seg_counts; q.splits = P.splits;
@@ -499,7 +501,7 @@ static inline int latent_core(const mla_handle* h, const LatentCall& call, void*
   const int H = c.n_heads, rkv = c.kv_lora_rank, dr = c.qk_rope;
   const size_t esz = c.act_dtype == MLA_F32 ? 4 : 2, o_esz = o_dt == 0 ? 4 : 2;
   const bool aligned = (((uintptr_t)call.q_abs | (uintptr_t)call.q_pe) & 15) == 0;
-  const LatentPlan w = latent_plan(h, call.n, call.prefix_len, call.max_ctx, aligned);
+  const LatentPlan w = latent_plan(h, call.n, call.prefix_len, call.max_ctx, aligned, lse != nullptr);
   for (int t = 0; t < call.n; t += w.chunk) {
     LatentCall a = call;
     a.n = call.n - t < w.chunk ? call.n - t : w.chunk;

@@ -16,6 +16,9 @@
 //   exchange) and O^T rescaled; per-row partial sums are reduced once at the
 //   end. Both CTAs add the same two partials, each its own in fp32 and the
 //   peer's in f16, so their P^T agree to the f16 rounding of a partial score
+//   (LSE, where the log-sum-exp is wanted: the partials cross in fp32 and the
+//   row sums take the weights before their rounding to bf16, so that it is good
+//   to fp32)
 //   O_r^T += V_r^T . P^T                 2 x (M 128 latent x N NH, K 128 rows),
 //                                        V^T read MN-major from the same tile
 // A CTA keeps 64 KB of a tile until its P.V (half of what one CTA holding the
@@ -28,12 +31,12 @@
 namespace mla {
 namespace tc {
 
-template <int NH>
+template <int NH, bool LSE = false>
 struct AttnPairSmem {
   // ring entries: [128 rows x 128 latent] bf16, 32 KB, laid out [16 row octets][2 k-blocks][8 rows][128 B]
   static constexpr int NPR = NH <= 16 ? 5 : 4;
   static constexpr int QKB = NH * 128;                   // one [NH x 64] bf16 k-block of Q or P^T
-  static constexpr int XB = 128 * NH * 2;                // one [128 x NH] f16 partial S^T
+  static constexpr int XB = 128 * NH * (LSE ? 4 : 2);    // one [128 x NH] partial S^T, f16 or fp32
   static constexpr int RING_OFF = 0;
   static constexpr int ROPE_OFF = NPR * 32768;           // [128 x 64] rotary block of the current tile
   static constexpr int Q_OFF = ROPE_OFF + 16384;         // this CTA's 4 latent k-blocks of Q, then q_pe
@@ -43,18 +46,20 @@ struct AttnPairSmem {
   static constexpr int BAR_OFF = RED_OFF + 2 * 4 * NH * 4;
   static constexpr int SIZE = 1024 + BAR_OFF + 512;
   static constexpr int TMEM_COLS = 4 * NH <= 64 ? 64 : 128;   // S^T x 2, O^T x 2
+  static_assert(SIZE <= 227 * 1024, "shared memory per CTA");
 };
 
-template <int NH>
+template <int NH, bool LSE = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
     tc_attn_pair_kernel(const __grid_constant__ CUtensorMap tm_qabs, const __grid_constant__ CUtensorMap tm_qpe,
                         const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_lat,
                         TcAttnArgs a) {
-  using SM = AttnPairSmem<NH>;
+  using SM = AttnPairSmem<NH, LSE>;
   griddep_wait();   // the inputs all come from the stream's earlier kernels
   constexpr int NPR = SM::NPR, QKB = SM::QKB;
-  constexpr int CPR = NH / 8;                  // 16-byte chunks per row of an f16 partial
-  constexpr int XSH = NH == 16 ? 2 : 1;        // chunk swizzle: the rows of one 128-byte line cover all 32 banks
+  constexpr int XROW = SM::XB / 128;           // bytes of a row of a partial
+  constexpr int CPR = XROW / 16;               // its 16-byte chunks
+  constexpr int XSH = XROW == 32 ? 2 : (XROW == 64 ? 1 : 0);   // chunk swizzle: the rows of one 128-byte line cover all 32 banks
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -286,17 +291,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
       if (lane == 0) mbar_arrive(s_free_b + 8 * sb);
       // the peer has read what we sent for tile u - 2 out of this buffer
       if (!mbar_wait_cluster_warp(x_free_b + 8 * sb, ((u >> 1) & 1) ^ 1, abort_word, a.flag)) return false;
-      // the partial crosses in f16 (half the bytes; partial scores stay far inside its range)
-      const uint32_t dst = peer_x + sb * SM::XB + i * (NH * 2);
+      // the partial crosses in f16 (half the bytes; partial scores stay far inside its range) or in fp32
+      const uint32_t dst = peer_x + sb * SM::XB + i * XROW;
 #pragma unroll
       for (int c = 0; c < CPR; ++c) {
-        uint32_t w[4];
+        if constexpr (LSE) {
+          st_async_v4(dst + 16 * (c ^ xsw), nxt[4 * c], nxt[4 * c + 1], nxt[4 * c + 2], nxt[4 * c + 3], peer_x_full + 8 * sb);
+        } else {
+          uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          __half2 hv = __floats2half2_rn(nxt[8 * c + 2 * j], nxt[8 * c + 2 * j + 1]);
-          w[j] = *reinterpret_cast<uint32_t*>(&hv);
+          for (int j = 0; j < 4; ++j) {
+            __half2 hv = __floats2half2_rn(nxt[8 * c + 2 * j], nxt[8 * c + 2 * j + 1]);
+            w[j] = *reinterpret_cast<uint32_t*>(&hv);
+          }
+          st_async_v4_b32(dst + 16 * (c ^ xsw), w[0], w[1], w[2], w[3], peer_x_full + 8 * sb);
         }
-        st_async_v4_b32(dst + 16 * (c ^ xsw), w[0], w[1], w[2], w[3], peer_x_full + 8 * sb);
       }
       return true;
     };
@@ -330,16 +339,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
       if (i == 0) mbar_arrive_expect_tx(x_full_b + 8 * sb, SM::XB);
       if (!mbar_wait_warp(x_full_b + 8 * sb, (t >> 1) & 1, abort_word, a.flag)) { ok = false; break; }
       {
-        const uint4* xr = (const uint4*)(smem + SM::X_OFF + sb * SM::XB + i * (NH * 2));
+        const uint4* xr = (const uint4*)(smem + SM::X_OFF + sb * SM::XB + i * XROW);
 #pragma unroll
         for (int c = 0; c < CPR; ++c) {
           const uint4 x = xr[c ^ xsw];
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            cur[8 * c + 2 * j] += f.x;
-            cur[8 * c + 2 * j + 1] += f.y;
+            if constexpr (LSE) {
+              cur[4 * c + j] += __uint_as_float(w[j]);
+            } else {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+              cur[8 * c + 2 * j] += f.x;
+              cur[8 * c + 2 * j + 1] += f.y;
+            }
           }
         }
       }
@@ -392,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
         // no reference yet: scores of -inf, weight 0, or NaN, which stay visible
         const float p = valid ? ex2_approx(fmaf(cur[h], a.scale_log2, m_ref[h] == -INFINITY ? 0.f : -m_ref[h])) : 0.f;
         const bf16 pb = __float2bfloat16_rn(p);
-        l_part[h] = l_part[h] * alpha[h] + __bfloat162float(pb);
+        l_part[h] = l_part[h] * alpha[h] + (LSE ? p : __bfloat162float(pb));
         *reinterpret_cast<bf16*>(pbuf + h * 128 + ((((col >> 3) ^ (h & 7))) << 4) + (col & 7) * 2) = pb;
       }
       if (rescale && t >= 1) {   // identical on every thread: m_ref is shared

@@ -710,7 +710,7 @@ struct LatentExt {
 // Split-KV absorbed attention and the LSE merge of the splits -> o_lat (bf16).
 // tcgen05 kernel for the DeepSeek latent dims, CUDA-core kernel otherwise.
 // tc_attention_launch leaves the split partials and says in *out how they lie;
-// tc_attention_core merges them.
+// tc_attention_core merges them. `lse`: the log-sum-exp is wanted (up to 32 heads).
 struct AttnParts {
   long long ml_r;       // offset of the second CTA's (m, l) copy (tensor-core kernels)
   int half_cols;        // latent columns per (m, l) copy (0: one copy)
@@ -720,7 +720,7 @@ struct AttnParts {
 static inline int tc_attention_launch(const mla_handle* h, const void* q_abs, const void* q_pe, const void* kv_cache,
                                       int n_blocks, const int32_t* block_table, int mbps, const int32_t* ctx,
                                       int max_ctx, int n, float* part_o, float* part_ml, int splits, int* flag,
-                                      int* nseg, int allow_empty, AttnParts* out, cudaStream_t s) {
+                                      int* nseg, int allow_empty, int lse, AttnParts* out, cudaStream_t s) {
   const mla_config& c = h->cfg;
   const TcState& T = h->tc;
   const int H = c.n_heads, dr = c.qk_rope, rkv = c.kv_lora_rank;
@@ -766,15 +766,16 @@ static inline int tc_attention_launch(const mla_handle* h, const void* q_abs, co
     ta.part_o = part_o; ta.part_ml = part_ml; ta.flag = flag;
     ta.ml_r = ml_r = (long long)n * sp * H * 2;   // CTA r's (m, l) copy, one per latent half
     half_cols = 256;
-    static std::atomic<bool> attr16[64], attr32[64];
     mla_timer_begin("attn", s);
-    if (NH == 16) {
-      set_smem_once(attr16, tc_attn_pair_kernel<16>, AttnPairSmem<16>::SIZE);
-      launch_pdl(tc_attn_pair_kernel<16>, 2 * n * sp, 224, AttnPairSmem<16>::SIZE, s, mqa, mqp, mc, ml, ta);
-    } else {
-      set_smem_once(attr32, tc_attn_pair_kernel<32>, AttnPairSmem<32>::SIZE);
-      launch_pdl(tc_attn_pair_kernel<32>, 2 * n * sp, 224, AttnPairSmem<32>::SIZE, s, mqa, mqp, mc, ml, ta);
-    }
+    auto launch = [&](auto kernel, int smem, std::atomic<bool>* attr) {
+      set_smem_once(attr, kernel, smem);
+      launch_pdl(kernel, 2 * n * sp, 224, smem, s, mqa, mqp, mc, ml, ta);
+    };
+    static std::atomic<bool> attr[4][64];
+    if (NH == 16 && !lse) launch(tc_attn_pair_kernel<16>, AttnPairSmem<16>::SIZE, attr[0]);
+    else if (!lse) launch(tc_attn_pair_kernel<32>, AttnPairSmem<32>::SIZE, attr[1]);
+    else if (NH == 16) launch(tc_attn_pair_kernel<16, true>, AttnPairSmem<16, true>::SIZE, attr[2]);
+    else launch(tc_attn_pair_kernel<32, true>, AttnPairSmem<32, true>::SIZE, attr[3]);
     mla_timer_end("attn", s);
     mla_count_launch(1);
   } else if (latent_ok && H <= 128 && n <= ATT_MAX_SEQ && splits >= 2) {
@@ -836,7 +837,7 @@ static inline int tc_attention_core(const mla_handle* h, const void* q_abs, cons
   const float* sink = h->has_sink ? (const float*)(h->base + h->L.sink) : nullptr;
   AttnParts P{};
   const int st = tc_attention_launch(h, q_abs, q_pe, kv_cache, n_blocks, block_table, mbps, ctx, max_ctx, n, part_o,
-                                     part_ml, splits, flag, nseg, 0, &P, s);
+                                     part_ml, splits, flag, nseg, 0, 0, &P, s);
   if (st != MLA_OK) return st;
   splits = P.splits;
   if (olat_f16)   // its only reader is an FP8-weight GEMM

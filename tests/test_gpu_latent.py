@@ -813,3 +813,45 @@ def test_decode_attn_shows_a_nan_too(heads, fp8, act):
     out = layer.decode_attn(*args(case.device_inputs()), head_out=head)
     assert torch.isnan(head[0::2]).all() and torch.isnan(out[0::2]).all()
     assert same_bytes(head[1], whole[1]) and same_bytes(out[1], want[1])
+
+
+# ---------------------------------------------------------------------------
+# the log-sum-exp on every route that returns one
+# ---------------------------------------------------------------------------
+
+LSE_ROUTES = {
+    # name: (heads, own lengths, prefix, 8-bit)
+    "16_heads_16bit": (16, [700, 300, 64, 130], 0, False),
+    "5_heads_16bit": (5, [700, 300, 64, 130], 0, False),
+    "32_heads_16bit": (32, [700, 300, 64, 130], 0, False),
+    "40_heads_16bit": (40, [700, 300, 64, 130], 0, False),
+    "128_heads_16bit": (128, [700, 300, 64, 130], 0, False),
+    # ten sequences of up to 3840 rows are 600 tiles of 64: more than the prefix's launch takes along
+    "16_heads_16bit_prefix_and_long_rows": (16, [3840] + [90] * 9, 100, False),
+    "24_heads_16bit_prefix_and_long_rows": (24, [3840] + [90] * 9, 100, False),
+    "16_heads_8bit": (16, [700, 300, 64, 130], 0, True),
+    "40_heads_8bit": (40, [700, 300, 64, 130], 0, True),
+    "130_heads_8bit": (130, [300, 130], 0, True),
+    "4_heads_8bit_prefix": (4, [90, 64, 150], 700, True),
+    "16_heads_8bit_prefix_and_long_rows": (16, [3840] + [90] * 9, 100, True),
+}
+
+
+@pytest.mark.parametrize("name", list(LSE_ROUTES))
+def test_the_lse_is_good_to_fp32_on_every_route(name):
+    # What is left is fp32: sums of 576 products, exponentials, sums of weights, all below 2^-20 of a
+    # score of a few units; where partial scores cross in f16 and their first order is taken out, as in
+    # test_the_lse_is_good_to_fp32, below 2^-20 over sixty keys and more. 2e-6 of an lse of about 5 is 10 times
+    # that. Partials rounded to f16 leave 3e-5, row sums of weights rounded to bf16 2^-9 / sqrt(keys) / 5 = 5e-5.
+    heads, lens, prefix, fp8 = LSE_ROUTES[name]
+    case = Case(shape_of(heads, 64), lens, prefix, fp8, seed=23)
+    size = 2.0 ** np.floor(np.log2(np.abs(case.rows[:, :512].float().numpy()).mean(1, keepdims=True) + 1e-30))
+    size[~np.isfinite(size)] = 1.0
+    case.rows[:, :512] /= torch.from_numpy(size).bfloat16()   # rows of one size, as a norm leaves them
+    case.keys = row_values(case.shape, case.rows) if fp8 else case.rows.double().numpy()
+    layer = case.layer()
+    o, lse = layer.latent_attn(want_lse=True, **case.device_inputs())
+    want = case.oracle()
+    check(case, o, lse, want)
+    err = lse.double().cpu().numpy() - want[1]
+    assert np.linalg.norm(err) <= 2e-6 * np.linalg.norm(want[1])
