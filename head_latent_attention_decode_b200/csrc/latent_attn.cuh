@@ -68,6 +68,15 @@ __device__ __forceinline__ long long merge_units(const MergeSrc& s, int H, int t
   return g * s.group_units + f.x + e;
 }
 
+// What brings copy 0's sum of weights p_j e^{d_j} back to the sum of p_j, for the log-sum-exp: corr = sum_j p_j d_j /
+// sum_j p_j. e^{-corr} is that to first order, positive whatever the d_j (a partial score near f16's largest is
+// rounded by more than one nat, which 1 - corr would make negative), and exact where one key holds the weight.
+// Keys of weight zero with an infinite partial score leave a corr of NaN: the sum then stays as it is.
+__device__ __forceinline__ float undo_corr(const float* corr, long long at) {
+  const float c = corr ? corr[at] : 0.f;
+  return c == c ? expf(-c) : 1.f;
+}
+
 // grid (n, H), 128 G threads: thread c % 128 owns four consecutive columns, the
 // G groups of threads take every G-th partial and meet in shared memory (one
 // token's 150 partials of 2 KB are a latency chain for a single group).
@@ -124,8 +133,7 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(MergeArgs p) {
       const float w = v.y > 0.f ? __expf(v.x - M) : (v.y != v.y ? v.y : 0.f);   // a NaN sum stays NaN
       wsh[warp][i] = w;
       den += w == 0.f ? 0.f : w * v.y;
-      const float* cr = p.src[i < cnt0 ? 0 : 1].corr;   // the log-sum-exp's own sum: with the score errors taken out
-      if (warp == 0 && p.lse) den_l += w == 0.f ? 0.f : w * v.y * (cr ? 1.f - cr[at(i)] : 1.f);
+      if (warp == 0 && p.lse && w != 0.f) den_l += w * v.y * undo_corr(p.src[i < cnt0 ? 0 : 1].corr, at(i));
     }
     const float sink = z > -INFINITY ? __expf(z - M) : 0.f;
     den = warp_sum(den) + sink;

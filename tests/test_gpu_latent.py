@@ -855,3 +855,87 @@ def test_the_lse_is_good_to_fp32_on_every_route(name):
     check(case, o, lse, want)
     err = lse.double().cpu().numpy() - want[1]
     assert np.linalg.norm(err) <= 2e-6 * np.linalg.norm(want[1])
+
+
+# ---------------------------------------------------------------------------
+# partial scores near f16's largest, and infinite ones
+# ---------------------------------------------------------------------------
+
+CORR_ROUTES = [(128, 0, True), (128, 0, False), (16, 150, True), (16, 150, False), (40, 100, False)]
+
+
+@pytest.mark.parametrize("heads,prefix,fp8", CORR_ROUTES)
+def test_the_lse_with_partial_scores_near_the_largest_of_f16(heads, prefix, fp8):
+    # The halves of a score are near +-50000, where f16's steps are 32 (1.15 nat after the scale for half a
+    # step), and cancel: a score of a few nats. One key, or one heavy key of many, holds nearly all the weight
+    # (e^-40 elsewhere), so that its own rounding is all there is to take out: lse is its score.
+    # fp32 sums of halves of 5e4 and their difference: 2^-24 512 5e4 scale = 0.11 at the worst, 2^-24 sqrt(512)
+    # 5e4 scale = 5e-3 for products of either sign. Without the correction up to 1.15 and 0.6 on average.
+    case = Case(shape_of(heads, 64), [1, 130], prefix, fp8, seed=3)
+    rng = np.random.default_rng(7)
+    q = np.sign(rng.standard_normal(512)) * 2.0 ** rng.integers(4, 6, 512)   # one direction for every head, but for
+    q[500] = 0.0                                                             # a column that moves them to all places
+    case.q_abs[:] = torch.from_numpy(q).bfloat16()                           # between two f16 values
+    case.q_abs[:, :, 500] = torch.arange(heads).bfloat16()
+    case.q_pe[:] = 0
+    a = np.sign(q) * np.where(np.arange(512) < 256, 1.0, -1.0) * 8.0
+    case.rows[:] = 0
+    for t in range(2):
+        for n, s in enumerate(case.key_slots(t)):
+            row = np.zeros(576)
+            if n == 0:
+                row[:512] = a * rng.choice([0.875, 1.0, 1.125], 512)
+                half = [float(q[:256] @ row[:256]), float(q[256:] @ row[256:512])]
+                k = 300 + np.argmax(np.abs(q[300:]))     # bring the sum to about 200 (14 nats and more)
+                row[k] += (200 - sum(half)) / q[k]
+                row[500] = 1.0
+            else:
+                row[:512] = -np.sign(q) * 0.0625          # far below
+            case.rows[s] = torch.from_numpy(row).bfloat16()
+    case.keys = row_values(case.shape, case.rows) if fp8 else case.rows.double().numpy()
+    o, lse = case.layer().latent_attn(want_lse=True, **case.device_inputs())
+    lse = lse.double().cpu().numpy()
+    for t in range(2):
+        k = case.keys[case.key_slots(t)]
+        _, want, p = lr.latent_attention(case.q_abs[t].double().numpy(), case.q_pe[t].double().numpy(), k[:, :512], k[:, 512:], case.scale)
+        h = case.q_abs[t].double().numpy()
+        h = np.abs([h[:, :256] @ k[0, :256], h[:, 256:] @ k[0, 256:512]])
+        assert 3e4 < h.min() and h.max() < 65504 and p[:, 0].min() > 1 - 1e-9
+        assert np.abs(h - np.float16(h)).max() * case.scale > 0.5
+        assert np.isfinite(lse[t]).all() and np.abs(lse[t] - want).max() <= 0.02
+
+
+@pytest.mark.parametrize("heads,bs,prefix,fp8", NAN_ROUTES)
+def test_keys_that_an_infinite_score_takes_out(heads, bs, prefix, fp8):
+    # -inf for every head: the row has no weight, in o and in the log-sum-exp
+    case = Case(shape_of(heads, bs), [129, 40, 1], prefix, fp8, seed=heads + 2)
+    case.q_pe[:, :, 2] = -case.q_pe[:, :, 2].abs() - 0.125
+    slots_of = [case.key_slots(t) for t in range(3)]
+    slots, at = case.key_slots, {0: prefix + 128, 1: prefix + 7}
+    case.lens, case.key_slots = [128, 39, 1], lambda t: np.delete(slots_of[t], at[t]) if t in at else slots_of[t]
+    want = case.oracle()   # without those keys
+    case.lens, case.key_slots = [129, 40, 1], slots
+    for t, j in at.items():
+        case.rows[slots_of[t][j], case.shape.kv_lora_rank + 2] = float("inf")
+    dead_and_alive(case, case.layer(), case.device_inputs(), want, np.zeros((3, heads), bool))
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads,prefix", [(128, 0), (40, 0), (16, 6400)])
+def test_keys_that_an_infinite_score_takes_out_of_long_rows(heads, prefix, fp8):
+    # several tiles to a cluster: the rotary keys of every second one belong to the CTA that sums the correction
+    lens = [40] if prefix else [9600, 40]
+    case = Case(shape_of(heads, 64), lens, prefix, fp8, seed=heads + 3)
+    case.q_pe[:, :, 2] = -case.q_pe[:, :, 2].abs() - 0.125
+    slots_of = [case.key_slots(t) for t in range(len(lens))]
+    gone = np.arange(70, 64 * 12, 64)
+    slots = case.key_slots
+    if prefix:
+        case.prefix_len -= len(gone)
+    else:
+        case.lens[0] -= len(gone)
+    case.key_slots = lambda t: np.delete(slots_of[t], gone) if t == 0 else slots_of[t]
+    want = case.oracle()   # without those keys
+    case.lens, case.prefix_len, case.key_slots = lens, prefix, slots
+    case.rows[slots_of[0][gone], case.shape.kv_lora_rank + 2] = float("inf")
+    dead_and_alive(case, case.layer(), case.device_inputs(), want, np.zeros((len(lens), heads), bool))
