@@ -34,7 +34,12 @@ def upload_weights(weights, device) -> dict:
 
 
 class MlaLayer:
-    """One layer's repacked weights (device) and C-ABI handle."""
+    """One layer's repacked weights (device) and C-ABI handle.
+
+    The calls of a layer share one workspace, `ws`, made and enlarged as they need it. Calls on different
+    streams are therefore put in order, each behind the calls before it. A captured graph keeps the workspace it
+    was captured with; replays of graphs, and calls beside them, must not overlap on the GPU. `ws` holds the
+    device flag of the calls made on it: a graph captured before any call has a workspace of its own."""
 
     def __init__(self, shape, weights, row_layout: int = MLA_ROW_LATENT_FIRST,
                  device: str = "cuda", softmax_scale: float = 0.0, attn_sink=None, cache_dtype: str | None = None):
@@ -62,8 +67,10 @@ class MlaLayer:
         self.block_bytes = mla_cache_block_bytes(self.handle)
         self._cache_torch = torch.uint8 if cache_dtype == "fp8" else self.act
         self.ws = None
-        self._graph_ws = []
-        self._ws_for = None   # the sizes the workspace was last asked for
+        self._graph_ws = []         # workspaces that captured graphs hold
+        self._ws_for = (None, 0)    # the sizes that prefix_workspace was last asked for, and their bytes
+        self._device_index = self.blob.get_device()
+        self._ws_stream = self._ws_raw = None   # the stream of the last call, and its raw handle
 
     def close(self) -> None:
         """Release the library handle (the weight blob is torch memory)."""
@@ -77,33 +84,55 @@ class MlaLayer:
         if mla_destroy is not None:
             self.close()
 
-    def _held(self, ws: torch.Tensor) -> torch.Tensor:
-        """ws, kept alive with the layer if a graph is being captured (a later call may need a larger one)."""
-        if torch.cuda.is_current_stream_capturing() and all(w is not ws for w in self._graph_ws):
-            self._graph_ws.append(ws)
+    def _new_ws(self, need: int) -> torch.Tensor:
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        mla_workspace_init(ws)
         return ws
 
-    def workspace(self, max_tokens: int, max_context_len: int = 1) -> torch.Tensor:
-        need = mla_workspace_bytes(self.handle, max(1, max_tokens), max(1, max_context_len))
+    def _workspace(self, need: int) -> torch.Tensor:
+        """A workspace of `need` bytes or more for a call on the current stream."""
+        if torch.cuda.is_current_stream_capturing():
+            # kept alive with the layer (a later call may need a larger one); one made here is the graph's own
+            for ws in (self.ws, *self._graph_ws):
+                if ws is not None and ws.numel() >= need:
+                    break
+            else:
+                ws = self._new_ws(need)
+            if all(w is not ws for w in self._graph_ws):
+                self._graph_ws.append(ws)
+            return ws
+        if torch._C._cuda_getCurrentRawStream(self._device_index) != self._ws_raw:
+            self._change_stream()
         if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            mla_workspace_init(self.ws)
+            old, self.ws = self.ws, self._new_ws(need)
+            if old is not None:
+                self.ws[:4].copy_(old[:4])            # the device flag is sticky
+                old.record_stream(self._ws_stream)    # the last calls on it may still run
         return self.ws
+
+    def _change_stream(self):
+        """The current stream waits for the calls made on the one before it."""
+        stream, before = torch.cuda.current_stream(self.device), self._ws_stream
+        if before is not None:
+            with torch.cuda.stream(before):
+                capturing = torch.cuda.is_current_stream_capturing()   # its earlier work was waited for then
+            if not capturing:
+                stream.wait_stream(before)
+        self._ws_stream, self._ws_raw = stream, stream.cuda_stream
+
+    def workspace(self, max_tokens: int, max_context_len: int = 1) -> torch.Tensor:
+        return self._workspace(mla_workspace_bytes(self.handle, max(1, max_tokens), max(1, max_context_len)))
 
     def prefix_workspace(self, max_tokens: int, max_prefix_len: int, max_context_len: int) -> torch.Tensor:
         """A workspace for latent_attn and decode_attn_prefix (and every other call)."""
         sizes = (max_tokens, max_prefix_len, max_context_len)
-        if sizes == self._ws_for:
-            return self._held(self.ws)
-        need = mla_prefix_workspace_bytes(self.handle, max(1, max_tokens), max(0, max_prefix_len),
-                                          max(1, max_context_len))
-        if need == 0:
-            raise ValueError("prefix_workspace: sizes not accepted by the library")
-        if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            mla_workspace_init(self.ws)
-        self._ws_for = sizes   # it only ever grows, so it stays large enough
-        return self._held(self.ws)
+        if sizes != self._ws_for[0]:
+            need = mla_prefix_workspace_bytes(self.handle, max(1, max_tokens), max(0, max_prefix_len),
+                                              max(1, max_context_len))
+            if need == 0:
+                raise ValueError("prefix_workspace: sizes not accepted by the library")
+            self._ws_for = (sizes, need)
+        return self._workspace(self._ws_for[1])
 
     def new_cache(self, n_blocks: int) -> torch.Tensor:
         """A zeroed paged cache: [n_blocks, 1, block_size, R], or [n_blocks, block bytes] uint8 if 8-bit."""
@@ -134,7 +163,7 @@ class MlaLayer:
         """rows [n, R] into the cache's flat rows slot_mapping (negative: skipped), quantised if it is 8-bit."""
         self._check_rows(rows)
         self._check_cache(kv_cache)
-        ws = self._held(self.ws if self.ws is not None else self.workspace(1))
+        ws = self._workspace(256) if self.ws is not None else self.workspace(1)   # the device flag alone
         mla_cache_write(self.handle, rows, kv_cache, slot_mapping, ws)
         return kv_cache
 
@@ -144,7 +173,7 @@ class MlaLayer:
             rows = torch.zeros((slots.numel(), self.shape.kv_row_dim), dtype=self.act, device=self.device)
         self._check_rows(rows)
         self._check_cache(kv_cache)
-        ws = self._held(self.ws if self.ws is not None else self.workspace(1))
+        ws = self._workspace(256) if self.ws is not None else self.workspace(1)   # the device flag alone
         mla_cache_read(self.handle, kv_cache, slots, rows, ws)
         return rows
 
@@ -214,8 +243,7 @@ class MlaLayer:
             q_abs = torch.empty((n, s.n_heads, s.kv_lora_rank), dtype=self.act, device=self.device)
         if q_pe is None:
             q_pe = torch.empty((n, s.n_heads, s.qk_rope), dtype=self.act, device=self.device)
-        ws = self.ws if self.ws is not None and self.ws.numel() >= mla_workspace_bytes(
-            self.handle, max(n, 1), 1) else self.workspace(n, 1)
+        ws = self.workspace(n, 1)
         mla_decode_qkv(self.handle, hidden, cos, sin, kv_cache, slot_mapping, q_abs, q_pe, ws,
                        input_norm_w=input_norm_w)
         return q_abs, q_pe
@@ -227,8 +255,7 @@ class MlaLayer:
         self._check_cache_bytes(kv_cache)
         if out is None:
             out = torch.empty((n, s.hidden), dtype=self.act, device=self.device)
-        ws = self.ws if self.ws is not None and self.ws.numel() >= mla_workspace_bytes(
-            self.handle, max(n, 1), max_context_len) else self.workspace(n, max_context_len)
+        ws = self.workspace(n, max_context_len)
         mla_decode_attn(self.handle, q_abs, q_pe, kv_cache, block_table, context_lens,
                         max_context_len, out, ws, head_out=head_out)
         return out
@@ -241,8 +268,7 @@ class MlaLayer:
             q_out = torch.empty((S, s.n_heads, s.qk_nope + s.qk_rope), dtype=self.act, device=self.device)
         if kv_out is None:
             kv_out = torch.empty((S, s.kv_lora_rank + s.qk_rope), dtype=self.act, device=self.device)
-        ws = self.ws if self.ws is not None and self.ws.numel() >= mla_workspace_bytes(
-            self.handle, max(S, 1), 1) else self.workspace(S, 1)
+        ws = self.workspace(S, 1)
         mla_v4_qkv(self.handle, hidden, cos, sin, kv_norm_w, q_out, kv_out, ws)
         return q_out, kv_out
 
@@ -252,8 +278,7 @@ class MlaLayer:
         self._check_cache_bytes(kv_cache)
         if out is None:
             out = torch.empty((S, s.hidden), dtype=self.act, device=self.device)
-        ws = self.ws if self.ws is not None and self.ws.numel() >= mla_workspace_bytes(
-            self.handle, max(S, 1), 1) else self.workspace(S, 1)
+        ws = self.workspace(S, 1)
         mla_prefill(self.handle, hidden, cos, sin, out, ws, head_out=head_out, kv_cache=kv_cache,
                     slot_mapping=slot_mapping)
         return out

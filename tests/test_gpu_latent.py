@@ -939,3 +939,105 @@ def test_keys_that_an_infinite_score_takes_out_of_long_rows(heads, prefix, fp8):
     case.lens, case.prefix_len, case.key_slots = lens, prefix, slots
     case.rows[slots_of[0][gone], case.shape.kv_lora_rank + 2] = float("inf")
     dead_and_alive(case, case.layer(), case.device_inputs(), want, np.zeros((len(lens), heads), bool))
+
+
+# ---------------------------------------------------------------------------
+# a layer's workspace: graphs that hold it, streams that share it, growth
+# ---------------------------------------------------------------------------
+
+def decode_layer(fp8, heads=16):
+    from head_latent_attention_decode_b200.layer import MlaLayer
+    shape = dataclasses.replace(wl.V2LITE, hidden=512, n_heads=heads)
+    return MlaLayer(shape, wl.make_weights(shape, 3), cache_dtype="fp8" if fp8 else None)
+
+
+def step_inputs(layer, n=3, ctx=90, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = layer.shape
+    table = torch.randperm(2 * n, generator=g, device="cuda").int().view(n, 2)
+    cache = layer.new_cache(2 * n)
+    rows = torch.randn(2 * n * 64, shape.kv_row_dim, generator=g, device="cuda").bfloat16()
+    layer.cache_write(rows, cache, torch.arange(2 * n * 64, dtype=torch.int32, device="cuda"))
+    lens = torch.full((n,), ctx, dtype=torch.int32, device="cuda")
+    cos, sin = layer.rope(lens - 1)
+    h = torch.randn(n, shape.hidden, generator=g, device="cuda").bfloat16()
+    slots = (table[:, (ctx - 1) // 64] * 64 + (ctx - 1) % 64).int()
+
+    def step(out=None):
+        q_abs, q_pe = layer.decode_qkv(h, cos, sin, cache, slots)
+        return layer.decode_attn(q_abs, q_pe, cache, table, lens, ctx, out=out)
+
+    return step
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("warm", [True, False])
+def test_a_decode_step_in_a_graph_outlives_a_larger_workspace(fp8, warm):
+    layer = decode_layer(fp8)
+    want = step_inputs(decode_layer(fp8))()     # (another layer's, with a workspace of its own)
+    step = step_inputs(layer)
+    if warm:
+        step()
+    else:
+        layer.ws = None                         # nothing but the captured calls has asked for one
+    out, g = torch.empty_like(want), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        step(out)
+    held = layer.ws.data_ptr() if warm else None
+    layer.prefix_workspace(500, 4000, 4000)
+    assert layer.ws.data_ptr() != held and mla.mla_read_device_flag(layer.ws) == 0
+    junk = [torch.full((layer.ws.numel() // 64,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        assert same_bytes(step(), want)         # an eager call between replays
+        torch.cuda.synchronize()
+        assert same_bytes(out, want) and all(bool((j == 255).all()) for j in junk)
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_two_streams_share_a_layer(heads, fp8):
+    case = Case(shape_of(heads, 64), [1, 2000, 640, 0], 1500, fp8, seed=8)
+    layer = case.layer()
+    x = case.device_inputs()
+    y = dict(x, q_abs=x["q_abs"].flip(1).contiguous(), q_pe=x["q_pe"].flip(1).contiguous())
+    wants = [layer.latent_attn(want_lse=True, **z) for z in (x, y)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(20):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(layer.latent_attn(want_lse=True, **(x, y)[i % 2]))
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(outs):
+        assert same_bytes(o, wants[i % 2][0]) and same_bytes(lse, wants[i % 2][1]), i
+
+
+def test_a_workspace_grows_while_another_stream_uses_it():
+    case = Case(shape_of(16, 64), [2000, 900], 0, True, seed=2)
+    layer = case.layer()
+    x = case.device_inputs()
+    want, _ = layer.latent_attn(**x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        outs = [layer.latent_attn(**x)[0] for _ in range(20)]
+    old = layer.ws.numel()
+    layer.prefix_workspace(400, 4000, 4000)
+    junk = [torch.full((old,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]   # where the old one was, if free
+    torch.cuda.synchronize()
+    assert all([same_bytes(o, want) for o in outs]) and all(bool((j == 255).all()) for j in junk)
+
+
+def test_the_device_flag_survives_a_larger_workspace():
+    shape = shape_of(16, 64)
+    layer = layer_of(shape, True)
+    rows, slot = torch.zeros(1, 576, device="cuda").bfloat16(), torch.tensor([999], dtype=torch.int32, device="cuda")
+    layer.cache_write(rows, layer.new_cache(1), slot)
+    small = layer.ws
+    layer.prefix_workspace(300, 4000, 4000)
+    assert layer.ws is not small and mla.mla_read_device_flag(layer.ws) == mla.MLA_FLAG_BAD_SLOT
+    mla.mla_clear_device_flag(layer.ws)
+    assert mla.mla_read_device_flag(layer.ws) == 0
