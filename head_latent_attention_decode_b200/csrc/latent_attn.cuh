@@ -210,9 +210,13 @@ struct LatentPlan {
   size_t o_p, ml_p, seg_p, corr_h;
 };
 
-// `lse`: the log-sum-exp is wanted. `force` < 0: by the rules; else bit 0 says whether a prefix goes to the
-// head-major kernel and bit 1 whether the own rows ride along, as a smaller call may have it (latent_ws_bytes).
-static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool aligned, bool lse,
+constexpr int LAT_FEW_ROWS = 32;   // query rows up to which a prefix goes to the few-head 8-bit kernel
+
+// `lse`: the log-sum-exp is wanted. `budget` > 0: the query is not 16-byte aligned, as the tensor-core kernels
+// need it; CUDA cores then take as many tokens and splits at a time as this scratch holds. `force` < 0: by the
+// rules; else bit 0 says whether a prefix goes to the head-major kernel and bit 1 whether the own rows ride
+// along, as a smaller call may have it (latent_ws_bytes).
+static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefix_len, int max_ctx, bool lse, size_t budget = 0,
                                      int force = -1) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads;
@@ -221,34 +225,36 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   size_t off = 0;
   auto put = [&](size_t b) { size_t o = off; off = align_up(off + b, 256); return o; };
   // the tensor-core kernels: the DeepSeek latent, TMA boxes of whole parts of a block
-  const bool tc = h->tc.attn && aligned && c.kv_lora_rank == 512 && c.qk_rope == 64;
+  const bool tc = h->tc.attn && c.kv_lora_rank == 512 && c.qk_rope == 64;
   const bool b64 = c.block_size % 64 == 0, pre = prefix_len > 0;
   const long long tiles = cdiv(max_ctx, 64);
   // The own rows may ride in the prefix's head-major launch. With few heads that wastes most of its 128
   // rows (2 us per 64 rows and SM pair whatever the heads), but saves a launch with its start-up and tail
   // (about 17 us): worth it up to eight of such tiles per pair.
   const bool ride = H <= 128 && (force < 0 ? n * tiles <= 8LL * pairs : (force & 2) != 0);
-  if (tc && h->cache8 && c.block_size % 16 == 0) {
+  const bool fits = tc && (h->cache8 ? c.block_size % 16 == 0 : b64 && H <= 128);
+  if (!fits || budget > 0) {
+    w.simt = true;
+  } else if (h->cache8) {
     // Per 128 keys the few-head kernel takes 1.7 us of one SM for every 16 heads (or 16 query rows), the
     // head-major one 2.9 us of two SMs whatever the rows up to 128. Own rows, 32 sequences of 8192:
     // 64 heads 111 against 126 us, 80 heads 139 against 128. A prefix of 16384: 48 rows 36 against 29 us,
     // since the head-major launch takes the own rows along.
-    w.heads_pre = pre && b64 && (force < 0 ? n * H > 32 : (force & 1) != 0);
+    w.heads_pre = pre && b64 && (force < 0 ? n * H > LAT_FEW_ROWS : (force & 1) != 0);
     w.few_pre = pre && !w.heads_pre;
     w.heads_own = b64 && H <= 128 && (H > 64 || (w.heads_pre && ride));
     w.few_own = !w.heads_own;
-  } else if (tc && !h->cache8 && b64 && H <= 128) {
+  } else {
     // Beyond 32 heads only the head-major form of this file has the log-sum-exp good to fp32
     // (TcAttnArgs::corr); up to 32 the kernel of mla_decode_attn has a form for it.
     w.heads_pre = pre;
     w.heads_own = H > 32 ? pre || lse : pre && ride;
     w.own16 = !w.heads_own;
-  } else {
-    w.simt = true;
   }
   // tokens per pass: the kernels' entries (sequences; blocks of query rows) and tile lists
   long long most = n;
   auto limit = [&](long long m) { if (most > m) most = m > 0 ? m : 1; };
+  if (w.simt) limit(65535);   // its grid
   if (w.few_own) limit(A8_MAX_ENT);
   if (w.own16 && H > 32) limit(ATT_MAX_SEQ);
   if (w.heads_pre || w.heads_own) {   // chunk + ceil(chunk H / 128) entries
@@ -270,6 +276,13 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   } else if (!w.heads_own) {
     const long long s = cdiv((long long)(w.simt ? prefix_len : 0) + max_ctx, 256);
     w.splits = s < 2 ? 2 : (s > 16 ? 16 : (int)s);
+    if (fits && budget > 0) {
+      auto token = [&] { return (size_t)w.splits * H * (c.kv_lora_rank + 4) * 4; };
+      const size_t most_bytes = budget > 768 ? budget - 768 : 0;   // less the roundings of `put`
+      while (w.splits > 1 && token() > most_bytes) --w.splits;
+      const size_t tokens = most_bytes / (token() + 4);
+      if (tokens < (size_t)w.chunk) w.chunk = tokens > 0 ? (int)tokens : 1;
+    }
     const size_t rows = (size_t)w.chunk * w.splits * H;
     w.o = put(rows * c.kv_lora_rank * 4);
     w.ml = put(rows * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
@@ -296,15 +309,17 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   return w;
 }
 // Enough for every call of up to these sizes: what a smaller one needs may be more where it takes other
-// kernels.
+// kernels. (An unaligned query makes do with what the aligned one has.)
 static inline size_t latent_ws_bytes(const mla_handle* h, long long n, int prefix_len, int max_ctx) {
   size_t most = 0;
   for (int p = 0; p < (prefix_len > 0 ? 2 : 1); ++p)
-    for (int force = 0; force < 4; ++force)
-      for (int k = 0; k < 4; ++k) {
-        const size_t t = latent_plan(h, n, p ? prefix_len : 0, max_ctx, (k & 1) != 0, (k & 2) != 0, force).total;
-        if (t > most) most = t;
-      }
+    for (int k = 0; k < 8; ++k) {
+      long long m = n;
+      if (p && !(k & 1) && h->cache8 && h->cfg.block_size % 64 == 0)   // a prefix on the few-head kernel
+        m = n * h->cfg.n_heads > LAT_FEW_ROWS ? LAT_FEW_ROWS / h->cfg.n_heads : n;
+      const size_t t = m > 0 ? latent_plan(h, m, p ? prefix_len : 0, max_ctx, (k & 4) != 0, 0, k & 3).total : 0;
+      if (t > most) most = t;
+    }
   return most;
 }
 
@@ -502,14 +517,15 @@ static int pass_simt(const mla_handle* h, const LatentPlan& w, const LatentCall&
   return MLA_OK;
 }
 
-// o_lat [n, H, r_kv] (o_dt: 0 fp32, 1 bf16, 2 f16) and, if given, lse [n, H].
-static inline int latent_core(const mla_handle* h, const LatentCall& call, void* o_lat, int o_dt, float* lse,
-                              char* scratch, int* flag, cudaStream_t s) {
+// o_lat [n, H, r_kv] (o_dt: 0 fp32, 1 bf16, 2 f16) and, if given, lse [n, H]. `scratch`: bytes of them, at least
+// latent_ws_bytes of the call's sizes.
+static inline int latent_core(const mla_handle* h, const LatentCall& call, void* o_lat, int o_dt, float* lse, char* scratch,
+                              size_t bytes, int* flag, cudaStream_t s) {
   const mla_config& c = h->cfg;
   const int H = c.n_heads, rkv = c.kv_lora_rank, dr = c.qk_rope;
   const size_t esz = c.act_dtype == MLA_F32 ? 4 : 2, o_esz = o_dt == 0 ? 4 : 2;
   const bool aligned = (((uintptr_t)call.q_abs | (uintptr_t)call.q_pe) & 15) == 0;
-  const LatentPlan w = latent_plan(h, call.n, call.prefix_len, call.max_ctx, aligned, lse != nullptr);
+  const LatentPlan w = latent_plan(h, call.n, call.prefix_len, call.max_ctx, lse != nullptr, aligned ? 0 : bytes);
   for (int t = 0; t < call.n; t += w.chunk) {
     LatentCall a = call;
     a.n = call.n - t < w.chunk ? call.n - t : w.chunk;

@@ -126,7 +126,7 @@ struct WsLayout {
   size_t Y1, qn, Q, part_o, part_ml, nseg, o_lat, head, xn, oy;   // decode
   size_t pY1, pqn, pQ, pcn, pkpe, pKV, phead, pDQ, poy;            // prefill
   size_t tc;                                                   // tensor-core path scratch
-  size_t lat;                                                  // 8-bit cache: the attention's scratch (latent_attn.cuh)
+  size_t lat, lat_bytes;                                       // latent attention's scratch (latent_attn.cuh)
   size_t qkv_total;                                            // what the decode front-fold needs
   size_t dec_total;                                            // what the decode calls need
   size_t total;                                                // what every call needs
@@ -138,7 +138,10 @@ static int decode_splits(int max_ctx) {
   return c < 2 ? 2 : (c > 16 ? 16 : c);
 }
 
-static WsLayout make_ws(const mla_handle* h, long long n, int max_ctx) {
+// prefix_len >= 0: a call with a prefix or in latent form. Its attention, and every one on an 8-bit cache, is
+// latent_attn.cuh's: on a 16-bit cache its scratch lies over the split partials of mla_decode_attn, which an
+// 8-bit cache has none of.
+static WsLayout make_ws(const mla_handle* h, long long n, int max_ctx, int prefix_len = -1) {
   const mla_config* c = &h->cfg;
   const WeightLayout& L = h->L;
   const size_t a = dtype_size(c->act_dtype);
@@ -150,16 +153,25 @@ static WsLayout make_ws(const mla_handle* h, long long n, int max_ctx) {
   W.Y1 = put((size_t)n * L.N1 * 4);
   W.qn = put((size_t)n * (c->q_lora_rank ? c->q_lora_rank : 1) * a);
   W.Q = put((size_t)n * L.Hq * 4);
-  W.part_o = put((size_t)n * W.splits * H * rkv * 4);
-  W.part_ml = put((size_t)n * W.splits * H * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
-  W.nseg = put((size_t)n * 4);                                // split partials per sequence
+  const size_t lat = h->cache8 || prefix_len >= 0 ? latent_ws_bytes(h, n, prefix_len > 0 ? prefix_len : 0, max_ctx) : 0;
+  if (!h->cache8) {
+    W.part_o = put((size_t)n * W.splits * H * rkv * 4);
+    W.part_ml = put((size_t)n * W.splits * H * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
+    W.nseg = put((size_t)n * 4);                                // split partials per sequence
+    W.lat = W.part_o;
+    if (W.lat + lat > off) off = align_up(W.lat + lat, 256);
+    W.lat_bytes = off - W.lat;
+  }
   W.o_lat = put((size_t)n * H * rkv * a);
   W.head = put((size_t)n * H * dv * a);
   W.xn = put((size_t)n * c->hidden * a);
   W.oy = put((size_t)n * (L.G ? L.G * L.ro : 1) * a);   // grouped output projection: the low-rank rows
   W.tc = put(tc_decode_ws_bytes(h, n, max_ctx));
   W.qkv_total = off;
-  W.lat = put(h->cache8 ? latent_ws_bytes(h, n, 0, max_ctx) : 0);
+  if (h->cache8) {   // behind what the front-fold needs
+    W.lat = put(lat);
+    W.lat_bytes = lat;
+  }
   const size_t dec_end = off;
   W.dec_total = dec_end;
   off = 256;
@@ -531,7 +543,7 @@ static int decode_attn_impl(mla_handle* h, const void* q_abs, const void* q_pe, 
   }
   void* o_lat = wsb + W.o_lat;
   if (ext) {
-    const int r = latent_core(h, *ext->call, o_lat, ta, nullptr, ext->scratch, flag, s);
+    const int r = latent_core(h, *ext->call, o_lat, ta, nullptr, ext->scratch, ext->bytes, flag, s);
     if (r != MLA_OK) return r;
   } else if (tc_attention_supported(h)) {
     // tensor-core attention (bf16 activations) ahead of CUDA-core W_UV / o_proj
@@ -585,7 +597,7 @@ int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
   if (ws_bytes < W.dec_total) return MLA_ERR_WORKSPACE;
   const LatentCall call{q_abs, q_pe, kv_cache, n_blocks, nullptr, 0, block_table, max_blocks_per_seq,
                         context_lens, max_context_len, n};
-  const LatentExt ext{&call, (char*)ws + W.lat};
+  const LatentExt ext{&call, (char*)ws + W.lat, W.lat_bytes};
   return decode_attn_impl(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq, context_lens,
                           max_context_len, n, out, head_out, ws, W, h->cache8 ? &ext : nullptr, stream);
 }
@@ -655,7 +667,7 @@ int mla_cache_read(mla_handle* h, const void* kv_cache, int n_blocks, const int3
 size_t mla_prefix_workspace_bytes(const mla_handle* h, int max_tokens, int max_prefix_len, int max_context_len) {
   if (!h || max_tokens < 1 || max_prefix_len < 0 || max_context_len < 1) return 0;
   if ((long long)max_prefix_len + max_context_len > (1 << 30)) return 0;
-  return make_ws(h, max_tokens, max_context_len).total + latent_ws_bytes(h, max_tokens, max_prefix_len, max_context_len);
+  return make_ws(h, max_tokens, max_context_len, max_prefix_len).total;
 }
 
 // Checks shared by the two calls below; *W the workspace layout.
@@ -666,8 +678,8 @@ static int latent_check(mla_handle* h, const LatentCall& a, const void* out, con
     return MLA_ERR_INVALID_ARG;
   if ((long long)a.prefix_len + a.max_ctx > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   if ((uintptr_t)a.cache % 16 || (uintptr_t)ws % 16 || !on_device(h)) return MLA_ERR_INVALID_ARG;
-  *W = make_ws(h, a.n, a.max_ctx);
-  if (ws_bytes < W->total + latent_ws_bytes(h, a.n, a.prefix_len, a.max_ctx)) return MLA_ERR_WORKSPACE;
+  *W = make_ws(h, a.n, a.max_ctx, a.prefix_len);
+  if (ws_bytes < W->dec_total) return MLA_ERR_WORKSPACE;
   return MLA_OK;
 }
 
@@ -682,7 +694,7 @@ int mla_latent_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
   WsLayout W;
   const int st = latent_check(h, a, o_lat, ws, ws_bytes, &W);
   if (st != MLA_OK) return st;
-  const int r = latent_core(h, a, o_lat, acode(h), lse, (char*)ws + W.total, (int*)ws, (cudaStream_t)stream);
+  const int r = latent_core(h, a, o_lat, acode(h), lse, (char*)ws + W.lat, W.lat_bytes, (int*)ws, (cudaStream_t)stream);
   return r != MLA_OK ? r : cuda_status();
 }
 
@@ -697,7 +709,7 @@ int mla_decode_attn_prefix(mla_handle* h, const void* q_abs, const void* q_pe, c
   WsLayout W;
   const int st = latent_check(h, a, out, ws, ws_bytes, &W);
   if (st != MLA_OK) return st;
-  const LatentExt ext{&a, (char*)ws + W.total};
+  const LatentExt ext{&a, (char*)ws + W.lat, W.lat_bytes};
   return decode_attn_impl(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq, context_lens,
                           max_context_len, n, out, head_out, ws, W, &ext, stream);
 }

@@ -701,10 +701,11 @@ static inline int tc_decode_qkv(const mla_handle* h, const void* hidden, int n, 
 // to, and its scratch (latent_attn.cuh).
 struct LatentCall;
 static inline int latent_core(const mla_handle* h, const LatentCall& a, void* o_lat, int o_dt, float* lse, char* scratch,
-                              int* flag, cudaStream_t s);
+                              size_t bytes, int* flag, cudaStream_t s);
 struct LatentExt {
   const LatentCall* call;
   char* scratch;
+  size_t bytes;
 };
 
 // Split-KV absorbed attention and the LSE merge of the splits -> o_lat (bf16).
@@ -864,7 +865,7 @@ static inline int tc_decode_attn(const mla_handle* h, const void* q_abs, const v
   // with the FP8-weight GEMM, o_lat, the head outputs (unless the caller asked for
   // them) and the grouped low-rank rows are written in f16: only those GEMMs read them
   const int af16 = h->tc.fp8 && !W.deq, hf16 = af16 && head_internal;
-  int st = ext ? latent_core(h, *ext->call, o_lat, af16 ? 2 : 1, nullptr, ext->scratch, flag, s)
+  int st = ext ? latent_core(h, *ext->call, o_lat, af16 ? 2 : 1, nullptr, ext->scratch, ext->bytes, flag, s)
                : tc_attention_core(h, q_abs, q_pe, kv_cache, n_blocks, block_table, mbps, ctx, max_ctx, n, part_o,
                                    part_ml, splits, o_lat, flag, nseg, s, af16);
   if (st != MLA_OK) return st;

@@ -11,8 +11,10 @@ import torch
 import head_latent_attention_decode_b200 as mla
 from head_latent_attention_decode_b200 import workloads as wl
 from oracle import latent_ref as lr
+from oracle import mla_ref as ref
 
 from latent_common import ACT, ESZ, Case, check, layer_of, pack_cache, row_scales, row_values, shape_of
+from latent_common import _weights as weights_of
 
 pytestmark = pytest.mark.gpu
 
@@ -1041,3 +1043,66 @@ def test_the_device_flag_survives_a_larger_workspace():
     assert layer.ws is not small and mla.mla_read_device_flag(layer.ws) == mla.MLA_FLAG_BAD_SLOT
     mla.mla_clear_device_flag(layer.ws)
     assert mla.mla_read_device_flag(layer.ws) == 0
+
+
+# ---------------------------------------------------------------------------
+# what a workspace holds
+# ---------------------------------------------------------------------------
+
+def misaligned(t):
+    """The same values at an address that is a multiple of an element alone."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view(t.shape)
+    buf.copy_(t)
+    assert buf.data_ptr() % 16 and buf.is_contiguous()
+    return buf
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads,lens,prefix,aligned", [
+    (16, [1, 200, 64], 0, True), (16, [1, 200, 64], 0, False), (16, [0, 3, 70], 150, True), (16, [0, 3, 70], 150, False),
+    (128, [300, 64], 0, True), (128, [300, 64], 0, False), (128, [10, 0], 190, True), (128, [10, 0], 190, False),
+    (40, [2111], 0, False), (1, [5], 0, False), (16, [i % 3 + 1 for i in range(900)], 0, False),
+    (128, [i % 2 + 1 for i in range(300)], 5, False), (130, [70, 3], 40, True), (130, [70, 3], 40, False)])
+def test_calls_stay_within_the_workspace_they_asked_for(heads, lens, prefix, aligned, fp8):
+    case = Case(shape_of(heads, 64), lens, prefix, fp8, seed=heads)
+    layer, x = case.layer(), case.device_inputs()
+    if not aligned:
+        x["q_abs"], x["q_pe"] = misaligned(x["q_abs"]), misaligned(x["q_pe"])
+    n, ctx = len(lens), max(1, *lens)
+    need = mla.mla_prefix_workspace_bytes(layer.handle, n, prefix, ctx)
+    want = case.oracle()
+    for lse in (True, False):
+        buf = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        ws = buf[:need]
+        mla.mla_workspace_init(ws)
+        o = torch.empty(x["q_abs"].shape, dtype=torch.bfloat16, device="cuda")
+        s = torch.empty(x["q_abs"].shape[:2], device="cuda") if lse else None
+        mla.mla_latent_attn(layer.handle, ws=ws, o_lat=o, lse=s, **x)
+        check(case, o, s, want)
+        assert bool((buf[need:] == 0x5A).all()) and mla.mla_read_device_flag(ws) == 0
+    if prefix == 0:
+        need = mla.mla_workspace_bytes(layer.handle, n, ctx)
+        buf = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        mla.mla_workspace_init(buf[:need])
+        out = torch.empty(n, case.shape.hidden, dtype=torch.bfloat16, device="cuda")
+        head = torch.empty(n, heads, case.shape.v_dim, dtype=torch.bfloat16, device="cuda")
+        args = [x[k] for k in ("q_abs", "q_pe", "kv_cache", "block_table", "context_lens", "max_context_len")]
+        mla.mla_decode_attn(layer.handle, *args, out, buf[:need], head_out=head)
+        assert bool((buf[need:] == 0x5A).all()) and mla.mla_read_device_flag(buf[:need]) == 0
+        _, w_uv = ref.split_wkv_b(ref.weights_fp64(weights_of(case.shape))["wkv_b"], heads, case.shape.qk_nope, case.shape.v_dim)
+        exact = np.einsum("thr,hrd->thd", want[0], w_uv)
+        assert np.abs(head.double().cpu().numpy() - exact).max() <= 2e-2 * np.abs(exact).max()
+
+
+def test_workspaces_are_no_larger_than_their_kernels_need():
+    size = lambda layer, *a: mla.mla_prefix_workspace_bytes(layer.handle, *a)  # noqa: E731
+    plain = lambda layer, *a: mla.mla_workspace_bytes(layer.handle, *a)  # noqa: E731
+    eight, full = layer_of(shape_of(128, 64), True), layer_of(shape_of(128, 64), False)
+    # split partials of 128 rows of 2 KB and their sums: 74 SM pairs and 64 sequences; beside them a step's own buffers
+    assert plain(eight, 64, 16384) < 138 * 128 * 2100 + (60 << 20)
+    assert size(eight, 64, 0, 16384) == plain(eight, 64, 16384)
+    # a prompt, which attends to no cache, asks for no more than on the other cache
+    assert plain(eight, 8192, 1) <= plain(full, 8192, 1)
+    # a prefix adds its own partials alone
+    assert size(full, 64, 8192, 16384) <= plain(full, 64, 16384) + 202 * 128 * 2100
+    assert size(eight, 64, 8192, 16384) <= plain(eight, 64, 16384) + 64 * 128 * 2100 + (1 << 20)
