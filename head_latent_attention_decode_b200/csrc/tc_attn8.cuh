@@ -4,18 +4,21 @@
 // value is ever widened in shared memory.
 //
 // The other operand of each product would lose accuracy in E4M3, so it is split
-// in two E4M3 parts, x = hi + lo with hi = e4m3(x) and lo = e4m3(x - hi): two 4-bit
-// significands carry the 8 bits of a bf16 value, and both parts ride in one MMA
-// as extra columns (N = 32 for 16 heads). An MMA of M 128 takes as long as its
+// in two E4M3 parts, x = hi + lo / m with hi = e4m3(x) and lo = e4m3(m (x - hi)): two
+// 4-bit significands carry the 8 bits of a bf16 value, and both parts ride in one MMA
+// as extra columns (N = 32 for 16 heads), whose sums only meet in registers. So lo has
+// a scale m of its own, the largest power of two that keeps it within E4M3, and with it
+// hi's smallest steps divided by m. An MMA of M 128 takes as long as its
 // operands' way out of shared memory, 40 cycles for N 32 and 39 for N 16 (48 for
 // 64, 63 for 128; K- or MN-major and 8- or 16-bit alike), so the second part is
 // nearly free.
-//   q_abs_h = 2^k_h (hi + lo): k_h brings the row's largest to at most 448; columns
-//     within 2^-10 of it are exact, smaller ones off by at most 2^-18 of it
+//   q_abs_h = 2^k_h (hi + lo / 16): k_h brings the row's largest to at most 448; columns
+//     within 2^-14 of it are exact, smaller ones off by at most 2^-22 of it
 //   p: relative to a per-head reference R that follows the tiles' maxima both up
 //     and down, so that thousands of light keys behind a heavy one keep their
-//     weight: a weight is off by 2^-8 of itself or 2^-12 of the largest of the
-//     last few tiles
+//     weight: a weight hi + lo / 32 is off by 2^-8 of itself or 2^-17 of the largest
+//     of the last few tiles (with m = 1 it was 2^-12, and hundreds of keys that light
+//     went missing from o while l counted them: 1.5 % of o where the values share a mean)
 //
 // The row scale s_j = 2^k_j folds into both products: with u_hj = q_h . code_j,
 //   y_hj = scale log2(e) (s_j u_hj + q_pe_h . k_pe_j) + k_j
@@ -82,6 +85,8 @@ struct TcAttn8Args {
   int2* seg;                  // [n_ent]: {first slice, slices} of each entry
   int* flag;
 };
+
+constexpr float A8_QLO = 16.f, A8_WLO = 32.f;   // the scales m: |x - hi| <= 16 for |x| <= 448, <= 8 for x <= 256
 
 constexpr int A8_MAX_ENT = 768;   // sequences per launch (their tile prefix in shared memory)
 
@@ -472,7 +477,8 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
           const uint16_t a0 = e4m3x2_sat(f0, f1), a1 = e4m3x2_sat(f2, f3);
           const float2 g0v = e4m3x2_f32(a0), g1v = e4m3x2_f32(a1);
           hi[j] = (uint32_t)a0 | ((uint32_t)a1 << 16);
-          lo[j] = (uint32_t)e4m3x2_sat(f0 - g0v.x, f1 - g0v.y) | ((uint32_t)e4m3x2_sat(f2 - g1v.x, f3 - g1v.y) << 16);
+          lo[j] = (uint32_t)e4m3x2_sat((f0 - g0v.x) * A8_QLO, (f1 - g0v.y) * A8_QLO) |
+                  ((uint32_t)e4m3x2_sat((f2 - g1v.x) * A8_QLO, (f3 - g1v.y) * A8_QLO) << 16);
         }
         const int chunk = ((sub & 1) * 4 + ch) ^ (hd & 7);
         *reinterpret_cast<uint4*>(qb + r_hi * 128 + 16 * chunk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int h = 4 * k + j, at = 16 * (h >> 3) + (h & 7);
-            const float uu = __uint_as_float(u[at]) + __uint_as_float(u[at + 8]);
+            const float uu = fmaf(__uint_as_float(u[at + 8]), 1.f / A8_QLO, __uint_as_float(u[at]));
             y[h] = fmaf(uu, sj * sv[j], fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj));
           }
         }
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
           l[h + 1] = fmaf(e1, un, l[h + 1]);
           const uint16_t c_hi = e4m3x2_sat(e0, e1);
           const float2 back = e4m3x2_f32(c_hi);
-          const uint16_t c_lo = e4m3x2_sat(e0 - back.x, e1 - back.y);
+          const uint16_t c_lo = e4m3x2_sat((e0 - back.x) * A8_WLO, (e1 - back.y) * A8_WLO);
           uint8_t* p0 = pb + (16 * (h >> 3) + (h & 7)) * 128 + (((row >> 4) ^ (h & 7)) << 4);
           uint8_t* p1 = pb + (16 * (h >> 3) + (h & 7) + 1) * 128 + (((row >> 4) ^ ((h & 7) + 1)) << 4);
           p0[0] = (uint8_t)c_hi;
@@ -688,7 +694,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
         tmem_ld_wait<32>(o);
 #pragma unroll
         for (int h = 0; h < 16; ++h)
-          out[h] = __uint_as_float(o[16 * (h >> 3) + (h & 7)]) + __uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]);
+          out[h] = fmaf(__uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]), 1.f / A8_WLO, __uint_as_float(o[16 * (h >> 3) + (h & 7)]));
         if (!first) {
           tmem_ld16(tm_o + 128 * (set ^ 1) + 32 * g, o);
           tmem_ld16(tm_o + 128 * (set ^ 1) + 32 * g + 16, o + 16);
@@ -696,7 +702,7 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
             const float fa = ref_w[h], fb = al_w[h];
-            const float ob = __uint_as_float(o[16 * (h >> 3) + (h & 7)]) + __uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]);
+            const float ob = fmaf(__uint_as_float(o[16 * (h >> 3) + 8 + (h & 7)]), 1.f / A8_WLO, __uint_as_float(o[16 * (h >> 3) + (h & 7)]));
             out[h] = (fa != 0.f ? fa * out[h] : 0.f) + (fb != 0.f ? fb * ob : 0.f);
           }
         }

@@ -1106,3 +1106,45 @@ def test_workspaces_are_no_larger_than_their_kernels_need():
     # a prefix adds its own partials alone
     assert size(full, 64, 8192, 16384) <= plain(full, 64, 16384) + 202 * 128 * 2100
     assert size(eight, 64, 8192, 16384) <= plain(eight, 64, 16384) + 64 * 128 * 2100 + (1 << 20)
+
+
+# ---------------------------------------------------------------------------
+# light keys behind heavy ones
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bs", [64, 16])
+def test_light_keys_behind_heavy_ones_keep_their_weight(bs):
+    # As many sequences as SMs, so that each CTA has one of 28 tiles of 128 keys. Two tiles of every eight begin
+    # with a heavy key; the others have a weight of 2^-15.1 of it, 1.2 % of the sum together. All values share a
+    # mean, so that o is that mean whatever the weights, if o and the sum count the same keys: half a step of the
+    # heavy key's weight, 2^-8, of the light ones', 2^-4 of 1.2 %, and of o's type, 2^-8 at the worst: 0.0085 in all.
+    # Without the light keys o is 0.012 short.
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    shape = shape_of(16, bs)
+    layer = layer_of(shape, True)
+    n, L = sms, 28 * 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    mean = torch.rand(512, generator=g, device="cuda") * 0.4 + 0.55
+    mean[0] = 1.0
+    mean *= torch.where(torch.rand(512, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    rows = torch.zeros(L, 576, device="cuda")
+    rows[:, :512] = mean * (1 + 0.02 * torch.randn(L, 512, generator=g, device="cuda").clamp(-3, 3))
+    tile = torch.arange(L, device="cuda") // 128
+    heavy = (torch.arange(L, device="cuda") % 128 == 0) & (tile // 2 % 4 == 0)
+    rows[:, 512] = torch.where(heavy, 18.125, -0.048)
+    cache = layer.new_cache(L // bs)
+    slots = torch.arange(L, dtype=torch.int32, device="cuda")
+    layer.cache_write(rows.bfloat16(), cache, slots)
+    q_abs, q_pe = torch.zeros(n, 16, 512, device="cuda").bfloat16(), torch.zeros(n, 16, 64, device="cuda").bfloat16()
+    q_pe[:, :, 0] = 8.0
+    table = torch.arange(L // bs, dtype=torch.int32, device="cuda").expand(n, -1).contiguous()
+    o, lse = layer.latent_attn(q_abs, q_pe, cache, table, torch.full((n,), L, dtype=torch.int32, device="cuda"), L, want_lse=True)
+    keys = layer.cache_read(cache, slots).double()
+    s = 8.0 * keys[:, 512] / np.sqrt(192.0)
+    p = torch.softmax(s, 0)
+    light = float(p[~heavy].sum())
+    assert 0.0115 < light < 0.013 and float(p[~heavy].max() / p[heavy].max()) < 2.0 ** -15
+    want = p @ keys[:, :512]
+    short = (1 - o.double() / want).mean(-1)   # the rounding of single values averages out over the columns
+    assert float(short.abs().max()) <= 0.0085
+    assert float((lse.double() - torch.logsumexp(s, 0)).abs().max()) <= 1e-5
