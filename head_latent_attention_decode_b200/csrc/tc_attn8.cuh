@@ -88,6 +88,13 @@ struct TcAttn8Args {
 
 constexpr float A8_QLO = 16.f, A8_WLO = 32.f;   // the scales m: |x - hi| <= 16 for |x| <= 448, <= 8 for x <= 256
 
+// Two E4M3 values times m, exact in f16 for a power of two of up to 2^7.
+__device__ __forceinline__ float2 e4m3x2_times(uint16_t c, float m) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(m)));
+}
+
 constexpr int A8_MAX_ENT = 768;   // sequences per launch (their tile prefix in shared memory)
 
 constexpr int A8_THREADS = 8 * 32 + 96;   // two sets of four softmax warps; TMA, score and value MMA warps
@@ -528,12 +535,17 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float4 s4 = *reinterpret_cast<const float4*>(sq + 4 * k);
-          const float sv[4] = {s4.x, s4.y, s4.z, s4.w};
+          const float2 sv[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
+          const float2 sj2 = make_float2(sj, sj), zero2 = make_float2(-0.f, -0.f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 4; j += 2) {
             const int h = 4 * k + j, at = 16 * (h >> 3) + (h & 7);
-            const float uu = fmaf(__uint_as_float(u[at + 8]), 1.f / A8_QLO, __uint_as_float(u[at]));
-            y[h] = fmaf(uu, sj * sv[j], fmaf(__uint_as_float(rp[h]), a.scale_log2, (float)kj));
+            auto pair = [](const uint32_t* x) { return make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])); };
+            const float2 uu = fma2(pair(u + at + 8), make_float2(1.f / A8_QLO, 1.f / A8_QLO), pair(u + at));
+            const float2 rot = fma2(pair(rp + h), make_float2(a.scale_log2, a.scale_log2), make_float2((float)kj, (float)kj));
+            const float2 yy = fma2(uu, fma2(sj2, sv[j >> 1], zero2), rot);
+            y[h] = yy.x;
+            y[h + 1] = yy.y;
           }
         }
         tc_fence_before();
@@ -620,12 +632,14 @@ __global__ void __launch_bounds__(A8_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           const int h = 4 * k + j;
-          const float e0 = ex2_approx(y[h] + rv[j]), e1 = ex2_approx(y[h + 1] + rv[j + 1]);
-          l[h] = fmaf(e0, un, l[h]);
-          l[h + 1] = fmaf(e1, un, l[h + 1]);
+          const float2 yr = add2(make_float2(y[h], y[h + 1]), make_float2(rv[j], rv[j + 1]));
+          const float e0 = ex2_approx(yr.x), e1 = ex2_approx(yr.y);
+          const float2 ll = fma2(make_float2(e0, e1), make_float2(un, un), make_float2(l[h], l[h + 1]));
+          l[h] = ll.x;
+          l[h + 1] = ll.y;
           const uint16_t c_hi = e4m3x2_sat(e0, e1);
-          const float2 back = e4m3x2_f32(c_hi);
-          const uint16_t c_lo = e4m3x2_sat((e0 - back.x) * A8_WLO, (e1 - back.y) * A8_WLO);
+          const float2 lo = fma2(make_float2(e0, e1), make_float2(A8_WLO, A8_WLO), e4m3x2_times(c_hi, -A8_WLO));
+          const uint16_t c_lo = e4m3x2_sat(lo.x, lo.y);
           uint8_t* p0 = pb + (16 * (h >> 3) + (h & 7)) * 128 + (((row >> 4) ^ (h & 7)) << 4);
           uint8_t* p1 = pb + (16 * (h >> 3) + (h & 7) + 1) * 128 + (((row >> 4) ^ ((h & 7) + 1)) << 4);
           p0[0] = (uint8_t)c_hi;
