@@ -138,6 +138,10 @@ static int decode_splits(int max_ctx) {
   return c < 2 ? 2 : (c > 16 ? 16 : c);
 }
 
+// The head-major attention stores its partials 32 bytes at a time: they begin at the first 32-byte boundary of
+// their region, whatever 16-byte boundary the workspace is at.
+static char* partials_at(char* region) { return (char*)(((uintptr_t)region + 31) & ~(uintptr_t)31); }
+
 // prefix_len >= 0: a call with a prefix or in latent form. Its attention, and every one on an 8-bit cache, is
 // latent_attn.cuh's: on a 16-bit cache its scratch lies over the split partials of mla_decode_attn, which an
 // 8-bit cache has none of.
@@ -155,12 +159,12 @@ static WsLayout make_ws(const mla_handle* h, long long n, int max_ctx, int prefi
   W.Q = put((size_t)n * L.Hq * 4);
   const size_t lat = h->cache8 || prefix_len >= 0 ? latent_ws_bytes(h, n, prefix_len > 0 ? prefix_len : 0, max_ctx) : 0;
   if (!h->cache8) {
-    W.part_o = put((size_t)n * W.splits * H * rkv * 4);
+    W.part_o = put((size_t)n * W.splits * H * rkv * 4 + 16);
     W.part_ml = put((size_t)n * W.splits * H * 2 * 4 * 2);   // one (m, l) copy per CTA of a pair
     W.nseg = put((size_t)n * 4);                                // split partials per sequence
     W.lat = W.part_o;
-    if (W.lat + lat > off) off = align_up(W.lat + lat, 256);
-    W.lat_bytes = off - W.lat;
+    if (W.lat + lat + 16 > off) off = align_up(W.lat + lat + 16, 256);
+    W.lat_bytes = off - W.lat - 16;
   }
   W.o_lat = put((size_t)n * H * rkv * a);
   W.head = put((size_t)n * H * dv * a);
@@ -169,7 +173,7 @@ static WsLayout make_ws(const mla_handle* h, long long n, int max_ctx, int prefi
   W.tc = put(tc_decode_ws_bytes(h, n, max_ctx));
   W.qkv_total = off;
   if (h->cache8) {   // behind what the front-fold needs
-    W.lat = put(lat);
+    W.lat = put(lat + 16);
     W.lat_bytes = lat;
   }
   const size_t dec_end = off;
@@ -537,7 +541,7 @@ static int decode_attn_impl(mla_handle* h, const void* q_abs, const void* q_pe, 
   if (tc_decode_attn_supported(h, n, max_context_len)) {
     const int r = tc_decode_attn(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq,
                                  context_lens, max_context_len, n, out, head, wsb, W.tc, s,
-                                 (float*)(wsb + W.part_o), (float*)(wsb + W.part_ml), W.splits,
+                                 (float*)partials_at(wsb + W.part_o), (float*)(wsb + W.part_ml), W.splits,
                                  (bf16*)(wsb + W.o_lat), (int*)(wsb + W.nseg), head_out == nullptr, ext);
     return r != MLA_OK ? r : cuda_status();
   }
@@ -548,7 +552,7 @@ static int decode_attn_impl(mla_handle* h, const void* q_abs, const void* q_pe, 
   } else if (tc_attention_supported(h)) {
     // tensor-core attention (bf16 activations) ahead of CUDA-core W_UV / o_proj
     const int r = tc_attention_core(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq,
-                                    context_lens, max_context_len, n, (float*)(wsb + W.part_o),
+                                    context_lens, max_context_len, n, (float*)partials_at(wsb + W.part_o),
                                     (float*)(wsb + W.part_ml), W.splits, (bf16*)o_lat, flag,
                                     (int*)(wsb + W.nseg), s);
     if (r != MLA_OK) return r;
@@ -559,7 +563,7 @@ static int decode_attn_impl(mla_handle* h, const void* q_abs, const void* q_pe, 
     p.H = H; p.r_kv = rkv; p.d_r = dr; p.layout = c->row_layout; p.scale = h->scale;
     p.n_splits = W.splits;
     p.chunk = (int)cdiv(cdiv(max_context_len, W.splits), ATT_TR) * ATT_TR;
-    p.part_o = (float*)(wsb + W.part_o); p.part_ml = (float*)(wsb + W.part_ml); p.flag = flag;
+    p.part_o = (float*)partials_at(wsb + W.part_o); p.part_ml = (float*)(wsb + W.part_ml); p.flag = flag;
     const int R = rkv + dr;
     const size_t smem = (size_t)(ATT_TR * (R + 1) + ATT_HPB * R) * 4;
     dim3 grid(W.splits, n, (unsigned)cdiv(H, ATT_HPB));
@@ -597,7 +601,7 @@ int mla_decode_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
   if (ws_bytes < W.dec_total) return MLA_ERR_WORKSPACE;
   const LatentCall call{q_abs, q_pe, kv_cache, n_blocks, nullptr, 0, block_table, max_blocks_per_seq,
                         context_lens, max_context_len, n};
-  const LatentExt ext{&call, (char*)ws + W.lat, W.lat_bytes};
+  const LatentExt ext{&call, partials_at((char*)ws + W.lat), W.lat_bytes};
   return decode_attn_impl(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq, context_lens,
                           max_context_len, n, out, head_out, ws, W, h->cache8 ? &ext : nullptr, stream);
 }
@@ -694,7 +698,7 @@ int mla_latent_attn(mla_handle* h, const void* q_abs, const void* q_pe, const vo
   WsLayout W;
   const int st = latent_check(h, a, o_lat, ws, ws_bytes, &W);
   if (st != MLA_OK) return st;
-  const int r = latent_core(h, a, o_lat, acode(h), lse, (char*)ws + W.lat, W.lat_bytes, (int*)ws, (cudaStream_t)stream);
+  const int r = latent_core(h, a, o_lat, acode(h), lse, partials_at((char*)ws + W.lat), W.lat_bytes, (int*)ws, (cudaStream_t)stream);
   return r != MLA_OK ? r : cuda_status();
 }
 
@@ -709,7 +713,7 @@ int mla_decode_attn_prefix(mla_handle* h, const void* q_abs, const void* q_pe, c
   WsLayout W;
   const int st = latent_check(h, a, out, ws, ws_bytes, &W);
   if (st != MLA_OK) return st;
-  const LatentExt ext{&a, (char*)ws + W.lat, W.lat_bytes};
+  const LatentExt ext{&a, partials_at((char*)ws + W.lat), W.lat_bytes};
   return decode_attn_impl(h, q_abs, q_pe, kv_cache, n_blocks, block_table, max_blocks_per_seq, context_lens,
                           max_context_len, n, out, head_out, ws, W, &ext, stream);
 }

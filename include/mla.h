@@ -171,7 +171,7 @@ void mla_destroy(mla_handle* h);
  * `max_context_len` rows. For FP8 weights this includes one bf16 buffer of
  * the largest weight, into which mla_prefill dequantises each weight in turn
  * (the decode calls never use it and accept a workspace without it). A
- * workspace is 16-byte aligned (as every allocation is); attention on an 8-bit
+ * workspace is 16-byte aligned (any allocation is); attention on an 8-bit
  * cache, in latent form or with a prefix refuses another. */
 size_t mla_workspace_bytes(const mla_handle* h, int max_tokens, int max_context_len);
 
