@@ -1148,3 +1148,75 @@ def test_light_keys_behind_heavy_ones_keep_their_weight(bs):
     short = (1 - o.double() / want).mean(-1)   # the rounding of single values averages out over the columns
     assert float(short.abs().max()) <= 0.0085
     assert float((lse.double() - torch.logsumexp(s, 0)).abs().max()) <= 1e-5
+
+
+# ---------------------------------------------------------------------------
+# the serving calls against fp64, and errors on average
+# ---------------------------------------------------------------------------
+
+def off_by(got, want):
+    """(the error's size, its part along the result), both relative to the result's size."""
+    d = got.double().cpu().numpy() - want
+    return np.linalg.norm(d) / np.linalg.norm(want), abs((d * want).sum()) / (want * want).sum()
+
+
+def steps_shape(weights, heads, bs=64):
+    if weights == "fp8":
+        return dataclasses.replace(wl.V3_FP8, hidden=512, n_heads=heads, q_lora_rank=128, block_size=bs)
+    return shape_of(heads, bs)
+
+
+@pytest.mark.parametrize("weights", ["fp8", "bf16"])
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads,n,prefix", [(16, 3, 0), (16, 3, 150), (16, 1, 700), (40, 5, 70), (128, 3, 0), (128, 3, 150),
+                                            (16, 140, 70), (16, 300, 5)])
+def test_decode_calls_against_fp64(weights, heads, n, prefix, fp8):
+    # o_lat within its bound (Case.oracle; rounded to f16 or bf16), then sums of 512 and heads * 128 products in
+    # fp32 and a rounding to 16 bits after each: 2^-8 of the value at most. On average (the roundings of weights,
+    # o_lat, head_out and out are independent, each at most 2^-8 / sqrt(3) of the value in the mean square) half of 2^-7;
+    # along the result they cancel.
+    shape = steps_shape(weights, heads)
+    case = Case(shape, [(37 * i) % 260 + 1 for i in range(n)], prefix, fp8, seed=n)
+    layer, x = case.layer(), case.device_inputs()
+    W = ref.weights_fp64(weights_of(shape))
+    _, w_uv = ref.split_wkv_b(W["wkv_b"], heads, shape.qk_nope, shape.v_dim)
+    o, _, bo, _ = case.oracle()
+    want = np.einsum("thr,hrd->thd", o, w_uv)
+    bh = np.einsum("thr,hrd->thd", bo + 2.0 ** -14 * np.abs(o), np.abs(w_uv)) + 2.0 ** -8 * np.abs(want)
+    final = want.reshape(n, -1) @ W["wo"]
+    bf = bh.reshape(n, -1) @ np.abs(W["wo"]) + 2.0 ** -12 * np.abs(want).reshape(n, -1) @ np.abs(W["wo"]) + 2.0 ** -8 * np.abs(final)
+    act = dict(device="cuda", dtype=torch.bfloat16)
+    table = [x[k] for k in ("block_table", "context_lens", "max_context_len")]
+    for head in (torch.empty(n, heads, shape.v_dim, **act), None):   # with FP8 weights, without head_out: kept in f16
+        if prefix:
+            out = layer.decode_attn_prefix(x["q_abs"], x["q_pe"], x["kv_cache"], x["prefix_table"], prefix, *table, head_out=head)
+        else:
+            out = layer.decode_attn(x["q_abs"], x["q_pe"], x["kv_cache"], *table, head_out=head)
+        for got, w, b in ((head, want, bh), (out, final, bf)):
+            if got is not None:
+                assert (np.abs(got.double().cpu().numpy() - w) <= b).all()
+                size, along = off_by(got, w)
+                assert size <= 2.0 ** -7 and along <= 1e-3, (size, along)
+    assert mla.mla_read_device_flag(layer.ws) == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False], ids=["cache8", "cache16"])
+@pytest.mark.parametrize("heads,bs,lens,prefix", [
+    (16, 64, [700, 300, 512, 130], 0), (16, 16, [700, 300, 130], 0), (40, 64, [700, 300], 0), (128, 64, [700, 300, 64], 0),
+    (16, 64, [100, 70, 200], 900), (4, 64, [90, 200], 700), (128, 64, [70, 200], 500), (130, 64, [300, 90], 100),
+    (16, 24, [200, 90], 100)])
+def test_errors_on_average(heads, bs, lens, prefix, fp8):
+    # o is rounded once to bf16 (at most 2^-8 / sqrt(3) = 2.3e-3 in the mean square, 1.7e-3 for values spread evenly),
+    # after weights rounded to bf16, f16 or two E4M3 parts and scores with a half rounded to f16 (2^-12 of a few
+    # units), each of whose errors averages out over a hundred keys and more: 3e-3 in all, and along the result,
+    # where nothing is left but a steady bias, 3e-4.
+    case = Case(shape_of(heads, bs), lens, prefix, fp8, seed=heads + bs)
+    size = 2.0 ** np.floor(np.log2(np.abs(case.rows[:, :512].float().numpy()).mean(1, keepdims=True) + 1e-30))
+    size[~np.isfinite(size)] = 1.0
+    case.rows[:, :512] /= torch.from_numpy(size).bfloat16()   # rows of one size, as a norm leaves them
+    case.keys = row_values(case.shape, case.rows) if fp8 else case.rows.double().numpy()
+    want = case.oracle()[0]
+    for lse in (True, False):
+        o, _ = case.layer().latent_attn(want_lse=lse, **case.device_inputs())
+        size, along = off_by(o, want)
+        assert size <= 3e-3 and along <= 3e-4, (size, along)
