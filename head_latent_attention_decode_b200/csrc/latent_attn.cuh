@@ -211,6 +211,7 @@ struct LatentPlan {
 };
 
 constexpr int LAT_FEW_ROWS = 32;   // query rows up to which a prefix goes to the few-head 8-bit kernel
+constexpr int LAT_MAX_HEADS = 128 * (ATT_MAX_SEQ - 1);
 
 // `lse`: the log-sum-exp is wanted. `budget` > 0: the query is not 16-byte aligned, as the tensor-core kernels
 // need it; CUDA cores then take as many tokens and splits at a time as this scratch holds. `force` < 0: by the
@@ -240,7 +241,8 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
     // head-major one 2.9 us of two SMs whatever the rows up to 128. Own rows, 32 sequences of 8192:
     // 64 heads 111 against 126 us, 80 heads 139 against 128. A prefix of 16384: 48 rows 36 against 29 us,
     // since the head-major launch takes the own rows along.
-    w.heads_pre = pre && b64 && (force < 0 ? n * H > LAT_FEW_ROWS : (force & 1) != 0);
+    // (One token's query rows have to fit the head-major kernel's list of blocks of 128.)
+    w.heads_pre = pre && b64 && H <= LAT_MAX_HEADS && (force < 0 ? n * H > LAT_FEW_ROWS : (force & 1) != 0);
     w.few_pre = pre && !w.heads_pre;
     w.heads_own = b64 && H <= 128 && (H > 64 || (w.heads_pre && ride));
     w.few_own = !w.heads_own;
@@ -314,9 +316,10 @@ static inline size_t latent_ws_bytes(const mla_handle* h, long long n, int prefi
   size_t most = 0;
   for (int p = 0; p < (prefix_len > 0 ? 2 : 1); ++p)
     for (int k = 0; k < 8; ++k) {
+      const int H = h->cfg.n_heads;
       long long m = n;
-      if (p && !(k & 1) && h->cache8 && h->cfg.block_size % 64 == 0)   // a prefix on the few-head kernel
-        m = n * h->cfg.n_heads > LAT_FEW_ROWS ? LAT_FEW_ROWS / h->cfg.n_heads : n;
+      if (p && !(k & 1) && h->cache8 && h->cfg.block_size % 64 == 0 && H <= LAT_MAX_HEADS)
+        m = n * H > LAT_FEW_ROWS ? LAT_FEW_ROWS / H : n;   // as many tokens as take a prefix to the few-head kernel
       const size_t t = m > 0 ? latent_plan(h, m, p ? prefix_len : 0, max_ctx, (k & 4) != 0, 0, k & 3).total : 0;
       if (t > most) most = t;
     }

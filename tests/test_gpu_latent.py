@@ -1220,3 +1220,27 @@ def test_errors_on_average(heads, bs, lens, prefix, fp8):
         o, _ = case.layer().latent_attn(want_lse=lse, **case.device_inputs())
         size, along = off_by(o, want)
         assert size <= 3e-3 and along <= 3e-4, (size, along)
+
+
+def test_a_prefix_at_more_heads_than_the_head_major_list_holds():
+    # 256 blocks of 128 query rows of one token: one more than fit beside the sequence's own entry
+    heads, prefix, own = 128 * 255 + 64, 70, 3
+    shape = dataclasses.replace(wl.V2LITE, hidden=64, n_heads=heads, qk_nope=8, v_dim=32, block_size=64)
+    weights = {k: torch.zeros(v, dtype=torch.bfloat16, device="cuda") for k, v in wl.weight_shapes(shape).items()}
+    weights["kv_norm_w"] = torch.ones(512, device="cuda")
+    from head_latent_attention_decode_b200.layer import MlaLayer
+    layer = MlaLayer(shape, weights, cache_dtype="fp8")
+    del weights
+    cache = layer.new_cache(3)
+    slots = torch.arange(192, dtype=torch.int32, device="cuda")
+    layer.cache_write(torch.randn(192, 576, device="cuda").bfloat16(), cache, slots)
+    q = torch.randn(1, heads, 576, device="cuda").bfloat16()
+    args = (cache, torch.tensor([[2]], dtype=torch.int32, device="cuda"), torch.tensor([own], dtype=torch.int32, device="cuda"), own)
+    o, lse = layer.latent_attn(q[..., :512].contiguous(), q[..., 512:].contiguous(), *args, want_lse=True,
+                               prefix_table=torch.tensor([0, 1], dtype=torch.int32, device="cuda"), prefix_len=prefix)
+    keys = layer.cache_read(cache, slots).double()[torch.cat([torch.arange(prefix), torch.arange(128, 128 + own)]).cuda()]
+    s = q[0].double() @ keys.T / np.sqrt(72.0)
+    want = torch.softmax(s, 1) @ keys[:, :512]
+    assert float((o[0].double() - want).norm() / want.norm()) <= 2.0 ** -7
+    assert float((lse[0].double() - torch.logsumexp(s, 1)).abs().max()) <= 1e-4
+    assert mla.mla_read_device_flag(layer.ws) == 0
