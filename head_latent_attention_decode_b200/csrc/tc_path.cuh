@@ -756,11 +756,11 @@ static inline int tc_attention_launch(const mla_handle* h, const void* q_abs, co
     if ((st = make_map2(&mqp, q_pe, dr, (long long)n * H, dr, NH)) != MLA_OK) return st;
     if ((st = make_map2(&mc, kv_cache, R, (long long)n_blocks * c.block_size, R, 64)) != MLA_OK) return st;
     if ((st = make_map_cache_groups(&ml, kv_cache, R, (long long)n_blocks * c.block_size, 2)) != MLA_OK) return st;
-    TcAttnArgs ta{};
+    TcAttnPairArgs ta{};
     ta.allow_empty = allow_empty;
-    ta.n = n; ta.H = H; ta.splits = sp; ta.chunk = chunk;
+    ta.H = H; ta.splits = sp; ta.chunk = chunk;
     ta.bs = c.block_size; ta.n_blocks = n_blocks; ta.mbps = mbps; ta.max_ctx = max_ctx;
-    ta.block_table = block_table; ta.ctx = ctx; ta.q_abs = (const bf16*)q_abs;
+    ta.block_table = block_table; ta.ctx = ctx;
     ta.lat_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? 0 : dr;
     ta.rope_col0 = c.row_layout == MLA_ROW_LATENT_FIRST ? rkv : 0;
     ta.scale_log2 = h->scale * 1.4426950408889634f;
