@@ -318,12 +318,14 @@ def _bad_tensor(where: str, name: str, t) -> ValueError:
 
 def _check_tensors(where: str, need: tuple, ints: tuple) -> int:
     """Contiguous tensors on one device, those of `ints` int32; (name, tensor or None) pairs. The device's index."""
-    dev = need[0][1].get_device()
+    dev = need[0][1].get_device()   # negative on the host
+    if dev < 0:
+        raise _bad_tensor(where, *need[0])
     for name, t in need:
-        if t is not None and not (t.is_cuda and t.is_contiguous() and t.get_device() == dev):
+        if t is not None and not (t.get_device() == dev and t.is_contiguous()):
             raise _bad_tensor(where, name, t)
     for name, t in ints:
-        if t is not None and not (t.is_cuda and t.dtype is torch.int32 and t.is_contiguous() and t.get_device() == dev):
+        if t is not None and not (t.get_device() == dev and t.dtype is torch.int32 and t.is_contiguous()):
             raise _bad_tensor(where, name, t)
     return dev
 

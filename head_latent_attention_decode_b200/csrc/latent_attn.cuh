@@ -314,9 +314,9 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
 // kernels. (An unaligned query makes do with what the aligned one has.)
 static inline size_t latent_ws_bytes(const mla_handle* h, long long n, int prefix_len, int max_ctx) {
   size_t most = 0;
+  const int H = h->cfg.n_heads, kinds = !h->cache8 && H > 32 ? 8 : 4;   // the log-sum-exp changes the plan there alone
   for (int p = 0; p < (prefix_len > 0 ? 2 : 1); ++p)
-    for (int k = 0; k < 8; ++k) {
-      const int H = h->cfg.n_heads;
+    for (int k = 0; k < kinds; ++k) {
       long long m = n;
       if (p && !(k & 1) && h->cache8 && h->cfg.block_size % 64 == 0 && H <= LAT_MAX_HEADS)
         m = n * H > LAT_FEW_ROWS ? LAT_FEW_ROWS / H : n;   // as many tokens as take a prefix to the few-head kernel

@@ -91,7 +91,7 @@ class MlaLayer:
 
     def _workspace(self, need: int) -> torch.Tensor:
         """A workspace of `need` bytes or more for a call on the current stream."""
-        if torch.cuda.is_current_stream_capturing():
+        if torch._C._cuda_isCurrentStreamCapturing():
             # kept alive with the layer (a later call may need a larger one); one made here is the graph's own
             for ws in (self.ws, *self._graph_ws):
                 if ws is not None and ws.numel() >= need:
@@ -182,9 +182,9 @@ class MlaLayer:
             raise ValueError("prefix_table does not cover prefix_len rows")
 
     def _check_query(self, q_abs, q_pe):
-        s, n = self.shape, q_abs.shape[0]
-        if (q_abs.shape != (n, s.n_heads, s.kv_lora_rank) or q_pe.shape != (n, s.n_heads, s.qk_rope)
-                or q_abs.dtype is not self.act or q_pe.dtype is not self.act):
+        s, a, p, act = self.shape, q_abs.shape, q_pe.shape, self.act
+        n, heads = a[0], s.n_heads
+        if a != (n, heads, s.kv_lora_rank) or p != (n, heads, s.qk_rope) or q_abs.dtype is not act or q_pe.dtype is not act:
             raise ValueError(f"q_abs must be [n, {s.n_heads}, {s.kv_lora_rank}] and q_pe [n, {s.n_heads}, {s.qk_rope}], {self.act}")
 
     def _check_out(self, n, out, head_out):
