@@ -237,8 +237,8 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
   if (!fits || budget > 0) {
     w.simt = true;
   } else if (h->cache8) {
-    // Per 128 keys the few-head kernel takes 1.7 us of one SM for every 16 heads (or 16 query rows), the
-    // head-major one 2.9 us of two SMs whatever the rows up to 128. Own rows, 32 sequences of 8192:
+    // Per 128 keys the few-head kernel takes 2.2 us of one SM for every 16 heads (or 16 query rows), the
+    // head-major one 4.1 us of two SMs whatever the rows up to 128. Own rows, 32 sequences of 8192:
     // 64 heads 111 against 126 us, 80 heads 139 against 128. A prefix of 16384: 48 rows 36 against 29 us,
     // since the head-major launch takes the own rows along.
     // (One token's query rows have to fit the head-major kernel's list of blocks of 128.)
@@ -248,7 +248,9 @@ static inline LatentPlan latent_plan(const mla_handle* h, long long n, int prefi
     w.few_own = !w.heads_own;
   } else {
     // Beyond 32 heads only the head-major form of this file has the log-sum-exp good to fp32
-    // (TcAttnArgs::corr); up to 32 the kernel of mla_decode_attn has a form for it.
+    // (TcAttnArgs::corr); up to 32 the kernel of mla_decode_attn has a form for it. Own rows, with it and
+    // without: 32 sequences of 4096 rows, 16 heads 46.4 and 45.4 us, 32 heads 70.9 with it; 64 sequences of
+    // 1024 to 16384 rows, 128 heads 228 and 230.
     w.heads_pre = pre;
     w.heads_own = H > 32 ? pre || lse : pre && ride;
     w.own16 = !w.heads_own;

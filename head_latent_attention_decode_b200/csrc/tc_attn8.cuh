@@ -1,6 +1,7 @@
-// Latent attention over the 8-bit cache on tcgen05 for up to 64 heads, with the
-// DeepSeek latent (kv_lora_rank 512, qk_rope 64) and blocks of a multiple of 16
-// rows. The E4M3 codes go to the tensor cores as they are (kind::f8f6f4); no
+// Latent attention over the 8-bit cache on tcgen05 with the DeepSeek latent
+// (kv_lora_rank 512, qk_rope 64) and blocks of a multiple of 16 rows: up to 64
+// heads, beyond 128, and any number where the blocks are no multiple of 64 rows
+// (latent_plan has the rules). The E4M3 codes go to the tensor cores as they are (kind::f8f6f4); no
 // value is ever widened in shared memory.
 //
 // The other operand of each product would lose accuracy in E4M3, so it is split
@@ -49,9 +50,11 @@
 // More than 16 heads: `groups` CTAs, each with 16 heads, walk the same slice at
 // the same time, so the rows come from HBM once and from L2 after.
 //
-// 32 sequences of 4096 rows, 16 heads: 35 us with the merge, of which 7 tiles an SM
-// at 1.64 us (6 TB/s of codes, rotary keys and scales) and 6.4 us before the first
-// scores; 64 sequences of 1024 to 16384 rows, 128 heads in 8 groups: 438 us.
+// 16 heads, caches cold, by the kernel timer over 1 to 28 tiles an SM: 15 us to
+// start and end (lengths, block table, first tile and query each a trip to memory,
+// first fetches of code; O out), and 2.3 us a tile (5.3 TB/s of codes, rotary keys
+// and scales). 32 sequences of 4096 rows are 7 tiles an SM: 31 us, and 32 a call with
+// the merge. 64 sequences of 1024 to 16384 rows, 128 heads in 8 groups: 438 us.
 #pragma once
 
 #include "cache8.cuh"

@@ -18,7 +18,7 @@
 //   peer's in f16, so their P^T agree to the f16 rounding of a partial score
 //   (LSE, where the log-sum-exp is wanted: the partials cross in fp32 and the
 //   row sums take the weights before their rounding to bf16, so that it is good
-//   to fp32)
+//   to fp32; 46.4 us a call instead of 45.4 for 32 sequences of 4096 rows)
 //   O_r^T += V_r^T . P^T                 2 x (M 128 latent x N NH, K 128 rows),
 //                                        V^T read MN-major from the same tile
 // A CTA keeps 64 KB of a tile until its P.V (half of what one CTA holding the
