@@ -207,7 +207,7 @@ int mla_clear_device_flag(void* ws, void* stream);
  * of it) and q_abs in f16, whose entries must then lie within +-65504.
  * The two halves' partial scores (q_abs . c over r_kv / 2 columns, before
  * softmax_scale) cross in f16 there, and on every 16-bit cache with r_kv 512 and
- * up to 128 heads: one beyond +-65504 counts as infinite.
+ * up to 128 heads: one beyond +-65504 may count as infinite.
  * Not to be called while calls on the same handle are in progress. */
 int mla_set_cache_dtype(mla_handle* h, int cache_dtype);
 
