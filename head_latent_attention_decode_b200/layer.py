@@ -84,9 +84,9 @@ class MlaLayer:
         if mla_destroy is not None:
             self.close()
 
-    def _new_ws(self, need: int) -> torch.Tensor:
+    def _new_ws(self, need: int, head: int | None = None) -> torch.Tensor:
         ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        mla_workspace_init(ws)
+        mla_workspace_init(ws[:head])
         return ws
 
     def _workspace(self, need: int) -> torch.Tensor:
@@ -97,7 +97,7 @@ class MlaLayer:
                 if ws is not None and ws.numel() >= need:
                     break
             else:
-                ws = self._new_ws(need)
+                ws = self._new_ws(need, 256)   # at each replay: the device flag and the counters alone
             if all(w is not ws for w in self._graph_ws):
                 self._graph_ws.append(ws)
             return ws
